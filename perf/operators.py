@@ -272,8 +272,8 @@ def _run_own(s):
     if c["n_top"]:
         got.update(top_tokens=r["top_tokens"], top_logprobs=r["top_logprobs"])
     if c["train"]:
-        got["grad"] = sv.spec_token_logprobs_backward(s["x"], s["tokens"], r["lse"], r["entropy"], s["g_lp"],
-                                                      grad_entropy=s["g_ent"], temperature=c["T"])
+        got["grad"] = sv.spec_token_logprobs_backward(s["x"], s["tokens"], r["saved"], s["g_lp"], grad_entropy=s["g_ent"],
+                                                      temperature=c["T"])
     return got
 
 
