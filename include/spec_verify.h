@@ -432,6 +432,130 @@ sv_status spec_verify_greedy_host(const void* target_logits, int32_t dtype, int6
                                   float* out_logprob, float* out_mu, int32_t* out_status,
                                   void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The 8-bit paged cache: writing it, the verify pass's attention over it,
+ * accumulated attention weight, and eviction by it.
+ *
+ * K and V are e4m3 codes [num_pages, Hkv, page_size, D], contiguous, with fp32
+ * scales [num_pages, Hkv]; a code stands for code * scale. Position p of
+ * request b is slot p % page_size of page page_table[b, p / page_size].
+ * page_size is 16, 32, 64 or 128; D is 64 or 128; codes are 16-byte aligned.
+ * Offsets into a cache are 64-bit. Entries of page_table past a request's
+ * length are not read. A page id outside [0, num_pages), a position outside
+ * the page table or a node id outside [0, N) sets SV_STATUS_BAD_PAGE.
+ * status pointers may be NULL. */
+#define SV_F16 2   /* element type of queries and new rows only */
+typedef struct sv_q8_cache {
+  void* k;                     /* e4m3 codes */
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* page_table;   /* [B, max_pages] */
+  int32_t num_pages, Hkv, page_size, D, max_pages;
+} sv_q8_cache;
+
+/* Rows of a [B, N, heads, D] tensor: element strides of request, row and head
+ * (each a multiple of 16 bytes; elements of a head are contiguous). */
+typedef struct sv_rows {
+  const void* data;
+  int64_t stride_b, stride_n, stride_h;
+} sv_rows;
+
+/* Write rows of new keys and values (fp32, bf16 or fp16): row i of request b
+ * becomes position seq_base[b] + i. With path_nodes [B, path_cols] row i is
+ * row path_nodes[b, i] of the new rows, and with num_accepted row count is
+ * num_accepted[b] + 1 (else N): a verify pass appends all of its nodes, and
+ * afterwards the accepted path again over them, which leaves the cache as if
+ * only the accepted tokens had been appended. Per page and head touched, the
+ * scale becomes the smallest power of two with max |x| <= 448 scale over the
+ * new rows, or stays if that is larger and the page holds positions below
+ * seq_base; codes of those are rescaled when it grows. Rounding is to nearest
+ * even; infinities saturate, NaN stays NaN, neither counts in the maximum.
+ * out_len[b] = seq_base[b] + row count. A request with a bad page, position or
+ * node is left untouched (out_len = seq_base). Requests must not share the
+ * pages written. */
+sv_status spec_kv_append_q8(const sv_q8_cache* cache, const sv_rows* k_new, const sv_rows* v_new, int32_t dtype,
+                            int32_t B, int32_t N, const int32_t* seq_base, const int32_t* path_nodes,
+                            int32_t path_cols, const int32_t* num_accepted, int32_t* out_len, int32_t* out_status,
+                            void* stream);
+
+/* Attention of the N nodes of a verify pass (bf16 or fp16 queries [B, N, Hq,
+ * D], Hq a multiple of Hkv; head h reads kv head h / (Hq / Hkv)). Node n of
+ * request b is position seq_base[b] + n, whose key and value are in the cache;
+ * it sees every position below seq_base[b], itself, and its ancestors by
+ * parents [B, N] (parents[0] = -1, parents[n] in [0, n)) or, with parents
+ * NULL, every earlier node. n_nodes [B] (or NULL: N) is the number of nodes
+ * of each request; rows past it, and rows that see nothing, get output 0 and
+ * lse -inf. Scores are sm_scale q.k; out [B, N, Hq, D] in the queries' type,
+ * out_lse [B, N, Hq] the natural log of the sum of exponentials (may be
+ * NULL). A parent outside [0, n) ends the path there and sets
+ * SV_STATUS_BAD_PARENT; positions on a bad page are not seen. */
+size_t spec_attention_q8_workspace_size(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int32_t D);
+sv_status spec_attention_q8(const sv_rows* q, int32_t dtype, const sv_q8_cache* cache, int32_t B, int32_t N, int32_t Hq,
+                            const int32_t* seq_base, const int32_t* parents, const int32_t* n_nodes, float sm_scale,
+                            void* out, float* out_lse, int32_t* out_status, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
+/* Accumulated attention weight of accepted rows. Row i (i <= num_accepted[b],
+ * or all N if NULL) of request b is node path_nodes[b, i] (or i) of the verify
+ * pass, at position seq_base[b] + i, and sees the positions up to its own. w[b, hk, j] is the
+ * sum over those rows and the heads of group hk of exp(score - lse), with lse
+ * [B, N, Hq] from spec_attention_q8. out_scores [B, Hkv, S] = decay * scores +
+ * w below seq_base, w from there to the last row's position, 0 past it.
+ * out_scores may be scores. */
+sv_status spec_attention_weights_q8(const sv_rows* q, int32_t dtype, const float* lse, const sv_q8_cache* cache,
+                                    int32_t B, int32_t N, int32_t Hq, const int32_t* seq_base,
+                                    const int32_t* path_nodes, int32_t path_cols, const int32_t* num_accepted,
+                                    float sm_scale, float decay, const float* scores, float* out_scores, int32_t S,
+                                    int32_t* out_status, void* stream);
+
+/* Eviction down to `keep` slots (a multiple of page_size) per request and
+ * head. Slot s < seq_len[b] of head h holds the token at position
+ * positions[b, h, s] (each head keeps its own tokens). Kept are the first
+ * `keep` by: protected (position < sinks, or >= protect_from[b] if given),
+ * then higher score, then lower slot; NaN scores rank last. Kept tokens of
+ * slots >= keep move, in order, into the slots < keep whose tokens go; a
+ * page's scales become the largest of its slots' source pages' scales.
+ * out_scores / out_positions [B, Hkv, S] follow the tokens (0 and -1 past
+ * out_len[b] = min(seq_len[b], keep)) and may be the inputs. Requests no
+ * longer than keep, or with a bad page, keep their tokens. */
+size_t spec_kv_evict_q8_workspace_size(int32_t B, int32_t Hkv, int32_t keep);
+sv_status spec_kv_evict_q8(const sv_q8_cache* cache, int32_t B, const int32_t* seq_len, const float* scores,
+                           const int32_t* positions, int32_t S, int32_t keep, int32_t sinks,
+                           const int32_t* protect_from, float* out_scores, int32_t* out_positions, int32_t* out_len,
+                           int32_t* out_status, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Log-probabilities of given tokens, with entropy and top alternatives, for
+ * rows of logits (fp32 or bf16): per row, p = softmax(x / T);
+ *   out_logprob = ln p(token), 0 where token is -1 (no token);
+ *   out_entropy = -sum p ln p, out_lse = ln sum exp(x / T);
+ *   out_top_tokens / out_top_logprobs [rows, n_top]: the n_top largest logits,
+ *     ties to the lower index, -1 and -inf past the last unmasked token;
+ *   out_saved [rows, 4] fp32, 16-byte aligned: what the gradient needs.
+ * Any output but out_logprob may be NULL (the top pair only if n_top = 0).
+ * Logits of -inf are masked tokens (p = 0). out_status is per row: a token
+ * outside [-1, V) sets SV_STATUS_BAD_TOKEN (log-prob 0); a row with NaN or
+ * +inf sets SV_STATUS_NONFINITE_ROW and its values are NaN; so does a row
+ * whose tokens are all masked, whose lse and log-prob are -inf, entropy 0 and
+ * gradient 0. */
+#define SV_MAX_TOP_ALTERNATIVES 32
+size_t spec_token_logprobs_workspace_size(int32_t rows, int32_t V, int32_t dtype, int32_t n_top);
+sv_status spec_token_logprobs(const void* logits, int32_t dtype, int64_t row_stride, const int32_t* tokens,
+                              int32_t rows, int32_t V, float temperature, int32_t n_top, float* out_logprob,
+                              float* out_entropy, float* out_lse, float* out_saved, int32_t* out_top_tokens,
+                              float* out_top_logprobs, int32_t* out_status, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/* Gradient of sum(grad_logprob * logprob + grad_entropy * entropy) with
+ * respect to the logits, in their type; grad_entropy may be NULL. saved is the
+ * forward call's (same logits, tokens and temperature). out_grad may be
+ * logits (same row stride). */
+sv_status spec_token_logprobs_backward(const void* logits, int32_t dtype, int64_t row_stride, const int32_t* tokens,
+                                       const float* saved, const float* grad_logprob, const float* grad_entropy,
+                                       int32_t rows, int32_t V, float temperature, void* out_grad,
+                                       int64_t grad_row_stride, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

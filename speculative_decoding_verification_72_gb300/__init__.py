@@ -15,3 +15,7 @@ from .verify import (  # noqa: F401
     spec_verify_greedy_host,
     spec_verify_sample, spec_verify_selftest_wait, spec_verify_tree, spec_verify_workspace_size,
 )
+from .kv_q8 import (  # noqa: F401
+    Q8Cache, q8_cache, spec_attention_q8, spec_attention_weights_q8, spec_kv_append_q8, spec_kv_evict_q8,
+)
+from .logprobs import spec_token_logprobs, spec_token_logprobs_backward, token_logprobs  # noqa: F401

@@ -1,4 +1,4 @@
-"""In-tree build of libspecverify.so for sm_103a (nvcc, one translation unit).
+"""In-tree build of libspecverify.so for sm_103a (nvcc, translation units compiled in parallel).
 
 The library links the CUDA runtime statically (nvcc's default), so it does not
 depend on which libcudart the Python process has loaded; device pointers and
@@ -13,7 +13,7 @@ import subprocess
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SRC = os.path.join(PKG, "csrc", "spec_verify.cu")
+SRCS = [os.path.join(PKG, "csrc", n) for n in ("spec_verify.cu", "verify_step.cu")]
 OUT_DIR = os.path.join(PKG, "_lib")
 OUT = os.path.join(OUT_DIR, "libspecverify.so")
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
@@ -33,7 +33,7 @@ def build(verbose=False):
     os.makedirs(OUT_DIR, exist_ok=True)
     cmd = [nvcc_path(), ARCH, "-O3", "-lineinfo", "-std=c++17", "--shared",
            "-Xcompiler", "-fPIC", "-Xptxas", "-v",
-           "-I", os.path.join(ROOT, "include"), "-o", OUT, SRC]
+           "-I", os.path.join(ROOT, "include"), "--threads", "0", "-o", OUT, *SRCS]
     res = subprocess.run(cmd, capture_output=True, text=True)
     with open(os.path.join(OUT_DIR, "build.log"), "w") as f:
         f.write(" ".join(cmd) + "\n" + res.stdout + res.stderr)

@@ -27,6 +27,7 @@
 #include "rules.cuh"
 #include "tree_build.cuh"
 #include "tree_draw.cuh"
+#include "host_util.cuh"
 #include "kv_compact.cuh"
 #include "selftest.cuh"
 
@@ -36,8 +37,6 @@ using namespace sv;
 
 constexpr size_t kAlign = 256;
 static_assert(SV_MAX_STOP_IDS == kMaxStopIds, "stop ids staged in shared memory");
-
-size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 int elem_size(int32_t dtype) {
   if (dtype == SV_F32) return 4;
@@ -95,36 +94,7 @@ bool make_plan(int64_t rows_t, int64_t rows_d, int64_t B, int64_t V, int es, boo
   return true;
 }
 
-// Per-device facts looked up once (SM count, kernel attributes set). Reads
-// take an atomic fast path; the first lookup on a device runs under a mutex,
-// so concurrent first calls from several host threads are safe. Devices past
-// kMaxDevices are not cached (looked up on every call).
-constexpr int kMaxDevices = 64;
-std::mutex g_dev_cache_mu;
-std::atomic<int> g_sm_count[kMaxDevices];
 std::atomic<uint32_t> g_attr_done[kMaxDevices];
-
-int current_device() {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return -1;
-  return dev;
-}
-
-// SM count of the current device.
-int sm_count() {
-  const int dev = current_device();
-  const bool cached = dev >= 0 && dev < kMaxDevices;
-  if (cached) {
-    const int n = g_sm_count[dev].load(std::memory_order_acquire);
-    if (n > 0) return n;
-  }
-  std::lock_guard<std::mutex> lock(g_dev_cache_mu);
-  if (cached && g_sm_count[dev].load(std::memory_order_relaxed) > 0) return g_sm_count[dev].load();
-  int n = 0;
-  if (dev < 0 || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
-  if (cached) g_sm_count[dev].store(n, std::memory_order_release);
-  return n;
-}
 
 // Runs `set` (kernel attribute calls) once per device for the attribute group
 // `bit`; a failed attempt is retried on the next call.
@@ -142,16 +112,6 @@ cudaError_t once_per_device(uint32_t bit, F&& set) {
   return e;
 }
 
-// Largest dynamic shared memory and the largest shared-memory carveout, so
-// two rings fit on one SM.
-template <typename Kern>
-cudaError_t set_smem_attrs(Kern kernel, int smem_bytes) {
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                              static_cast<int>(cudaSharedmemCarveoutMaxShared));
-}
-
 // K1 grid for this device: kK1CtasPerSm per SM, fewer for small problems.
 int k1_grid(int64_t T, int es) {
   int64_t g = static_cast<int64_t>(sm_count()) * kK1CtasPerSm;
@@ -161,8 +121,6 @@ int k1_grid(int64_t T, int es) {
   if (g < 1) g = 1;
   return static_cast<int>(g);
 }
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 bool valid_temperature(float t) { return std::isfinite(t) && t >= 1e-4f; }
 
@@ -185,23 +143,6 @@ RuleArgs rule_args(const sv_rule_params& r) {
   a.alpha = r.rule == SV_RULE_POWER ? r.alpha : 1.f;
   a.thr = nullptr;
   return a;
-}
-
-template <typename Kern, typename Args>
-cudaError_t launch(Kern kernel, int grid, int block, size_t smem, cudaStream_t stream, bool pdl,
-                   const Args& args) {
-  cudaLaunchConfig_t cfg;
-  std::memset(&cfg, 0, sizeof(cfg));
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(static_cast<unsigned>(block));
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = pdl ? attr : nullptr;
-  cfg.numAttrs = pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, args);
 }
 
 template <int ES>
