@@ -1,7 +1,7 @@
 """Token log-probabilities with entropy and top alternatives, and their
-gradient: ctypes binding of spec_token_logprobs and
-spec_token_logprobs_backward (include/spec_verify.h), and ``token_logprobs``,
-the pair as one differentiable torch function."""
+gradient: spec_token_logprobs and spec_token_logprobs_backward
+(include/spec_verify.h), and ``token_logprobs``, the pair as one differentiable
+torch function. Arguments are checked and marshalled by csrc/binding.cpp."""
 
 from __future__ import annotations
 
@@ -9,8 +9,8 @@ import ctypes
 
 import torch
 
-from .verify import SpecVerifyError, _SIGS, _check, _dtype_code, _f32, _rows_view, _ws, load_library
-from .kv_q8 import _ints, _out, _p
+from .verify import _SIGS
+from .kv_q8 import binding
 
 MAX_TOP_ALTERNATIVES = 32
 
@@ -32,57 +32,14 @@ def spec_token_logprobs(logits, tokens, temperature=1.0, n_top=0, workspace=None
     [B, R] (-1: no token, log-prob 0). Returns a dict of CUDA tensors: logprob, entropy, lse [B, R], status [B, R],
     saved [B, R, 4] (for the gradient) and, with n_top > 0 (at most 32), top_tokens and top_logprobs [B, R, n_top] in
     descending order, ties to the lower index, -1 and -inf past the last unmasked token."""
-    lib = load_library()
-    x, stride = _rows_view(logits, "logits")
-    B, R, V = x.shape
-    dev, n_top = x.device, int(n_top)
-    if not 0 <= n_top <= MAX_TOP_ALTERNATIVES:
-        raise SpecVerifyError(f"n_top must lie in [0, {MAX_TOP_ALTERNATIVES}]")
-    tok = _ints(tokens, "tokens", (B, R), dev)
-    code = _dtype_code(x)
-    f, i = torch.float32, torch.int32
-    want = {"logprob": ((B, R), f), "entropy": ((B, R), f), "lse": ((B, R), f), "saved": ((B, R, 4), f), "status": ((B, R), i)}
-    if n_top:
-        want.update(top_tokens=((B, R, n_top), i), top_logprobs=((B, R, n_top), f))
-    out = _out(out, want, dev)
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    need = lib.spec_token_logprobs_workspace_size(B * R, V, code, n_top)
-    if need == 0:
-        raise SpecVerifyError("invalid sizes")
-    ws = _ws(workspace, need, dev, stream)
-    _check(lib.spec_token_logprobs(x.data_ptr(), code, stride, tok.data_ptr(), B * R, V, float(temperature), n_top,
-                                   out["logprob"].data_ptr(), out["entropy"].data_ptr(), out["lse"].data_ptr(),
-                                   out["saved"].data_ptr(), _p(out["top_tokens"]) if n_top else None,
-                                   _p(out["top_logprobs"]) if n_top else None, out["status"].data_ptr(), ws.data_ptr(),
-                                   ws.numel() * ws.element_size(), stream))
-    return out
+    return binding().token_logprobs(logits, tokens, temperature, n_top, workspace, out)
 
 
 def spec_token_logprobs_backward(logits, tokens, saved, grad_logprob, grad_entropy=None, temperature=1.0, out=None):
     """Gradient [B, R, V] (logits' dtype) of sum(grad_logprob * logprob + grad_entropy * entropy); `saved` is
     spec_token_logprobs' for the same logits, tokens and temperature. `out` may be a [B, R, V] tensor, `logits` itself
     among them."""
-    lib = load_library()
-    x, stride = _rows_view(logits, "logits")
-    B, R, V = x.shape
-    dev = x.device
-    tok = _ints(tokens, "tokens", (B, R), dev)
-    if tuple(saved.shape) != (B, R, 4) or saved.dtype != torch.float32 or saved.device != dev or not saved.is_contiguous():
-        raise SpecVerifyError(f"saved must be spec_token_logprobs' contiguous float32 {(B, R, 4)} tensor")
-    g = _f32(grad_logprob, "grad_logprob", (B, R), dev)
-    h = None if grad_entropy is None else _f32(grad_entropy, "grad_entropy", (B, R), dev)
-    if out is None:
-        out, ostride = torch.empty((B, R, V), dtype=x.dtype, device=dev), V
-    else:
-        if tuple(out.shape) != (B, R, V) or out.dtype != x.dtype or out.device != dev:
-            raise SpecVerifyError(f"out must be a {(B, R, V)} {x.dtype} tensor on {dev}")
-        view, ostride = _rows_view(out, "out")
-        if view is not out:
-            raise SpecVerifyError("out must have evenly strided rows of unit stride")
-    _check(lib.spec_token_logprobs_backward(x.data_ptr(), _dtype_code(x), stride, tok.data_ptr(), saved.data_ptr(),
-                                            g.data_ptr(), _p(h), B * R, V, float(temperature), out.data_ptr(), ostride,
-                                            torch.cuda.current_stream(dev).cuda_stream))
-    return out
+    return binding().token_logprobs_backward(logits, tokens, saved, grad_logprob, grad_entropy, temperature, out)
 
 
 class _TokenLogprobs(torch.autograd.Function):
