@@ -59,15 +59,21 @@ struct AttnArgs {
   float* lse;                  // [B, N, Hq] or nullptr
   int32_t* status;             // [B] or nullptr
   int32_t B, N, G, Hq, RB;     // RB: row blocks per kv head
+  uint64_t inv_g;              // ceil(2^32 / G): r / G = r * inv_g >> 32 for r * G < 2^32
   float coef;                  // sm_scale * log2(e)
   float* part;                 // [2 grid][16 MT][D + 4]: o, then (max, sum) in the pad
   int64_t* plan;               // [B + 1] tile offsets of the requests, then the CTAs in use
+  uint32_t* failed;            // [grid]: whether a wait of the CTA gave up, or nullptr
   int32_t grid;
 };
 
 struct AttnReq {
   int base, n, len;
 };
+
+__device__ __forceinline__ int attn_node(const AttnArgs& a, int r) {
+  return static_cast<int>(static_cast<uint64_t>(r) * a.inv_g >> 32);
+}
 
 // Base, node count and length of a request, clamped to the page table's
 // capacity (out_status reports what was clamped).
@@ -82,26 +88,30 @@ __device__ __forceinline__ AttnReq attn_req(const AttnArgs& a, int b) {
   return r;
 }
 
-__device__ __forceinline__ int attn_tiles(const AttnReq& r) { return max(1, (r.len + kAttnTile - 1) / kAttnTile); }
+template <int kTile>
+__device__ __forceinline__ int attn_tiles(const AttnReq& r) {
+  return max(1, (r.len + kTile - 1) / kTile);
+}
 
-// The line of tiles. attn_scan sums the requests' tiles (tiles_of(b) each, for
-// each of ipr items) and, where find >= 0, finds the request that holds tile
-// `find`. CTA-wide; the result is in shared memory. With `store`, the offsets
-// go there.
+// The line of tiles: tiles_of(b) for each of ipr items of every request b.
 struct AttnLine {
-  int64_t total;
-  int64_t off;   // tiles before request b
+  int64_t total;   // tiles of all requests (one item each)
+  int64_t off;     // tiles before request b
   int32_t b;
 };
 
-template <typename F>
-__device__ __forceinline__ void attn_scan(int B, F&& tiles_of, AttnLine* s_line, int64_t* s_warp, int64_t find, int64_t ipr,
+// CTA-wide: sums the requests' tiles, and finds the request that holds the
+// first tile of the CTA's range, first_of(total); offsets go to `store` if given.
+// The result is in shared memory.
+template <int kThreads, typename F, typename G>
+__device__ __forceinline__ void attn_scan(int B, F&& tiles_of, G&& first_of, AttnLine* s_line, int64_t* s_warp, int64_t ipr,
                                           int64_t* store) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int64_t run = 0;
-  for (int c0 = 0; c0 < B; c0 += kAttnThreads) {
+  int64_t run = 0, off = 0;
+  int32_t t = 0;
+  auto chunk = [&](int c0) {   // off, t: of request c0 + tid
     const int b = c0 + tid;
-    const int64_t t = b < B ? tiles_of(b) : 0;
+    t = b < B ? tiles_of(b) : 0;
     int64_t inc = t;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -111,25 +121,63 @@ __device__ __forceinline__ void attn_scan(int B, F&& tiles_of, AttnLine* s_line,
     __syncthreads();
     if (lane == 31) s_warp[warp] = inc;
     __syncthreads();
-    int64_t before = run;
+    off = run + inc - t;
 #pragma unroll
-    for (int w = 0; w < kAttnWarps; ++w) {
-      if (w < warp) before += s_warp[w];
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) off += s_warp[w];
       run += s_warp[w];
     }
-    const int64_t off = before + inc - t;
     if (store && b < B) store[b] = off;
-    if (find >= 0 && b < B && off * ipr <= find && find < (off + t) * ipr) {
+  };
+  for (int c0 = 0; c0 < B; c0 += kThreads) chunk(c0);
+  const int64_t total = run, find = first_of(total);
+  for (int c0 = 0; c0 < B; c0 += kThreads) {
+    if (B > kThreads) {   // more requests than threads: the chunks again
+      if (c0 == 0) run = 0;
+      chunk(c0);
+    }
+    if (c0 + tid < B && off * ipr <= find && find < (off + t) * ipr) {
       s_line->off = off;
-      s_line->b = b;
+      s_line->b = c0 + tid;
     }
   }
-  if (tid == 0) s_line->total = run;
+  if (tid == 0) s_line->total = total;
   __syncthreads();
 }
 
 // CTAs that share TT tiles: all of the grid, or one per tile.
 __device__ __forceinline__ int64_t attn_ctas(int64_t grid, int64_t TT) { return TT < grid ? TT : grid; }
+
+// A CTA's walk over its range of the line: the pieces of items it has.
+struct AttnCursor {
+  int64_t pos, off;
+  AttnReq rq;
+  int b, tiles, h, rb, t0, n;   // request, its tiles, kv head, row block, first tile and tiles of the piece
+
+  __device__ void start(const AttnArgs& a, const AttnLine& line, int64_t lo) {
+    pos = lo;
+    off = line.off;
+    b = line.b;
+    n = 0;
+  }
+  // The next piece (called while pos + n < hi); pos is then its first tile.
+  template <int kTile>
+  __device__ void piece(const AttnArgs& a, int64_t hi, int ipr) {
+    rq = attn_req(a, b);
+    tiles = attn_tiles<kTile>(rq);
+    while (pos >= (off + tiles) * ipr) {
+      off += tiles;
+      rq = attn_req(a, ++b);
+      tiles = attn_tiles<kTile>(rq);
+    }
+    const int rel = static_cast<int>(pos - off * ipr);
+    const int item = rel / tiles;
+    t0 = rel - item * tiles;
+    n = static_cast<int>(min(static_cast<int64_t>(tiles - t0), hi - pos));
+    h = item / a.RB;
+    rb = item - h * a.RB;
+  }
+};
 
 template <int D>
 struct AttnLayout {
@@ -262,8 +310,10 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 ? 3 : 2) attn_q8_kernel(
   const int g = lane >> 2, c = lane & 3;
   const int ipr = a.c.Hkv * a.RB;            // items per request
   const int cta = blockIdx.x;
-  auto tiles_of = [&](int r) { return static_cast<int64_t>(attn_tiles(attn_req(a, r))); };
-  attn_scan(a.B, tiles_of, &s_line, s_warp, -1, ipr, cta == 0 ? a.plan : nullptr);
+  attn_scan<kAttnThreads>(
+      a.B, [&](int r) { return attn_tiles<kAttnTile>(attn_req(a, r)); },
+      [&](int64_t total) { return total * ipr * cta / attn_ctas(a.grid, total * ipr); }, &s_line, s_warp, ipr,
+      cta == 0 ? a.plan : nullptr);
   const int64_t TT = s_line.total * ipr;
   const int64_t Ge = attn_ctas(a.grid, TT);
   if (cta == 0 && tid == 0) {
@@ -272,26 +322,16 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 ? 3 : 2) attn_q8_kernel(
   }
   if (cta >= Ge) return;
   const int64_t lo = TT * cta / Ge, hi = TT * (cta + 1) / Ge;
-  attn_scan(a.B, tiles_of, &s_line, s_warp, lo, ipr, nullptr);
-  int b = s_line.b;
-  int64_t off = s_line.off;
-  AttnReq rq = attn_req(a, b);
   const uint32_t ring = smem_u32(smem) + warp * (kAttnStages * L::kStageBytes);
-  const int words = (a.N + 31) / 32;
 
-  for (int64_t pos = lo; pos < hi;) {
-    int tiles = attn_tiles(rq);
-    while (pos >= (off + tiles) * ipr) {
-      off += tiles;
-      rq = attn_req(a, ++b);
-      tiles = attn_tiles(rq);
-    }
-    const int rel = static_cast<int>(pos - off * ipr);
-    const int item = rel / tiles, t0 = rel - item * tiles;
-    const int nt_ = static_cast<int>(min(static_cast<int64_t>(tiles - t0), hi - pos));
-    const int h = item / a.RB, rb = item - h * a.RB;
-    const int row0 = rb * kRows;
-    const int rows_total = a.N * a.G;
+  AttnCursor cur;
+  for (cur.start(a, s_line, lo); cur.pos < hi; cur.pos += cur.n) {
+    cur.piece<kAttnTile>(a, hi, ipr);
+    const AttnReq rq = cur.rq;
+    const int b = cur.b, h = cur.h, t0 = cur.t0, nt_ = cur.n, tiles = cur.tiles;
+    const int64_t pos = cur.pos;
+    const int row0 = cur.rb * kRows;
+    const int rows_total = a.N * a.G, words = (a.N + 31) / 32;
 
     // ---- page ids and scales of 32 units at a time, one per lane
     int pid = -1, pid_n = -1;
@@ -576,22 +616,29 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 1 ? 3 : 2) attn_q8_kernel(
       }
     }
     __syncthreads();
-    pos += nt_;
   }
 }
 
-// Joins the pieces of items that several CTAs shared, one warp per row; the
-// CTAs of item 0 of each request also check its pages, lengths and tree.
+// Joins the pieces of items that several CTAs shared, one warp a row; B more
+// CTAs check the requests' pages, lengths and trees. All loads of a row's first
+// eight pieces go out together, after one for the plan.
+constexpr int kJoinBatch = 8;
+
 template <typename T, int D, int MT>
 __global__ void __launch_bounds__(kAttnThreads) attn_q8_combine_kernel(const AttnArgs a) {
   constexpr int kRows = 16 * MT, kPitch = AttnLayout<D>::kPitch;
   constexpr int kV = D / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int ipr = a.c.Hkv * a.RB;
-  const int b = blockIdx.x / ipr, item = blockIdx.x - b * ipr;
   grid_dep_wait();
   grid_dep_launch();
-  if (a.status && item == 0) {
+  const int64_t join = blockIdx.x - static_cast<int64_t>(a.status ? a.B : 0);
+  const bool check = join < 0;
+  const int b = check ? blockIdx.x : static_cast<int>(join / (kRows / 4) / ipr);
+  const int64_t off = a.plan[b], total = a.plan[a.B], Ge = a.plan[a.B + 1];
+  const int64_t next = b + 1 < a.B ? a.plan[b + 1] : total;
+  const int64_t tiles = next - off, TT = total * ipr;
+  if (check) {
     const AttnReq rq = attn_req(a, b);
     bool bad_page = a.base[b] < 0 || (a.n_nodes && (a.n_nodes[b] < 0 || a.n_nodes[b] > a.N)) || rq.len != a.base[b] + rq.n;
     for (int j = tid; j < (rq.len + (1 << a.c.page_shift) - 1) >> a.c.page_shift; j += kAttnThreads)
@@ -602,55 +649,76 @@ __global__ void __launch_bounds__(kAttnThreads) attn_q8_combine_kernel(const Att
         const int p = a.parents[static_cast<int64_t>(b) * a.N + n];
         bad_parent = bad_parent || (n == 0 ? p != -1 : p < 0 || p >= n);
       }
+    bool late = false;
+    if (a.failed) {
+      const int64_t first = ((off * ipr + 1) * Ge - 1) / TT, last = (next * ipr * Ge - 1) / TT;
+      for (int64_t i = first + tid; i <= last; i += kAttnThreads) late = late || a.failed[i] != 0;
+    }
     bad_page = __syncthreads_or(bad_page);
     bad_parent = __syncthreads_or(bad_parent);
-    if (tid == 0) a.status[b] = (bad_page ? SV_STATUS_BAD_PAGE : 0) | (bad_parent ? SV_STATUS_BAD_PARENT : 0);
+    late = __syncthreads_or(late);
+    if (tid == 0)
+      a.status[b] = (bad_page ? SV_STATUS_BAD_PAGE : 0) | (bad_parent ? SV_STATUS_BAD_PARENT : 0) | (late ? SV_STATUS_TIMEOUT : 0);
+    return;
   }
-  const int64_t off = a.plan[b], total = a.plan[a.B], Ge = a.plan[a.B + 1];
-  const int64_t next = b + 1 < a.B ? a.plan[b + 1] : total;
-  const int64_t tiles = next - off, TT = total * ipr;
+  const int item = static_cast<int>(join / (kRows / 4) - static_cast<int64_t>(b) * ipr);
   const int64_t t0 = off * ipr + item * tiles, t1 = t0 + tiles;
   const int64_t c0 = ((t0 + 1) * Ge - 1) / TT, c1 = (t1 * Ge - 1) / TT;
   if (c0 == c1) return;   // one CTA had all of it
   const int h = item / a.RB, rb = item - h * a.RB;
   const int slot0 = TT * c0 / Ge == t0 ? 0 : 1;
-  for (int r = warp; r < kRows; r += kAttnWarps) {
-    const int R = rb * kRows + r;
-    if (R >= a.N * a.G) break;
-    float m = -INFINITY;
-    for (int64_t i = c0 + lane; i <= c1; i += 32)
-      m = fmaxf(m, a.part[((2 * i + (i == c0 ? slot0 : 0)) * kRows + r) * kPitch + D]);
-    m = warp_max(m);
-    const float m0 = m == -INFINITY ? 0.f : m;
-    float l = 0.f, v[kV];
+  const int r = static_cast<int>(join % (kRows / 4)) * 4 + warp, R = rb * kRows + r;
+  if (R >= a.N * a.G) return;
+  float m = -INFINITY, l = 0.f, v[kV];
 #pragma unroll
-    for (int k = 0; k < kV; ++k) v[k] = 0.f;
-#pragma unroll 4
-    for (int64_t i = c0; i <= c1; ++i) {
+  for (int k = 0; k < kV; ++k) v[k] = 0.f;
+  for (int64_t i0 = c0; i0 <= c1; i0 += kJoinBatch) {
+    float2 ml[kJoinBatch];
+    float t[kJoinBatch][kV];
+#pragma unroll
+    for (int k = 0; k < kJoinBatch; ++k) {
+      const int64_t i = min(i0 + k, c1);
       const float* p = a.part + ((2 * i + (i == c0 ? slot0 : 0)) * kRows + r) * kPitch;
-      const float2 ml = *reinterpret_cast<const float2*>(p + D);
-      const float f = ex2(ml.x - m0);
-      l += ml.y * f;
+      ml[k] = *reinterpret_cast<const float2*>(p + D);
       if (kV == 4) {
-        const float4 t = *reinterpret_cast<const float4*>(p + lane * 4);
-        v[0] += t.x * f;
-        v[1] += t.y * f;
-        v[2 % kV] += t.z * f;
-        v[3 % kV] += t.w * f;
+        const float4 x = *reinterpret_cast<const float4*>(p + lane * 4);
+        t[k][0] = x.x;
+        t[k][1] = x.y;
+        t[k][2 % kV] = x.z;
+        t[k][3 % kV] = x.w;
       } else {
-        const float2 t = *reinterpret_cast<const float2*>(p + lane * 2);
-        v[0] += t.x * f;
-        v[1] += t.y * f;
+        const float2 x = *reinterpret_cast<const float2*>(p + lane * 2);
+        t[k][0] = x.x;
+        t[k][1] = x.y;
       }
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int n = R / a.G;
-    const int64_t row = (static_cast<int64_t>(b) * a.N + n) * a.Hq + h * a.G + (R - n * a.G);
-    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.out) + row * D * 2) + lane * (kV / 2);
-    dst[0] = T::pack2(v[0] * inv, v[1] * inv);
-    if (kV == 4) dst[1] = T::pack2(v[2 % kV] * inv, v[3 % kV] * inv);
-    if (a.lse && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (m0 + log2f(l)) * kLn2;
+    float top = m;
+#pragma unroll
+    for (int k = 0; k < kJoinBatch; ++k) top = i0 + k <= c1 ? fmaxf(top, ml[k].x) : top;
+    const float top0 = top == -INFINITY ? 0.f : top;
+    const float f0 = ex2(m - top0);
+    l *= f0;
+#pragma unroll
+    for (int e = 0; e < kV; ++e) v[e] *= f0;
+#pragma unroll
+    for (int k = 0; k < kJoinBatch; ++k) {
+      const float f = ex2(ml[k].x - top0);
+      if (i0 + k <= c1) {
+        l = fmaf(ml[k].y, f, l);
+#pragma unroll
+        for (int e = 0; e < kV; ++e) v[e] = fmaf(t[k][e], f, v[e]);
+      }
+    }
+    m = top;
   }
+  const float m0 = m == -INFINITY ? 0.f : m;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int n = attn_node(a, R);
+  const int64_t row = (static_cast<int64_t>(b) * a.N + n) * a.Hq + h * a.G + (R - n * a.G);
+  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.out) + row * D * 2) + lane * (kV / 2);
+  dst[0] = T::pack2(v[0] * inv, v[1] * inv);
+  if (kV == 4) dst[1] = T::pack2(v[2 % kV] * inv, v[3 % kV] * inv);
+  if (a.lse && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (m0 + log2f(l)) * kLn2;
 }
 
 }  // namespace sv

@@ -70,15 +70,19 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 4 ? 3 : 4) attn_weights_q8
   const int g = lane >> 2, c = lane & 3;
   const int H = a.c.Hkv, cta = blockIdx.x;
 
-  auto tiles_of = [&](int r) { return static_cast<int64_t>((weight_req(a, r).len + kAttnTile - 1) / kAttnTile); };
-  attn_scan(a.B, tiles_of, &s_line, s_warp, -1, H, nullptr);
+  attn_scan<kAttnThreads>(
+      a.B, [&](int r) { return (weight_req(a, r).len + kAttnTile - 1) / kAttnTile; },
+      [&](int64_t total) {
+        const int64_t n = attn_ctas(a.grid, total * H);
+        return cta < n ? total * H * cta / n : 0;
+      },
+      &s_line, s_warp, H, nullptr);
   const int64_t TT = s_line.total * H;
   const int64_t Ge = attn_ctas(a.grid, TT);
   const uint32_t ring = smem_u32(smem) + warp * (kWtStages * kUnit);
 
   if (cta < Ge) {
     const int64_t lo = TT * cta / Ge, hi = TT * (cta + 1) / Ge;
-    attn_scan(a.B, tiles_of, &s_line, s_warp, lo, H, nullptr);
     int b = s_line.b;
     int64_t off = s_line.off;
     AttnReq rq = weight_req(a, b);

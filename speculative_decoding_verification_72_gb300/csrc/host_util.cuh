@@ -56,9 +56,9 @@ inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
-template <typename Kern, typename Args>
+template <typename Kern, typename... Args>
 cudaError_t launch(Kern kernel, int grid, int block, size_t smem, cudaStream_t stream, bool pdl,
-                   const Args& args) {
+                   const Args&... args) {
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof(cfg));
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
@@ -70,7 +70,7 @@ cudaError_t launch(Kern kernel, int grid, int block, size_t smem, cudaStream_t s
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = pdl ? attr : nullptr;
   cfg.numAttrs = pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, args);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // set_smem_attrs once per kernel and device, then a PDL launch.
@@ -79,8 +79,8 @@ struct SmemSet {
   inline static std::atomic<uint64_t> done{0};
 };
 
-template <auto Kern, typename Args>
-cudaError_t launch_smem(int grid, int block, size_t smem, cudaStream_t stream, const Args& args) {
+template <auto Kern, typename... Args>
+cudaError_t launch_smem(int grid, int block, size_t smem, cudaStream_t stream, const Args&... args) {
   const int dev = current_device();
   const bool cached = dev >= 0 && dev < kMaxDevices;
   if (!cached || !(SmemSet<Kern>::done.load(std::memory_order_acquire) >> dev & 1)) {
@@ -88,7 +88,7 @@ cudaError_t launch_smem(int grid, int block, size_t smem, cudaStream_t stream, c
     if (e != cudaSuccess) return e;
     if (cached) SmemSet<Kern>::done.fetch_or(1ull << dev, std::memory_order_release);
   }
-  return launch(Kern, grid, block, smem, stream, true, args);
+  return launch(Kern, grid, block, smem, stream, true, args...);
 }
 
 }  // namespace sv

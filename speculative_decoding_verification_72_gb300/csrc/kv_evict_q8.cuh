@@ -80,7 +80,7 @@ __device__ __forceinline__ uint32_t evict_scan(uint32_t v, uint32_t* s_warp, uin
 }
 
 __global__ void __launch_bounds__(kEvThreads, 1) kv_evict_select_kernel(const EvictArgs a) {
-  extern __shared__ __align__(16) uint8_t smem[];
+  extern __shared__ __align__(128) uint8_t smem[];
   uint32_t* s_hist = reinterpret_cast<uint32_t*>(smem);   // kEvBins
   uint32_t* s_key = s_hist + kEvBins;                     // n_keys
   __shared__ uint32_t s_warp[32], s_bin, s_above, s_in_bin;

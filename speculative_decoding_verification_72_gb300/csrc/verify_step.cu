@@ -10,6 +10,7 @@
 #include "spec_verify.h"
 #include "host_util.cuh"
 #include "attn_q8.cuh"
+#include "attn_q8_cols.cuh"
 #include "attn_weights_q8.cuh"
 #include "kv_append_q8.cuh"
 #include "kv_evict_q8.cuh"
@@ -70,20 +71,65 @@ cudaError_t launch_append(const AppendArgs& a, int grid, int P, int D, cudaStrea
 
 // --------------------------------------------------------------- attention
 
-// Row blocks of 16 rows where all of a kv head's rows fit, else of 32.
+// Row blocks of 16 rows where all of a kv head's rows fit, else of 32. One block takes the column kernel.
 int attn_mt(int64_t rows) { return rows <= 16 ? 1 : 2; }
 
-// CTAs an SM holds: 3 of the 16-row kernel, 2 of the 32-row kernel (registers and shared memory).
-int attn_grid_max(int mt) { return sm_count() * (mt == 1 ? 3 : 2); }
+// CTAs an SM holds: two of either kernel (TMEM and shared memory; registers).
+int attn_grid_max() { return 2 * sm_count(); }
 
 constexpr int kAttnGridMost = 1024;   // what a workspace is sized for, whatever the device
 
+// cuTensorMapEncodeTiled of the loaded driver.
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled encode_tiled() {
+  static std::atomic<void*> found{nullptr};
+  void* f = found.load(std::memory_order_acquire);
+  if (!f) {
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      return nullptr;
+    found.store(f, std::memory_order_release);
+  }
+  return reinterpret_cast<EncodeTiled>(f);
+}
+
+// The codes as [pages * heads][page rows][D bytes], read in boxes of a page's
+// head, swizzled for the tensor cores.
+bool code_map(const sv_q8_cache& c, void* codes, CUtensorMap* m) {
+  const EncodeTiled f = encode_tiled();
+  if (!f) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(c.D), static_cast<cuuint64_t>(c.page_size),
+                              static_cast<cuuint64_t>(c.num_pages) * c.Hkv};
+  const cuuint64_t strides[2] = {dims[0], dims[0] * dims[1]};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(c.D), static_cast<cuuint32_t>(c.page_size), 1}, one[3] = {1, 1, 1};
+  return f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, codes, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+           c.D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <typename T, int D, int MT>
-cudaError_t launch_attn(AttnArgs& a, int64_t items, cudaStream_t st) {
-  const size_t smem = attn_smem_bytes<D, MT>(SV_MAX_TREE_NODES);
-  cudaError_t e = launch_smem<attn_q8_kernel<T, D, MT>>(a.grid, kAttnThreads, smem, st, a);
-  if (e != cudaSuccess) return e;
-  return launch(attn_q8_combine_kernel<T, D, MT>, static_cast<int>(items), kAttnThreads, 0, st, true, a);
+cudaError_t launch_join(const AttnArgs& a, int64_t items, cudaStream_t st) {
+  const int64_t grid = items * 4 * MT + (a.status ? a.B : 0);
+  if (grid > INT32_MAX) return cudaErrorInvalidValue;
+  return launch(attn_q8_combine_kernel<T, D, MT>, static_cast<int>(grid), kAttnThreads, 0, st, true, a);
+}
+
+template <typename T, int D, int MT>
+cudaError_t launch_attn(const AttnArgs& a, int64_t items, cudaStream_t st) {
+  const cudaError_t e = launch_smem<attn_q8_kernel<T, D, MT>>(a.grid, kAttnThreads, attn_smem_bytes<D, MT>(SV_MAX_TREE_NODES), st, a);
+  return e != cudaSuccess ? e : launch_join<T, D, MT>(a, items, st);
+}
+
+template <typename T, int D, int MT, int NT>
+cudaError_t launch_cols(const sv_q8_cache& c, const AttnArgs& a, int64_t items, cudaStream_t st) {
+  CUtensorMap k, v;
+  if (!code_map(c, c.k, &k) || !code_map(c, c.v, &v)) return cudaErrorInvalidValue;
+  constexpr int kSmem = ColLayout<D, MT, NT>::bytes(1);   // at most 32 rows, so 32 nodes: one mask word
+  const cudaError_t e = launch_smem<attn_q8_cols_kernel<T, D, MT, NT>>(a.grid, ColLayout<D, MT, NT>::kThreads, kSmem, st, k, v, a);
+  return e != cudaSuccess ? e : launch_join<T, D, MT>(a, items, st);
 }
 
 template <typename T, int D>
@@ -167,7 +213,8 @@ sv_status spec_kv_append_q8(const sv_q8_cache* cache, const sv_rows* k_new, cons
 size_t spec_attention_q8_workspace_size(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int32_t D) {
   if (B < 0 || N < 1 || N > SV_MAX_TREE_NODES || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || (D != 64 && D != 128)) return 0;
   const int mt = attn_mt(static_cast<int64_t>(N) * (Hq / Hkv));
-  return attn_ws_part_bytes(mt, D) + align_up((static_cast<size_t>(B) + 2) * sizeof(int64_t), kAlign);
+  return attn_ws_part_bytes(mt, D) + align_up(kAttnGridMost * sizeof(uint32_t), kAlign) +
+         align_up((static_cast<size_t>(B) + 2) * sizeof(int64_t), kAlign);
 }
 
 sv_status spec_attention_q8(const sv_rows* q, int32_t dtype, const sv_q8_cache* cache, int32_t B, int32_t N, int32_t Hq,
@@ -200,24 +247,34 @@ sv_status spec_attention_q8(const sv_rows* q, int32_t dtype, const sv_q8_cache* 
   a.N = N;
   a.Hq = Hq;
   a.G = Hq / cache->Hkv;
+  a.inv_g = ((1ull << 32) + a.G - 1) / a.G;
   const int64_t rows = static_cast<int64_t>(N) * a.G;
+  if (rows > SV_MAX_TREE_NODES * 1024) return SV_ERR_INVALID_ARG;
   const int mt = attn_mt(rows);
   a.RB = static_cast<int32_t>((rows + 16 * mt - 1) / (16 * mt));
   a.coef = static_cast<float>(static_cast<double>(sm_scale) * 1.4426950408889634);
   a.part = static_cast<float*>(workspace);
-  a.plan = reinterpret_cast<int64_t*>(static_cast<uint8_t*>(workspace) + attn_ws_part_bytes(mt, cache->D));
+  uint8_t* after = static_cast<uint8_t*>(workspace) + attn_ws_part_bytes(mt, cache->D);
+  const bool cols = rows <= 32;
+  a.failed = cols ? reinterpret_cast<uint32_t*>(after) : nullptr;
+  a.plan = reinterpret_cast<int64_t*>(after + align_up(kAttnGridMost * sizeof(uint32_t), kAlign));
   const int64_t items = static_cast<int64_t>(B) * cache->Hkv * a.RB;
-  const int64_t tiles = (static_cast<int64_t>(cache->max_pages) * cache->page_size + kAttnTile - 1) / kAttnTile;
-  if (items > INT32_MAX || cache->Hkv * a.RB * tiles > INT32_MAX) return SV_ERR_INVALID_ARG;
-  a.grid = static_cast<int32_t>(std::min<int64_t>({attn_grid_max(mt), kAttnGridMost, items * tiles}));
+  const int tile = cols ? kColTile : kAttnTile;
+  const int64_t tiles = (static_cast<int64_t>(cache->max_pages) * cache->page_size + tile - 1) / tile;
+  if (items * 8 + B > INT32_MAX || cache->Hkv * a.RB * tiles > INT32_MAX) return SV_ERR_INVALID_ARG;
+  a.grid = static_cast<int32_t>(std::min<int64_t>({attn_grid_max(), kAttnGridMost, items * tiles}));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const sv_q8_cache& c = *cache;
   cudaError_t e;
-  if (dtype == SV_BF16)
-    e = cache->D == 128 ? (mt == 1 ? launch_attn<TypeBf16, 128, 1>(a, items, st) : launch_attn<TypeBf16, 128, 2>(a, items, st))
-                        : (mt == 1 ? launch_attn<TypeBf16, 64, 1>(a, items, st) : launch_attn<TypeBf16, 64, 2>(a, items, st));
+  if (!cols)
+    e = dtype == SV_BF16 ? (c.D == 128 ? launch_attn<TypeBf16, 128, 2>(a, items, st) : launch_attn<TypeBf16, 64, 2>(a, items, st))
+                         : (c.D == 128 ? launch_attn<TypeF16, 128, 2>(a, items, st) : launch_attn<TypeF16, 64, 2>(a, items, st));
+  else if (dtype == SV_BF16)
+    e = c.D == 128 ? (mt == 1 ? launch_cols<TypeBf16, 128, 1, 2>(c, a, items, st) : launch_cols<TypeBf16, 128, 2, 2>(c, a, items, st))
+                   : (mt == 1 ? launch_cols<TypeBf16, 64, 1, 2>(c, a, items, st) : launch_cols<TypeBf16, 64, 2, 2>(c, a, items, st));
   else
-    e = cache->D == 128 ? (mt == 1 ? launch_attn<TypeF16, 128, 1>(a, items, st) : launch_attn<TypeF16, 128, 2>(a, items, st))
-                        : (mt == 1 ? launch_attn<TypeF16, 64, 1>(a, items, st) : launch_attn<TypeF16, 64, 2>(a, items, st));
+    e = c.D == 128 ? (mt == 1 ? launch_cols<TypeF16, 128, 1, 3>(c, a, items, st) : launch_cols<TypeF16, 128, 2, 3>(c, a, items, st))
+                   : (mt == 1 ? launch_cols<TypeF16, 64, 1, 3>(c, a, items, st) : launch_cols<TypeF16, 64, 2, 3>(c, a, items, st));
   return done(e);
 }
 
