@@ -1,4 +1,4 @@
-// The verify pass's attention over the 8-bit paged cache.
+// The verify pass's attention over the 8-bit paged cache: what its kernels share.
 //
 // For node n of request b (position base_b + n) and head h of group h / G:
 //   s_j = sm_scale * q . (ck_j * ks), o = sum_j softmax(s)_j * (cv_j * vs), lse = ln sum_j exp s_j
@@ -7,35 +7,14 @@
 // sees nothing gets o = 0 and lse = -inf.
 //
 // Rows. The N * G rows of one kv head share its keys, so they are packed as
-// r = n * G + g and taken in blocks of 16 * MT.
+// r = n * G + g: up to 32 of them are columns of one product
+// (attn_q8_cols.cuh, bound by memory), more are blocks of 128 lanes
+// (attn_q8_rows.cuh, bound by the tensor cores).
 //
 // Split. The work of all (request, kv head, row block) items is one line of
-// 64-token tiles, cut into equal ranges, one per CTA, so mixed lengths load
+// 128-token tiles, cut into equal ranges, one per CTA, so mixed lengths load
 // every CTA alike. A range that holds only part of an item writes a partial
 // (max, sum, unnormalised o) that attn_q8_combine_kernel joins.
-//
-// One pass per range: running maximum and sum per row (fp32), o in registers
-// (fp32), keys and values read once. Each warp takes 16 tokens of a tile on
-// its own: its 4 KB of codes arrive by cp.async in a ring private to the warp,
-// and are turned into f16 fragments in registers. e4m3 to f16 is exact; q is
-// scaled per row by a power of two so that bf16 fits f16 exactly; so the
-// scores are exact products summed in fp32. P is rounded to f16 (relative
-// 2^-11, like the f16 output it feeds and finer than bf16), values are exact.
-//
-// Layout of the fragments. m16n8k16 leaves the order of k free as long as A
-// and B agree. For S = Q K^T lane quad c takes d in [c D/4, (c+1) D/4), so a
-// token's codes are 32 contiguous bytes per lane (D = 128). For O = P V the
-// rows of a k step are native, and lane group g takes the n columns
-// d = (D/8) g + j of n-tile j: 16 contiguous bytes of a token, two byte
-// permutes pairing two tokens' codes. Shared rows are swizzled (16-byte chunk
-// index xor row) so both patterns are free of bank conflicts at D = 128.
-//
-// Scales. A 16-token unit lies in one page, so ks and vs are uniform in the
-// warp: ks joins the softmax coefficient, vs multiplies p relative to the
-// largest |vs| so far (P stays within f16's range), o is rescaled when that
-// grows. The row maximum is raised only when a score exceeds it by 2^8 (P and
-// its sum stay far inside f16's and fp32's range), so most units need neither
-// a maximum across lanes nor a rescale.
 #pragma once
 
 #include "q8_common.cuh"
@@ -45,8 +24,6 @@ namespace sv {
 constexpr int kAttnThreads = 128;
 constexpr int kAttnWarps = 4;
 constexpr int kAttnTile = 64;        // tokens per CTA step: 16 per warp
-constexpr int kAttnStages = 4;
-constexpr float kAttnSlack = 8.f;    // log2 by which a score may exceed the running maximum
 
 struct AttnArgs {
   const uint8_t* q;
@@ -61,7 +38,7 @@ struct AttnArgs {
   int32_t B, N, G, Hq, RB;     // RB: row blocks per kv head
   uint64_t inv_g;              // ceil(2^32 / G): r / G = r * inv_g >> 32 for r * G < 2^32
   float coef;                  // sm_scale * log2(e)
-  float* part;                 // [2 grid][16 MT][D + 4]: o, then (max, sum) in the pad
+  float* part;                 // [2 grid][rows of a block][D + 4]: o, then (max, sum) in the pad
   int64_t* plan;               // [B + 1] tile offsets of the requests, then the CTAs in use
   uint32_t* failed;            // [grid]: whether a wait of the CTA gave up, or nullptr
   int32_t grid;
@@ -181,22 +158,8 @@ struct AttnCursor {
 
 template <int D>
 struct AttnLayout {
-  static constexpr int kUnitBytes = 16 * D;             // 16 tokens of K or V
-  static constexpr int kStageBytes = 2 * kUnitBytes;
-  static constexpr int kRingBytes = kAttnWarps * kAttnStages * kStageBytes;
-  static constexpr int kPitch = D + 4;                  // floats per row of the merge buffer
+  static constexpr int kPitch = D + 4;   // floats per row of a partial: o, then (max, sum)
 };
-
-// The ring, and over it the buffer that joins the warps' rows.
-template <int D, int MT>
-__host__ __device__ constexpr int attn_buf_bytes() {
-  constexpr int merge = kAttnWarps * 16 * MT * AttnLayout<D>::kPitch * 4;
-  return merge > AttnLayout<D>::kRingBytes ? merge : AttnLayout<D>::kRingBytes;
-}
-template <int D, int MT>
-constexpr int attn_smem_bytes(int N) {
-  return attn_buf_bytes<D, MT>() + MT * (D / 16) * 512 + 16 * MT * 4 + kAttnWarps * 16 * MT * 8 + 16 * MT * ((N + 31) / 32) * 4;
-}
 
 // Byte offset of 16-byte chunk ch of token row `row` within a unit.
 template <int D>
@@ -278,344 +241,6 @@ __device__ __forceinline__ void unit_scores(uint32_t k_unit, const uint4* s_q, i
       mma_f16(s[mt][0], qa, b[0][0], b[0][1]);
       mma_f16(s[mt][1], qa, b[1][0], b[1][1]);
     }
-  }
-}
-
-__device__ __forceinline__ uint32_t nan_ones(uint32_t h2) {   // f16x2: 1 where NaN, else 0
-  return ((h2 & 0x7fffu) > 0x7c00u ? 0x3c00u : 0u) | ((h2 >> 16 & 0x7fffu) > 0x7c00u ? 0x3c000000u : 0u);
-}
-__device__ __forceinline__ uint32_t nan_zero(uint32_t h2) {   // f16x2: 0 where NaN
-  return ((h2 & 0x7fffu) > 0x7c00u ? 0u : h2 & 0xffffu) | ((h2 >> 16 & 0x7fffu) > 0x7c00u ? 0u : h2 & 0xffff0000u);
-}
-
-template <typename T, int D, int MT>
-__global__ void __launch_bounds__(kAttnThreads, MT == 1 ? 3 : 2) attn_q8_kernel(const AttnArgs a) {
-  using L = AttnLayout<D>;
-  constexpr int kKs = D / 16;
-  constexpr int kRows = 16 * MT;
-  constexpr int kNt = D / 8;                 // n-tiles of O
-  constexpr int kChunks = 16 * (D / 16);     // 16-byte chunks per unit of K or V
-  extern __shared__ __align__(128) uint8_t smem[];
-  uint4* s_q = reinterpret_cast<uint4*>(smem + attn_buf_bytes<D, MT>());         // MT * kKs * 32
-  float* s_qs = reinterpret_cast<float*>(s_q + MT * kKs * 32);                 // kRows
-  float2* s_ml = reinterpret_cast<float2*>(s_qs + kRows);                      // [warps][kRows]
-  uint32_t* s_anc = reinterpret_cast<uint32_t*>(s_ml + kAttnWarps * kRows);    // [nodes of the block][words]
-  __shared__ AttnLine s_line;
-  __shared__ int64_t s_warp[kAttnWarps];
-  float* s_o = reinterpret_cast<float*>(smem);                                 // merge buffer over the ring
-
-  grid_dep_wait();
-  grid_dep_launch();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int g = lane >> 2, c = lane & 3;
-  const int ipr = a.c.Hkv * a.RB;            // items per request
-  const int cta = blockIdx.x;
-  attn_scan<kAttnThreads>(
-      a.B, [&](int r) { return attn_tiles<kAttnTile>(attn_req(a, r)); },
-      [&](int64_t total) { return total * ipr * cta / attn_ctas(a.grid, total * ipr); }, &s_line, s_warp, ipr,
-      cta == 0 ? a.plan : nullptr);
-  const int64_t TT = s_line.total * ipr;
-  const int64_t Ge = attn_ctas(a.grid, TT);
-  if (cta == 0 && tid == 0) {
-    a.plan[a.B] = s_line.total;
-    a.plan[a.B + 1] = Ge;
-  }
-  if (cta >= Ge) return;
-  const int64_t lo = TT * cta / Ge, hi = TT * (cta + 1) / Ge;
-  const uint32_t ring = smem_u32(smem) + warp * (kAttnStages * L::kStageBytes);
-
-  AttnCursor cur;
-  for (cur.start(a, s_line, lo); cur.pos < hi; cur.pos += cur.n) {
-    cur.piece<kAttnTile>(a, hi, ipr);
-    const AttnReq rq = cur.rq;
-    const int b = cur.b, h = cur.h, t0 = cur.t0, nt_ = cur.n, tiles = cur.tiles;
-    const int64_t pos = cur.pos;
-    const int row0 = cur.rb * kRows;
-    const int rows_total = a.N * a.G, words = (a.N + 31) / 32;
-
-    // ---- page ids and scales of 32 units at a time, one per lane
-    int pid = -1, pid_n = -1;
-    float ksv = 0.f, vsv = 0.f, ks_n = 0.f, vs_n = 0.f;
-    auto fetch = [&](int i0, int& p, float& k_, float& v_) {
-      const int tok = (t0 + i0 + lane) * kAttnTile + warp * 16;
-      p = i0 + lane < nt_ && tok < rq.len ? q8_page(a.c, b, tok >> a.c.page_shift) : -1;
-      k_ = v_ = 0.f;
-      if (p >= 0) {
-        const int64_t o = static_cast<int64_t>(p) * a.c.Hkv + h;
-        k_ = a.c.ks[o];
-        v_ = a.c.vs[o];
-      }
-    };
-    auto issue = [&](int i, int page) {
-      if (i < nt_) {
-        const int tok = (t0 + i) * kAttnTile + warp * 16;
-        const int valid = page < 0 ? 0 : rq.len - tok;
-        const int64_t o =
-            (((static_cast<int64_t>(max(page, 0)) * a.c.Hkv + h) << a.c.page_shift) + (tok & ((1 << a.c.page_shift) - 1))) * D;
-        const uint32_t dst = ring + (i % kAttnStages) * L::kStageBytes;
-#pragma unroll
-        for (int it = 0; it < kChunks / 32; ++it) {
-          const int ch = it * 32 + lane;
-          const int row = ch / (D / 16), col = ch % (D / 16);
-          const uint32_t to = dst + unit_off<D>(row, col);
-          cp_async16(to, a.c.k + o + ch * 16, row < valid);
-          cp_async16(to + L::kUnitBytes, a.c.v + o + ch * 16, row < valid);
-        }
-      }
-      cp_async_commit();
-    };
-    fetch(0, pid, ksv, vsv);
-    if (nt_ > 32) fetch(32, pid_n, ks_n, vs_n);
-#pragma unroll
-    for (int i = 0; i < kAttnStages - 1; ++i) issue(i, __shfl_sync(0xffffffffu, pid, i));
-
-    // ---- the row block's queries and its nodes' ancestor sets
-    load_q_frags<T, D, MT, kAttnThreads>(a.q + b * a.sqb + static_cast<int64_t>(h) * a.G * a.sqh, a.sqn, a.sqh, rows_total,
-                                         row0, a.G, nullptr, rq.n, reinterpret_cast<uint32_t*>(s_q), s_qs);
-    const int node0 = row0 / a.G;
-    const bool tail = (t0 + nt_) * kAttnTile > rq.base;
-    if (tail && a.parents) {
-      const int nodes = min((row0 + kRows - 1) / a.G, a.N - 1) - node0 + 1;
-      for (int i = tid; i < nodes * words; i += kAttnThreads) s_anc[i] = 0;
-      __syncthreads();
-      const int32_t* par = a.parents + static_cast<int64_t>(b) * a.N;
-      for (int i = tid; i < nodes; i += kAttnThreads) {
-        int n = node0 + i;
-        while (n >= 0) {
-          s_anc[i * words + (n >> 5)] |= 1u << (n & 31);
-          const int up = par[n];
-          n = up < n ? up : -1;   // a parent precedes its child; anything else ends the path
-        }
-      }
-    }
-    __syncthreads();
-
-    float o[MT][kNt][4];
-    float m_run[MT][2], l_run[MT][2], cq[MT][2];
-    int node[MT][2];
-    float ref = 1e-30f;   // largest |vs| so far
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-      for (int j = 0; j < kNt; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[mt][j][i] = 0.f;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = mt * 16 + i * 8 + g;
-        m_run[mt][i] = -INFINITY;
-        l_run[mt][i] = 0.f;
-        cq[mt][i] = s_qs[r] * a.coef;
-        const int R = row0 + r;
-        node[mt][i] = R < rows_total && R / a.G < rq.n ? R / a.G : -1;
-      }
-    }
-
-    for (int i = 0; i < nt_; ++i) {
-      const int page = __shfl_sync(0xffffffffu, pid, i & 31);
-      const float ks = __shfl_sync(0xffffffffu, ksv, i & 31), vs = __shfl_sync(0xffffffffu, vsv, i & 31);
-      cp_async_wait<kAttnStages - 2>();
-      __syncwarp();
-      // The slot of unit i - 1 is free now; fill it.
-      {
-        const int j = i + kAttnStages - 1;
-        const int pj = __shfl_sync(0xffffffffu, (j ^ i) & ~31 ? pid_n : pid, j & 31);
-        issue(j, pj);
-      }
-      if ((i & 31) == 31) {
-        pid = pid_n;
-        ksv = ks_n;
-        vsv = vs_n;
-        fetch(i + 33, pid_n, ks_n, vs_n);
-      }
-      if (page < 0) continue;   // past the end, or a page that is not there
-      const uint32_t k_unit = ring + (i % kAttnStages) * L::kStageBytes, v_unit = k_unit + L::kUnitBytes;
-      float s[MT][2][4];
-      unit_scores<D, MT>(k_unit, s_q, lane, s);
-      const int tok = (t0 + i) * kAttnTile + warp * 16;
-      const bool edge = tok + 16 > rq.base;   // holds new nodes or the end
-      bool raise = false;
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float x = s[mt][nt][e] * (cq[mt][e >> 1] * ks);
-            if (edge) {
-              const int m = tok + nt * 8 + 2 * c + (e & 1) - rq.base;
-              const int n = node[mt][e >> 1];
-              bool see = n >= 0 && m < rq.n;
-              if (see && m >= 0) {
-                see = m <= n;
-                if (see && a.parents) see = s_anc[(n - node0) * words + (m >> 5)] >> (m & 31) & 1;
-              }
-              if (!see) x = -INFINITY;
-            } else if (node[mt][e >> 1] < 0) {
-              x = -INFINITY;
-            }
-            s[mt][nt][e] = x;
-            raise = raise || x > m_run[mt][e >> 1] + kAttnSlack;
-          }
-      const float av = fabsf(vs);
-      if (__any_sync(0xffffffffu, raise || av > ref)) {
-        const float ref_new = fmaxf(ref, av);
-        const float fr = ref / ref_new;
-        ref = ref_new;
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int i2 = 0; i2 < 2; ++i2) {
-            float mx = fmaxf(fmaxf(s[mt][0][2 * i2], s[mt][0][2 * i2 + 1]), fmaxf(s[mt][1][2 * i2], s[mt][1][2 * i2 + 1]));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            mx = fmaxf(mx, m_run[mt][i2]);
-            const float f = m_run[mt][i2] == -INFINITY ? 0.f : ex2(m_run[mt][i2] - mx);
-            m_run[mt][i2] = mx;
-            l_run[mt][i2] *= f;
-#pragma unroll
-            for (int j = 0; j < kNt; ++j) {
-              o[mt][j][2 * i2] *= f * fr;
-              o[mt][j][2 * i2 + 1] *= f * fr;
-            }
-          }
-      }
-      const float vr = vs / ref;
-      uint4 pa[MT];
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        float p[2][4];
-#pragma unroll
-        for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float m = m_run[mt][e >> 1];
-            p[nt][e] = ex2(s[mt][nt][e] - (m == -INFINITY ? 0.f : m));
-            l_run[mt][e >> 1] += p[nt][e];
-          }
-        pa[mt].x = pack_half2(p[0][0] * vr, p[0][1] * vr);
-        pa[mt].y = pack_half2(p[0][2] * vr, p[0][3] * vr);
-        pa[mt].z = pack_half2(p[1][0] * vr, p[1][1] * vr);
-        pa[mt].w = pack_half2(p[1][2] * vr, p[1][3] * vr);
-      }
-      // V rows 2c, 2c+1, 2c+8, 2c+9, D/8 codes from column (D/8) g
-      uint32_t vw[4][D / 32];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const int row = 2 * c + (t & 1) + (t >> 1) * 8;
-        if (D == 128) {
-          const uint4 w = lds128(v_unit + unit_off<D>(row, g));
-          vw[t][0] = w.x; vw[t][1] = w.y; vw[t][2 % (D / 32)] = w.z; vw[t][3 % (D / 32)] = w.w;
-        } else {
-          const uint2 w = lds64(v_unit + unit_off<D>(row, g >> 1) + (g & 1) * 8);
-          vw[t][0] = w.x; vw[t][1] = w.y;
-        }
-      }
-      bool bad = false;   // NaN codes among positions that some rows do not see
-      if (edge) {
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-          for (int w = 0; w < D / 32; ++w) {
-            const uint32_t x = vw[t][w] & 0x7f7f7f7fu;
-            bad = bad || ((x + 0x01010101u) & 0x80808080u) != 0;
-          }
-        bad = __any_sync(0xffffffffu, bad);
-      }
-#pragma unroll
-      for (int w = 0; w < D / 32; ++w) {
-        const uint32_t x0 = __byte_perm(vw[0][w], vw[1][w], 0x5140), x1 = __byte_perm(vw[0][w], vw[1][w], 0x7362);
-        const uint32_t y0 = __byte_perm(vw[2][w], vw[3][w], 0x5140), y1 = __byte_perm(vw[2][w], vw[3][w], 0x7362);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t xs = e < 2 ? x0 : x1, ys = e < 2 ? y0 : y1;
-          uint32_t b0 = e & 1 ? e4m3x2_hi(xs) : e4m3x2_lo(xs), b1 = e & 1 ? e4m3x2_hi(ys) : e4m3x2_lo(ys);
-          if (bad) {
-            // A NaN value reaches the rows that see its position and no other:
-            // a product of visibility and NaN-ness finds them.
-            const uint32_t n0 = nan_ones(b0), n1 = nan_ones(b1);
-            b0 = nan_zero(b0);
-            b1 = nan_zero(b1);
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              uint4 see;
-              uint32_t* sw = reinterpret_cast<uint32_t*>(&see);
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                sw[k] = (s[mt][k >> 1][2 * (k & 1)] != -INFINITY ? 0x3c00u : 0u) |
-                        (s[mt][k >> 1][2 * (k & 1) + 1] != -INFINITY ? 0x3c000000u : 0u);
-              float hit[4] = {0.f, 0.f, 0.f, 0.f};
-              mma_f16(hit, see, n0, n1);
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (hit[k] > 0.f) o[mt][w * 4 + e][k] = __int_as_float(0x7fc00000);
-            }
-          }
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) mma_f16(o[mt][w * 4 + e], pa[mt], b0, b1);
-        }
-      }
-    }
-    cp_async_wait<0>();
-    __syncthreads();
-
-    // ---- join the four warps
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int i2 = 0; i2 < 2; ++i2) {
-        float l = l_run[mt][i2];
-        l += __shfl_xor_sync(0xffffffffu, l, 1);
-        l += __shfl_xor_sync(0xffffffffu, l, 2);
-        const int r = mt * 16 + i2 * 8 + g;
-        if (c == 0) s_ml[warp * kRows + r] = make_float2(m_run[mt][i2], l);
-        // columns 2c and 2c + 1 of the n-tiles: d = kNt * 2c + j and kNt * (2c + 1) + j
-        float* dst = s_o + (warp * kRows + r) * L::kPitch + 2 * c * kNt;
-#pragma unroll
-        for (int j = 0; j < kNt; j += 4) {
-          *reinterpret_cast<float4*>(dst + j) = make_float4(o[mt][j][2 * i2] * ref, o[mt][j + 1][2 * i2] * ref,
-                                                            o[mt][j + 2][2 * i2] * ref, o[mt][j + 3][2 * i2] * ref);
-          *reinterpret_cast<float4*>(dst + kNt + j) =
-              make_float4(o[mt][j][2 * i2 + 1] * ref, o[mt][j + 1][2 * i2 + 1] * ref, o[mt][j + 2][2 * i2 + 1] * ref,
-                          o[mt][j + 3][2 * i2 + 1] * ref);
-        }
-      }
-    __syncthreads();
-    const bool whole = nt_ == tiles;
-    float* part = a.part + static_cast<int64_t>(2 * cta + (pos == lo ? 0 : 1)) * kRows * L::kPitch;
-    for (int x = tid; x < kRows * (D / 4); x += kAttnThreads) {
-      const int r = x / (D / 4), d = (x % (D / 4)) * 4;
-      const int R = row0 + r;
-      if (R >= rows_total) break;
-      float m = -INFINITY, l = 0.f;
-#pragma unroll
-      for (int w = 0; w < kAttnWarps; ++w) m = fmaxf(m, s_ml[w * kRows + r].x);
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      const float m0 = m == -INFINITY ? 0.f : m;
-#pragma unroll
-      for (int w = 0; w < kAttnWarps; ++w) {
-        const float2 ml = s_ml[w * kRows + r];
-        const float f = ex2(ml.x - m0);
-        const float4 t = *reinterpret_cast<const float4*>(s_o + (w * kRows + r) * L::kPitch + d);
-        l += ml.y * f;
-        v.x += t.x * f;
-        v.y += t.y * f;
-        v.z += t.z * f;
-        v.w += t.w * f;
-      }
-      if (whole) {
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const int n = R / a.G;
-        const int64_t row = (static_cast<int64_t>(b) * a.N + n) * a.Hq + h * a.G + (R - n * a.G);
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + (row * D + d) * 2) =
-            make_uint2(T::pack2(v.x * inv, v.y * inv), T::pack2(v.z * inv, v.w * inv));
-        if (a.lse && d == 0) a.lse[row] = l == 0.f ? -INFINITY : (m0 + log2f(l)) * kLn2;
-      } else {
-        *reinterpret_cast<float4*>(part + r * L::kPitch + d) = v;
-        if (d == 0) *reinterpret_cast<float2*>(part + r * L::kPitch + D) = make_float2(m, l);
-      }
-    }
-    __syncthreads();
   }
 }
 

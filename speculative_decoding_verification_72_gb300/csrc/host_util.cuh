@@ -79,12 +79,13 @@ struct SmemSet {
   inline static std::atomic<uint64_t> done{0};
 };
 
+// `most` bounds every later call's smem.
 template <auto Kern, typename... Args>
-cudaError_t launch_smem(int grid, int block, size_t smem, cudaStream_t stream, const Args&... args) {
+cudaError_t launch_smem(int grid, int block, size_t smem, size_t most, cudaStream_t stream, const Args&... args) {
   const int dev = current_device();
   const bool cached = dev >= 0 && dev < kMaxDevices;
   if (!cached || !(SmemSet<Kern>::done.load(std::memory_order_acquire) >> dev & 1)) {
-    const cudaError_t e = set_smem_attrs(Kern, static_cast<int>(smem));
+    const cudaError_t e = set_smem_attrs(Kern, static_cast<int>(most));
     if (e != cudaSuccess) return e;
     if (cached) SmemSet<Kern>::done.fetch_or(1ull << dev, std::memory_order_release);
   }

@@ -10,7 +10,7 @@
 #include "spec_verify.h"
 #include "host_util.cuh"
 #include "attn_q8.cuh"
-#include "attn_q8_cols.cuh"
+#include "attn_q8_rows.cuh"
 #include "attn_weights_q8.cuh"
 #include "kv_append_q8.cuh"
 #include "kv_evict_q8.cuh"
@@ -71,13 +71,13 @@ cudaError_t launch_append(const AppendArgs& a, int grid, int P, int D, cudaStrea
 
 // --------------------------------------------------------------- attention
 
-// Row blocks of 16 rows where all of a kv head's rows fit, else of 32. One block takes the column kernel.
-int attn_mt(int64_t rows) { return rows <= 16 ? 1 : 2; }
+// Rows of a block: all of a kv head's as columns where they are at most 32
+// (in one or two groups of 16), else blocks of 128 lanes. At 33 to 64 rows the
+// row kernel's lanes are half empty, but two column kernels' traffic would cost
+// as much again.
+int attn_block(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 128; }
 
-// CTAs an SM holds: two of either kernel (TMEM and shared memory; registers).
-int attn_grid_max() { return 2 * sm_count(); }
-
-constexpr int kAttnGridMost = 1024;   // what a workspace is sized for, whatever the device
+constexpr int kAttnGridMost = 320;   // CTAs a workspace is sized for: two an SM of 152, whatever the device
 
 // cuTensorMapEncodeTiled of the loaded driver.
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -113,14 +113,18 @@ bool code_map(const sv_q8_cache& c, void* codes, CUtensorMap* m) {
 template <typename T, int D, int MT>
 cudaError_t launch_join(const AttnArgs& a, int64_t items, cudaStream_t st) {
   const int64_t grid = items * 4 * MT + (a.status ? a.B : 0);
-  if (grid > INT32_MAX) return cudaErrorInvalidValue;
   return launch(attn_q8_combine_kernel<T, D, MT>, static_cast<int>(grid), kAttnThreads, 0, st, true, a);
 }
 
-template <typename T, int D, int MT>
-cudaError_t launch_attn(const AttnArgs& a, int64_t items, cudaStream_t st) {
-  const cudaError_t e = launch_smem<attn_q8_kernel<T, D, MT>>(a.grid, kAttnThreads, attn_smem_bytes<D, MT>(SV_MAX_TREE_NODES), st, a);
-  return e != cudaSuccess ? e : launch_join<T, D, MT>(a, items, st);
+template <typename T, int D, int NT>
+cudaError_t launch_rows(const sv_q8_cache& c, AttnArgs& a, int64_t items, cudaStream_t st) {
+  CUtensorMap k;
+  if (!code_map(c, c.k, &k)) return cudaErrorInvalidValue;
+  using L = RowLayout<D, NT>;
+  const int smem = L::bytes(std::min(a.N, 127 / a.G + 2), (a.N + 31) / 32);
+  if (2 * (smem + 1024) > 228 * 1024) a.grid = std::min(a.grid, sm_count());   // one CTA an SM
+  const cudaError_t e = launch_smem<attn_q8_rows_kernel<T, D, NT>>(a.grid, kRowThreads, smem, L::most(), st, k, a);
+  return e != cudaSuccess ? e : launch_join<T, D, 8>(a, items, st);
 }
 
 template <typename T, int D, int MT, int NT>
@@ -128,19 +132,19 @@ cudaError_t launch_cols(const sv_q8_cache& c, const AttnArgs& a, int64_t items, 
   CUtensorMap k, v;
   if (!code_map(c, c.k, &k) || !code_map(c, c.v, &v)) return cudaErrorInvalidValue;
   constexpr int kSmem = ColLayout<D, MT, NT>::bytes(1);   // at most 32 rows, so 32 nodes: one mask word
-  const cudaError_t e = launch_smem<attn_q8_cols_kernel<T, D, MT, NT>>(a.grid, ColLayout<D, MT, NT>::kThreads, kSmem, st, k, v, a);
+  const cudaError_t e = launch_smem<attn_q8_cols_kernel<T, D, MT, NT>>(a.grid, ColLayout<D, MT, NT>::kThreads, kSmem, kSmem, st, k, v, a);
   return e != cudaSuccess ? e : launch_join<T, D, MT>(a, items, st);
 }
 
 template <typename T, int D>
 cudaError_t launch_weights(const WeightArgs& a, int mt, cudaStream_t st) {
-  return mt == 1   ? launch_smem<attn_weights_q8_kernel<T, D, 1>>(a.grid, kAttnThreads, weight_smem_bytes<D, 1>(), st, a)
-         : mt == 2 ? launch_smem<attn_weights_q8_kernel<T, D, 2>>(a.grid, kAttnThreads, weight_smem_bytes<D, 2>(), st, a)
-                   : launch_smem<attn_weights_q8_kernel<T, D, 4>>(a.grid, kAttnThreads, weight_smem_bytes<D, 4>(), st, a);
+  return mt == 1   ? launch_smem<attn_weights_q8_kernel<T, D, 1>>(a.grid, kAttnThreads, weight_smem_bytes<D, 1>(), weight_smem_bytes<D, 1>(), st, a)
+         : mt == 2 ? launch_smem<attn_weights_q8_kernel<T, D, 2>>(a.grid, kAttnThreads, weight_smem_bytes<D, 2>(), weight_smem_bytes<D, 2>(), st, a)
+                   : launch_smem<attn_weights_q8_kernel<T, D, 4>>(a.grid, kAttnThreads, weight_smem_bytes<D, 4>(), weight_smem_bytes<D, 4>(), st, a);
 }
 
-size_t attn_ws_part_bytes(int mt, int D) {
-  return align_up(static_cast<size_t>(2) * kAttnGridMost * 16 * mt * (D + 4) * sizeof(float), kAlign);
+size_t attn_ws_part_bytes(int block, int D) {
+  return align_up(static_cast<size_t>(2) * kAttnGridMost * block * (D + 4) * sizeof(float), kAlign);
 }
 
 // ---------------------------------------------------------------- logprobs
@@ -212,8 +216,7 @@ sv_status spec_kv_append_q8(const sv_q8_cache* cache, const sv_rows* k_new, cons
 
 size_t spec_attention_q8_workspace_size(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int32_t D) {
   if (B < 0 || N < 1 || N > SV_MAX_TREE_NODES || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || (D != 64 && D != 128)) return 0;
-  const int mt = attn_mt(static_cast<int64_t>(N) * (Hq / Hkv));
-  return attn_ws_part_bytes(mt, D) + align_up(kAttnGridMost * sizeof(uint32_t), kAlign) +
+  return attn_ws_part_bytes(attn_block(static_cast<int64_t>(N) * (Hq / Hkv)), D) + align_up(kAttnGridMost * sizeof(uint32_t), kAlign) +
          align_up((static_cast<size_t>(B) + 2) * sizeof(int64_t), kAlign);
 }
 
@@ -250,31 +253,29 @@ sv_status spec_attention_q8(const sv_rows* q, int32_t dtype, const sv_q8_cache* 
   a.inv_g = ((1ull << 32) + a.G - 1) / a.G;
   const int64_t rows = static_cast<int64_t>(N) * a.G;
   if (rows > SV_MAX_TREE_NODES * 1024) return SV_ERR_INVALID_ARG;
-  const int mt = attn_mt(rows);
-  a.RB = static_cast<int32_t>((rows + 16 * mt - 1) / (16 * mt));
+  const int block = attn_block(rows);
+  a.RB = static_cast<int32_t>((rows + block - 1) / block);
   a.coef = static_cast<float>(static_cast<double>(sm_scale) * 1.4426950408889634);
   a.part = static_cast<float*>(workspace);
-  uint8_t* after = static_cast<uint8_t*>(workspace) + attn_ws_part_bytes(mt, cache->D);
-  const bool cols = rows <= 32;
-  a.failed = cols ? reinterpret_cast<uint32_t*>(after) : nullptr;
+  uint8_t* after = static_cast<uint8_t*>(workspace) + attn_ws_part_bytes(block, cache->D);
+  a.failed = reinterpret_cast<uint32_t*>(after);
   a.plan = reinterpret_cast<int64_t*>(after + align_up(kAttnGridMost * sizeof(uint32_t), kAlign));
   const int64_t items = static_cast<int64_t>(B) * cache->Hkv * a.RB;
-  const int tile = cols ? kColTile : kAttnTile;
-  const int64_t tiles = (static_cast<int64_t>(cache->max_pages) * cache->page_size + tile - 1) / tile;
-  if (items * 8 + B > INT32_MAX || cache->Hkv * a.RB * tiles > INT32_MAX) return SV_ERR_INVALID_ARG;
-  a.grid = static_cast<int32_t>(std::min<int64_t>({attn_grid_max(), kAttnGridMost, items * tiles}));
+  const int64_t tiles = (static_cast<int64_t>(cache->max_pages) * cache->page_size + kColTile - 1) / kColTile;
+  if (items * 32 + B > INT32_MAX || cache->Hkv * a.RB * tiles > INT32_MAX) return SV_ERR_INVALID_ARG;
+  a.grid = static_cast<int32_t>(std::min<int64_t>({2 * sm_count(), kAttnGridMost, items * tiles}));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const sv_q8_cache& c = *cache;
+  const bool wide = c.D == 128;
   cudaError_t e;
-  if (!cols)
-    e = dtype == SV_BF16 ? (c.D == 128 ? launch_attn<TypeBf16, 128, 2>(a, items, st) : launch_attn<TypeBf16, 64, 2>(a, items, st))
-                         : (c.D == 128 ? launch_attn<TypeF16, 128, 2>(a, items, st) : launch_attn<TypeF16, 64, 2>(a, items, st));
-  else if (dtype == SV_BF16)
-    e = c.D == 128 ? (mt == 1 ? launch_cols<TypeBf16, 128, 1, 2>(c, a, items, st) : launch_cols<TypeBf16, 128, 2, 2>(c, a, items, st))
-                   : (mt == 1 ? launch_cols<TypeBf16, 64, 1, 2>(c, a, items, st) : launch_cols<TypeBf16, 64, 2, 2>(c, a, items, st));
+  if (dtype == SV_BF16)
+    e = block == 128  ? (wide ? launch_rows<TypeBf16, 128, 2>(c, a, items, st) : launch_rows<TypeBf16, 64, 2>(c, a, items, st))
+        : block == 32 ? (wide ? launch_cols<TypeBf16, 128, 2, 2>(c, a, items, st) : launch_cols<TypeBf16, 64, 2, 2>(c, a, items, st))
+                      : (wide ? launch_cols<TypeBf16, 128, 1, 2>(c, a, items, st) : launch_cols<TypeBf16, 64, 1, 2>(c, a, items, st));
   else
-    e = c.D == 128 ? (mt == 1 ? launch_cols<TypeF16, 128, 1, 3>(c, a, items, st) : launch_cols<TypeF16, 128, 2, 3>(c, a, items, st))
-                   : (mt == 1 ? launch_cols<TypeF16, 64, 1, 3>(c, a, items, st) : launch_cols<TypeF16, 64, 2, 3>(c, a, items, st));
+    e = block == 128  ? (wide ? launch_rows<TypeF16, 128, 3>(c, a, items, st) : launch_rows<TypeF16, 64, 3>(c, a, items, st))
+        : block == 32 ? (wide ? launch_cols<TypeF16, 128, 2, 3>(c, a, items, st) : launch_cols<TypeF16, 64, 2, 3>(c, a, items, st))
+                      : (wide ? launch_cols<TypeF16, 128, 1, 3>(c, a, items, st) : launch_cols<TypeF16, 64, 1, 3>(c, a, items, st));
   return done(e);
 }
 
@@ -369,7 +370,7 @@ sv_status spec_kv_evict_q8(const sv_q8_cache* cache, int32_t B, const int32_t* s
   a.n_keys = std::min(S, kEvMaxKeys);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const size_t smem = (kEvBins + static_cast<size_t>(kEvMaxKeys)) * sizeof(uint32_t);
-  cudaError_t e = launch_smem<kv_evict_select_kernel>(static_cast<int>(bh), kEvThreads, smem, st, a);
+  cudaError_t e = launch_smem<kv_evict_select_kernel>(static_cast<int>(bh), kEvThreads, smem, smem, st, a);
   if (e != cudaSuccess) return SV_ERR_CUDA;
   const int grid = static_cast<int>(bh * groups);
   return done(cache->D == 128 ? launch(kv_evict_move_kernel<128>, grid, kMvWarps * 32, 0, st, true, a)
