@@ -39,7 +39,7 @@ struct AttnArgs {
   uint64_t inv_g;              // ceil(2^32 / G): r / G = r * inv_g >> 32 for r * G < 2^32
   float coef;                  // sm_scale * log2(e)
   float* part;                 // [2 grid][rows of a block][D + 4]: o, then (max, sum) in the pad
-  int64_t* plan;               // [B + 1] tile offsets of the requests, then the CTAs in use
+  int32_t* plan;               // [B + 1] tile offsets of the requests, and their total
   uint32_t* failed;            // [grid]: whether a wait of the CTA gave up, or nullptr
   int32_t grid;
 };
@@ -70,68 +70,91 @@ __device__ __forceinline__ int attn_tiles(const AttnReq& r) {
   return max(1, (r.len + kTile - 1) / kTile);
 }
 
-// The line of tiles: tiles_of(b) for each of ipr items of every request b.
+// The line of tiles: tiles_of(b) for each of ipr items of every request b. The
+// entry point sees to it that it has fewer than 2^31.
 struct AttnLine {
-  int64_t total;   // tiles of all requests (one item each)
-  int64_t off;     // tiles before request b
+  int32_t total;   // tiles of all requests (one item each)
+  int32_t off;     // tiles before request b
   int32_t b;
 };
 
+// Equal ranges of TT tiles for n CTAs, the first TT % n of them one longer.
+struct AttnRanges {
+  int32_t n, per, more;
+  __device__ __forceinline__ AttnRanges(int32_t grid, int32_t TT) {
+    n = TT < grid ? TT : grid;
+    per = n > 0 ? TT / n : 0;
+    more = TT - per * n;
+  }
+  __device__ __forceinline__ int32_t begin(int32_t cta) const { return cta * per + min(cta, more); }
+  __device__ __forceinline__ int32_t cta_of(int32_t tile) const {   // tile < TT
+    const int32_t first = more * (per + 1);
+    return tile < first ? tile / (per + 1) : more + (tile - first) / per;
+  }
+};
+
 // CTA-wide: sums the requests' tiles, and finds the request that holds the
-// first tile of the CTA's range, first_of(total); offsets go to `store` if given.
-// The result is in shared memory.
-template <int kThreads, typename F, typename G>
-__device__ __forceinline__ void attn_scan(int B, F&& tiles_of, G&& first_of, AttnLine* s_line, int64_t* s_warp, int64_t ipr,
-                                          int64_t* store) {
+// first tile of the CTA's range; offsets go to `store` if given. The result is
+// in shared memory.
+template <int kThreads, typename F>
+__device__ __forceinline__ AttnRanges attn_scan(int B, F&& tiles_of, int32_t grid, int32_t cta, AttnLine* s_line, int32_t* s_warp,
+                                                int32_t ipr, int32_t* store) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int64_t run = 0, off = 0;
-  int32_t t = 0;
-  auto chunk = [&](int c0) {   // off, t: of request c0 + tid
-    const int b = c0 + tid;
-    t = b < B ? tiles_of(b) : 0;
-    int64_t inc = t;
+  int32_t run = 0, off = 0, t = 0, total = 0;
+  AttnRanges ranges(grid, 0);
+  // One chunk of kThreads requests serves both passes; more take each again.
+  const int chunks = (B + kThreads - 1) / kThreads;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
+    for (int c = 0; c < chunks; ++c) {
+      if (pass == 0 || chunks > 1) {
+        const int b = c * kThreads + tid;
+        t = b < B ? tiles_of(b) : 0;
+        int32_t inc = t;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += up;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int32_t up = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += up;
+        }
+        __syncthreads();
+        if (lane == 31) s_warp[warp] = inc;
+        __syncthreads();
+        off = run + inc - t;
+#pragma unroll 1
+        for (int w = 0; w < kThreads / 32; ++w) {
+          const int32_t s = s_warp[w];
+          if (w < warp) off += s;
+          run += s;
+        }
+        if (store && pass == 0 && b < B) store[b] = off;
+      }
+      if (pass == 1) {
+        const int32_t find = ranges.begin(cta);
+        if (c * kThreads + tid < B && off * ipr <= find && find < (off + t) * ipr) {
+          s_line->off = off;
+          s_line->b = c * kThreads + tid;
+        }
+      }
     }
-    __syncthreads();
-    if (lane == 31) s_warp[warp] = inc;
-    __syncthreads();
-    off = run + inc - t;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) off += s_warp[w];
-      run += s_warp[w];
-    }
-    if (store && b < B) store[b] = off;
-  };
-  for (int c0 = 0; c0 < B; c0 += kThreads) chunk(c0);
-  const int64_t total = run, find = first_of(total);
-  for (int c0 = 0; c0 < B; c0 += kThreads) {
-    if (B > kThreads) {   // more requests than threads: the chunks again
-      if (c0 == 0) run = 0;
-      chunk(c0);
-    }
-    if (c0 + tid < B && off * ipr <= find && find < (off + t) * ipr) {
-      s_line->off = off;
-      s_line->b = c0 + tid;
+    if (pass == 0) {
+      total = run;
+      run = 0;
+      ranges = AttnRanges(grid, total * ipr);
     }
   }
   if (tid == 0) s_line->total = total;
   __syncthreads();
+  return ranges;
 }
-
-// CTAs that share TT tiles: all of the grid, or one per tile.
-__device__ __forceinline__ int64_t attn_ctas(int64_t grid, int64_t TT) { return TT < grid ? TT : grid; }
 
 // A CTA's walk over its range of the line: the pieces of items it has.
 struct AttnCursor {
-  int64_t pos, off;
+  int32_t pos, off;
   AttnReq rq;
   int b, tiles, h, rb, t0, n;   // request, its tiles, kv head, row block, first tile and tiles of the piece
 
-  __device__ void start(const AttnArgs& a, const AttnLine& line, int64_t lo) {
+  __device__ __forceinline__ void start(const AttnArgs& a, const AttnLine& line, int32_t lo) {
     pos = lo;
     off = line.off;
     b = line.b;
@@ -139,7 +162,7 @@ struct AttnCursor {
   }
   // The next piece (called while pos + n < hi); pos is then its first tile.
   template <int kTile>
-  __device__ void piece(const AttnArgs& a, int64_t hi, int ipr) {
+  __device__ __forceinline__ void piece(const AttnArgs& a, int32_t hi, int ipr) {
     rq = attn_req(a, b);
     tiles = attn_tiles<kTile>(rq);
     while (pos >= (off + tiles) * ipr) {
@@ -147,10 +170,10 @@ struct AttnCursor {
       rq = attn_req(a, ++b);
       tiles = attn_tiles<kTile>(rq);
     }
-    const int rel = static_cast<int>(pos - off * ipr);
+    const int rel = pos - off * ipr;
     const int item = rel / tiles;
     t0 = rel - item * tiles;
-    n = static_cast<int>(min(static_cast<int64_t>(tiles - t0), hi - pos));
+    n = min(tiles - t0, hi - pos);
     h = item / a.RB;
     rb = item - h * a.RB;
   }
@@ -257,12 +280,11 @@ __global__ void __launch_bounds__(kAttnThreads) attn_q8_combine_kernel(const Att
   const int ipr = a.c.Hkv * a.RB;
   grid_dep_wait();
   grid_dep_launch();
-  const int64_t join = blockIdx.x - static_cast<int64_t>(a.status ? a.B : 0);
+  const int join = static_cast<int>(blockIdx.x) - (a.status ? a.B : 0);
   const bool check = join < 0;
-  const int b = check ? blockIdx.x : static_cast<int>(join / (kRows / 4) / ipr);
-  const int64_t off = a.plan[b], total = a.plan[a.B], Ge = a.plan[a.B + 1];
-  const int64_t next = b + 1 < a.B ? a.plan[b + 1] : total;
-  const int64_t tiles = next - off, TT = total * ipr;
+  const int b = check ? blockIdx.x : join / (kRows / 4) / ipr;
+  const int off = a.plan[b], total = a.plan[a.B], next = a.plan[b + 1], tiles = next - off;
+  const AttnRanges ranges(a.grid, total * ipr);
   if (check) {
     const AttnReq rq = attn_req(a, b);
     bool bad_page = a.base[b] < 0 || (a.n_nodes && (a.n_nodes[b] < 0 || a.n_nodes[b] > a.N)) || rq.len != a.base[b] + rq.n;
@@ -276,8 +298,8 @@ __global__ void __launch_bounds__(kAttnThreads) attn_q8_combine_kernel(const Att
       }
     bool late = false;
     if (a.failed) {
-      const int64_t first = ((off * ipr + 1) * Ge - 1) / TT, last = (next * ipr * Ge - 1) / TT;
-      for (int64_t i = first + tid; i <= last; i += kAttnThreads) late = late || a.failed[i] != 0;
+      const int last = ranges.cta_of(next * ipr - 1);
+      for (int i = ranges.cta_of(off * ipr) + tid; i <= last; i += kAttnThreads) late = late || a.failed[i] != 0;
     }
     bad_page = __syncthreads_or(bad_page);
     bad_parent = __syncthreads_or(bad_parent);
@@ -286,24 +308,24 @@ __global__ void __launch_bounds__(kAttnThreads) attn_q8_combine_kernel(const Att
       a.status[b] = (bad_page ? SV_STATUS_BAD_PAGE : 0) | (bad_parent ? SV_STATUS_BAD_PARENT : 0) | (late ? SV_STATUS_TIMEOUT : 0);
     return;
   }
-  const int item = static_cast<int>(join / (kRows / 4) - static_cast<int64_t>(b) * ipr);
-  const int64_t t0 = off * ipr + item * tiles, t1 = t0 + tiles;
-  const int64_t c0 = ((t0 + 1) * Ge - 1) / TT, c1 = (t1 * Ge - 1) / TT;
+  const int item = join / (kRows / 4) - b * ipr;
+  const int t0 = off * ipr + item * tiles;
+  const int c0 = ranges.cta_of(t0), c1 = ranges.cta_of(t0 + tiles - 1);
   if (c0 == c1) return;   // one CTA had all of it
   const int h = item / a.RB, rb = item - h * a.RB;
-  const int slot0 = TT * c0 / Ge == t0 ? 0 : 1;
-  const int r = static_cast<int>(join % (kRows / 4)) * 4 + warp, R = rb * kRows + r;
+  const int slot0 = ranges.begin(c0) == t0 ? 0 : 1;
+  const int r = join % (kRows / 4) * 4 + warp, R = rb * kRows + r;
   if (R >= a.N * a.G) return;
   float m = -INFINITY, l = 0.f, v[kV];
 #pragma unroll
   for (int k = 0; k < kV; ++k) v[k] = 0.f;
-  for (int64_t i0 = c0; i0 <= c1; i0 += kJoinBatch) {
+  for (int i0 = c0; i0 <= c1; i0 += kJoinBatch) {
     float2 ml[kJoinBatch];
     float t[kJoinBatch][kV];
 #pragma unroll
     for (int k = 0; k < kJoinBatch; ++k) {
-      const int64_t i = min(i0 + k, c1);
-      const float* p = a.part + ((2 * i + (i == c0 ? slot0 : 0)) * kRows + r) * kPitch;
+      const int i = min(i0 + k, c1);
+      const float* p = a.part + static_cast<int64_t>((2 * i + (i == c0 ? slot0 : 0)) * kRows + r) * kPitch;
       ml[k] = *reinterpret_cast<const float2*>(p + D);
       if (kV == 4) {
         const float4 x = *reinterpret_cast<const float4*>(p + lane * 4);

@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(ColLayout<D, MT, NT>::kThreads, 2)
   constexpr int kSoft = 128 * MT;   // softmax threads
   extern __shared__ uint8_t raw[];
   __shared__ AttnLine s_line;
-  __shared__ int64_t s_warp[L::kThreads / 32];
+  __shared__ int32_t s_warp[L::kThreads / 32];
   __shared__ __align__(8) uint64_t s_bar[2 * L::kKs + 2 * L::kVs + 2 * L::kNb + 2 * L::kPb + 1];
   __shared__ uint32_t s_tmem, s_fail;
   const uint32_t smem0 = (smem_u32(raw) + 1023u) & ~1023u;
@@ -149,17 +149,10 @@ __global__ void __launch_bounds__(ColLayout<D, MT, NT>::kThreads, 2)
   grid_dep_launch();
   const int ipr = a.c.Hkv * a.RB;
   const int cta = blockIdx.x;
-  attn_scan<L::kThreads>(
-      a.B, [&](int r) { return attn_tiles<kColTile>(attn_req(a, r)); },
-      [&](int64_t total) { return total * ipr * cta / attn_ctas(a.grid, total * ipr); }, &s_line, s_warp, ipr,
-      cta == 0 ? a.plan : nullptr);
-  const int64_t TT = s_line.total * ipr;
-  const int64_t Ge = attn_ctas(a.grid, TT);
-  if (cta == 0 && tid == 0) {
-    a.plan[a.B] = s_line.total;
-    a.plan[a.B + 1] = Ge;
-  }
-  const int64_t lo = cta < Ge ? TT * cta / Ge : 0, hi = cta < Ge ? TT * (cta + 1) / Ge : 0;
+  const AttnRanges ranges = attn_scan<L::kThreads>(
+      a.B, [&](int r) { return attn_tiles<kColTile>(attn_req(a, r)); }, a.grid, cta, &s_line, s_warp, ipr, cta == 0 ? a.plan : nullptr);
+  if (cta == 0 && tid == 0) a.plan[a.B] = s_line.total;
+  const int lo = cta < ranges.n ? ranges.begin(cta) : 0, hi = cta < ranges.n ? ranges.begin(cta + 1) : 0;
 
   // Every role walks the same pieces; n counts tiles across them.
   AttnCursor cur;

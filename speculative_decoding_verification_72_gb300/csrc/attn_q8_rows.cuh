@@ -44,7 +44,7 @@ struct RowLayout {
   static constexpr int kOffK = kQBytes;
   static constexpr int kOffV = kOffK + kKs * kTileBytes;
   static constexpr int kOffMisc = kOffV + kVb * kVBytes;
-  static constexpr int kMiscBytes = kVb * 128 * (D / 32) * 4 + 1024 + 128 * 4;
+  static constexpr int kMiscBytes = kVb * 128 * (D / 32) * 4 + 1024 + 128 * 4 + 128 * 20;
   static int bytes(int nodes, int words) { return 1024 + kOffMisc + kMiscBytes + nodes * words * 4; }
   static int most() { return bytes(128, SV_MAX_TREE_NODES / 32); }
 };
@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kRowThreads, 2)
   constexpr int kPitch = AttnLayout<D>::kPitch;
   extern __shared__ uint8_t raw[];
   __shared__ AttnLine s_line;
-  __shared__ int64_t s_warp[kRowThreads / 32];
+  __shared__ int32_t s_warp[kRowThreads / 32];
   __shared__ __align__(8) uint64_t s_bar[2 * L::kKs + 2 * L::kVb + 4];
   __shared__ uint32_t s_tmem, s_fail, s_bad[2];   // s_bad: by V buffer, the last tile (+ 1) with NaN codes taken out
   const uint32_t smem0 = (smem_u32(raw) + 1023u) & ~1023u;
@@ -79,7 +79,8 @@ __global__ void __launch_bounds__(kRowThreads, 2)
   float4* s_sc = reinterpret_cast<float4*>(smem + L::kOffMisc);          // [8 tiles][8 pages]: ks, log2(vs / v0), v0 / vs, v0
   float* s_cq = reinterpret_cast<float*>(s_sc + 64);                     // [128]
   uint32_t* s_nan = reinterpret_cast<uint32_t*>(s_cq + 128);             // [kVb][128 tokens][D / 32]
-  uint32_t* s_anc = s_nan + L::kVb * 128 * (D / 32);                     // [nodes of the block][words]
+  uint32_t* s_vis = s_nan + L::kVb * 128 * (D / 32);                     // [128 rows][5]: tokens of an edge tile that a row sees
+  uint32_t* s_anc = s_vis + 128 * 5;                                     // [nodes of the block][words]
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t full_k = smem_u32(s_bar), empty_k = full_k + 8 * L::kKs, v_ready = empty_k + 8 * L::kKs;
@@ -112,17 +113,10 @@ __global__ void __launch_bounds__(kRowThreads, 2)
   grid_dep_launch();
   const int ipr = a.c.Hkv * a.RB;
   const int cta = blockIdx.x;
-  attn_scan<kRowThreads>(
-      a.B, [&](int r) { return attn_tiles<kColTile>(attn_req(a, r)); },
-      [&](int64_t total) { return total * ipr * cta / attn_ctas(a.grid, total * ipr); }, &s_line, s_warp, ipr,
-      cta == 0 ? a.plan : nullptr);
-  const int64_t TT = s_line.total * ipr;
-  const int64_t Ge = attn_ctas(a.grid, TT);
-  if (cta == 0 && tid == 0) {
-    a.plan[a.B] = s_line.total;
-    a.plan[a.B + 1] = Ge;
-  }
-  const int64_t lo = cta < Ge ? TT * cta / Ge : 0, hi = cta < Ge ? TT * (cta + 1) / Ge : 0;
+  const AttnRanges ranges = attn_scan<kRowThreads>(
+      a.B, [&](int r) { return attn_tiles<kColTile>(attn_req(a, r)); }, a.grid, cta, &s_line, s_warp, ipr, cta == 0 ? a.plan : nullptr);
+  if (cta == 0 && tid == 0) a.plan[a.B] = s_line.total;
+  const int lo = cta < ranges.n ? ranges.begin(cta) : 0, hi = cta < ranges.n ? ranges.begin(cta + 1) : 0;
   AttnCursor cur;   // every role walks the same pieces; n counts tiles across them
   cur.start(a, s_line, lo);
   uint32_t n = 0;
@@ -247,12 +241,13 @@ __global__ void __launch_bounds__(kRowThreads, 2)
         const uint32_t vb = n % L::kVb;
         if (n >= L::kVb) wait_or_fail(v_free + 8 * vb, (n / L::kVb - 1) & 1, fail);
         const bool edge = (cur.t0 + i + 1) * kColTile > cur.rq.base;
+        if (edge) {
+          // NaN codes of nodes, which not every row may see: taken out, noted by column
 #pragma unroll
-        for (int it = 0; it < kIts; ++it) {
-          const int row = it * kStep + r0;
-          uint32_t* w = reinterpret_cast<uint32_t*>(&v[it]);
-          if (edge && (cur.t0 + i) * kColTile + row >= cur.rq.base) {
-            // NaN codes of nodes, which not every row may see: taken out, noted by column
+          for (int it = 0; it < kIts; ++it) {
+            const int row = it * kStep + r0;
+            if ((cur.t0 + i) * kColTile + row < cur.rq.base) continue;
+            uint32_t* w = reinterpret_cast<uint32_t*>(&v[it]);
             uint32_t cols = 0;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -263,14 +258,20 @@ __global__ void __launch_bounds__(kRowThreads, 2)
             reinterpret_cast<uint16_t*>(s_nan)[(vb * 128 + row) * (D / 16) + ch] = static_cast<uint16_t>(cols);
             if (cols) *const_cast<volatile uint32_t*>(&s_bad[vb]) = n + 1;
           }
-          // d = 16 ch ..: two 16-byte chunks of block ch / 4 (64 columns a block), odd blocks' stores in the other order
-          uint8_t* dst = smem + L::kOffV + vb * L::kVBytes + (ch >> 2) * 16384 + row * 128;
-          const int c0 = (ch & 3) * 2;
-          const uint4 x = make_uint4(e4m3x2_lo(w[0]), e4m3x2_hi(w[0]), e4m3x2_lo(w[1]), e4m3x2_hi(w[1]));
-          const uint4 y = make_uint4(e4m3x2_lo(w[2]), e4m3x2_hi(w[2]), e4m3x2_lo(w[3]), e4m3x2_hi(w[3]));
-          const bool odd = ch >> 2 & 1;
-          *reinterpret_cast<uint4*>(dst + (((c0 + odd) ^ (row & 7)) << 4)) = odd ? y : x;
-          *reinterpret_cast<uint4*>(dst + (((c0 + !odd) ^ (row & 7)) << 4)) = odd ? x : y;
+        }
+        // d = 16 ch ..: two 16-byte chunks of block ch / 4 (64 columns a block), odd blocks' stores in the other order;
+        // row & 7 is the same for all of a thread's rows
+        uint8_t* dst = smem + L::kOffV + vb * L::kVBytes + (ch >> 2) * 16384 + r0 * 128;
+        const bool odd = ch >> 2 & 1;
+        const int c0 = (ch & 3) * 2;
+        const int o1 = ((c0 + odd) ^ (r0 & 7)) << 4, o2 = ((c0 + !odd) ^ (r0 & 7)) << 4;
+#pragma unroll
+        for (int it = 0; it < kIts; ++it) {
+          const uint4 w = v[it];
+          const uint4 x = make_uint4(e4m3x2_lo(w.x), e4m3x2_hi(w.x), e4m3x2_lo(w.y), e4m3x2_hi(w.y));
+          const uint4 y = make_uint4(e4m3x2_lo(w.z), e4m3x2_hi(w.z), e4m3x2_lo(w.w), e4m3x2_hi(w.w));
+          *reinterpret_cast<uint4*>(dst + it * kStep * 128 + o1) = odd ? y : x;
+          *reinterpret_cast<uint4*>(dst + it * kStep * 128 + o2) = odd ? x : y;
         }
         fence_async_smem();
         mbar_arrive(v_ready + 8 * vb);
@@ -283,7 +284,7 @@ __global__ void __launch_bounds__(kRowThreads, 2)
     // A wait that gives up ends no loop here: these warps meet at barriers, so all
     // run on to the end (every later wait then returns at once), without meaning.
     const uint32_t t_s = tmem + (static_cast<uint32_t>(warp * 32) << 16), t_o = t_s + 128;
-    const int rows_total = a.N * a.G, words = (a.N + 31) / 32;
+    const int rows_total = a.N * a.G, words = (a.N + 31) / 32, boxes = kColTile >> a.c.page_shift;
     for (; cur.pos < hi; cur.pos += cur.n) {
       cur.piece<kColTile>(a, hi, ipr);
       const AttnReq rq = cur.rq;
@@ -291,33 +292,51 @@ __global__ void __launch_bounds__(kRowThreads, 2)
       const int Rg = row0 + tid, my_at = attn_node(a, Rg);
       const int node = Rg < rows_total && my_at < rq.n ? my_at : -1;
 
-      // ---- q as e4m3 terms, one warp a row at a time
+      // ---- q as e4m3 terms: D / 8 lanes a row, eight elements each, four loads of a warp in flight
       const uint8_t* q = a.q + cur.b * a.sqb + static_cast<int64_t>(cur.h) * a.G * a.sqh;
-#pragma unroll 4
-      for (int r = warp; r < 128; r += 4) {
-        const int R = row0 + r, at = attn_node(a, R);
-        const bool on = R < rows_total && at < rq.n;
-        float f[4] = {0.f, 0.f, 0.f, 0.f};
-        if (on && lane * 4 < D) T::load4(q + at * a.sqn + (R - at * a.G) * a.sqh + lane * 8, f);
-        const float m = warp_max(fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3]))));
-        const int e = m > 0.f ? static_cast<int>(__float_as_uint(m) >> 23) - 127 : 7;
-        const int x = min(max(7 - e, -126), 126);
-        const float up = a.coef < 0.f ? -exp2_int(x) : exp2_int(x);   // scores grow with S
-        if (lane * 4 < D) {
+      constexpr int kLpr = D / 8, kRpw = 32 / kLpr;
+      const int ql = lane % kLpr;
+#pragma unroll 1
+      for (int r0 = warp * 32; r0 < warp * 32 + 32; r0 += 4 * kRpw) {
+        uint4 raw4[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) f[i] *= up;
+        for (int u = 0; u < 4; ++u) {
+          const int R = row0 + r0 + u * kRpw + lane / kLpr, at = attn_node(a, R);
+          raw4[u] = make_uint4(0, 0, 0, 0);
+          if (R < rows_total && at < rq.n)
+            raw4[u] = *reinterpret_cast<const uint4*>(q + at * a.sqn + (R - at * a.G) * a.sqh + ql * 16);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int r = r0 + u * kRpw + lane / kLpr;
+          float f[8];
+          T::load8(&raw4[u], f);
+          float m = 0.f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(f[i]));
+#pragma unroll
+          for (int o = kLpr / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+          const int e = m > 0.f ? static_cast<int>(__float_as_uint(m) >> 23) - 127 : 7;
+          const int x = min(max(7 - e, -126), 126);
+          const float up = a.coef < 0.f ? -exp2_int(x) : exp2_int(x);   // scores grow with S
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] *= up;
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
-            const uint32_t w = e4m3_pack4(f[0], f[1], f[2], f[3]);
-            const float2 x0 = half2_bits(e4m3x2_lo(w)), x1 = half2_bits(e4m3x2_hi(w));
-            f[0] -= x0.x;
-            f[1] -= x0.y;
-            f[2] -= x1.x;
-            f[3] -= x1.y;
-            *reinterpret_cast<uint32_t*>(smem + t * L::kTileBytes + unit_off<D>(r, lane >> 2) + (lane & 3) * 4) = w;
+            uint32_t w[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              w[k] = e4m3_pack4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
+              const float2 x0 = half2_bits(e4m3x2_lo(w[k])), x1 = half2_bits(e4m3x2_hi(w[k]));
+              f[4 * k] -= x0.x;
+              f[4 * k + 1] -= x0.y;
+              f[4 * k + 2] -= x1.x;
+              f[4 * k + 3] -= x1.y;
+            }
+            *reinterpret_cast<uint2*>(smem + t * L::kTileBytes + unit_off<D>(r, ql >> 1) + (ql & 1) * 8) = make_uint2(w[0], w[1]);
           }
+          if (ql == 0) s_cq[r] = m == INFINITY ? __int_as_float(0x7fc00000) : exp2_int(-x) * fabsf(a.coef);
         }
-        if (lane == 0) s_cq[r] = m == INFINITY ? __int_as_float(0x7fc00000) : exp2_int(-x) * fabsf(a.coef);
       }
       const bool tail = (cur.t0 + cur.n) * kColTile > rq.base;
       if (tail && a.parents) {
@@ -357,15 +376,13 @@ __global__ void __launch_bounds__(kRowThreads, 2)
         wait_or_fail(s_ready, n & 1, fail);   // and every product before this S is done
         tc_fence_after();
         const float4* sc = s_sc + (n & 7) * 8;
-        uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
         bool whole_pages = true;
         if (!edge) {
-#pragma unroll
-          for (int g = 0; g < 8; ++g) whole_pages = whole_pages && sc[(g * 16) >> a.c.page_shift].z >= 0.f;
+#pragma unroll 1
+          for (int g = 0; g < boxes; ++g) whole_pages = whole_pages && sc[g].z >= 0.f;
         }
-        const bool masked = edge || !whole_pages;   // the same for every row
-        if (masked) {
-#pragma unroll
+        if (edge || !whole_pages) {   // the same for every row: what it does not see becomes -inf in S
+#pragma unroll 1
           for (int j = 0; j < 4; ++j) {
             const int m0 = tok0 + 32 * j - rq.base;   // the word's first token, as a node
             uint32_t bits = node < 0 ? 0u : 0xffffffffu;
@@ -377,31 +394,45 @@ __global__ void __launch_bounds__(kRowThreads, 2)
             }
             if (sc[(32 * j) >> a.c.page_shift].z < 0.f) bits &= 0xffff0000u;
             if (sc[(32 * j + 16) >> a.c.page_shift].z < 0.f) bits &= 0x0000ffffu;
-            vis[j] = bits;
+            s_vis[tid * 5 + j] = bits;
+#pragma unroll 1
+            for (int g = 2 * j; g < 2 * j + 2; ++g, bits >>= 16) {
+              uint32_t s[16];
+              tmem_ld16(t_s + g * 16, s);
+              tmem_ld_wait();
+              tmem_use(s);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) s[k] = bits >> k & 1 ? s[k] : 0xff800000u;
+              tmem_st16(t_s + g * 16, s);
+            }
           }
+          tmem_st_wait();
         }
         // ---- maximum
+        // A score's factor; 0 would make NaN of -inf.
+        auto factor = [&](float k) {
+          const float c = cq * k;
+          return c == 0.f ? 1e-30f : c;
+        };
         float top = -INFINITY;
         uint32_t w[2][16];
         tmem_ld16(t_s, w[0]);
+#pragma unroll 1
+        for (int g = 0; g < 8; g += 2) {
 #pragma unroll
-        for (int g = 0; g < 8; ++g) {
-          tmem_ld_wait();
-          tmem_use(w[g & 1]);
-          if (g < 7) tmem_ld16(t_s + (g + 1) * 16, w[(g + 1) & 1]);
-          uint32_t* s = w[g & 1];
-          if (masked) {
-            const uint32_t bits = vis[g >> 1] >> (16 * (g & 1));
+          for (int u = 0; u < 2; ++u) {
+            tmem_ld_wait();
+            tmem_use(w[u]);
+            tmem_ld16(t_s + ((g + u + 1) & 7) * 16, w[u ^ 1]);   // past the last, the first again
+            float mx[4];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) s[j] = bits >> j & 1 ? s[j] : 0xff800000u;
+            for (int j = 0; j < 4; ++j)
+              mx[j] = fmaxf(fmaxf(__uint_as_float(w[u][4 * j]), __uint_as_float(w[u][4 * j + 1])),
+                            fmaxf(__uint_as_float(w[u][4 * j + 2]), __uint_as_float(w[u][4 * j + 3])));
+            const float4 k = sc[((g + u) * 16) >> a.c.page_shift];
+            top = fmaxf(top, fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), factor(k.x), k.y));
           }
-          float mx = __uint_as_float(s[0]);
-#pragma unroll
-          for (int j = 1; j < 16; ++j) mx = fmaxf(mx, __uint_as_float(s[j]));
-          const float4 k = sc[(g * 16) >> a.c.page_shift];
-          top = fmaxf(top, mx == -INFINITY ? -INFINITY : fmaf(mx, cq * k.x, k.y));
         }
-        tmem_ld16(t_s, w[0]);
         const bool raise = top > m_run + kRowSlack || (m_run == -INFINITY && top > -INFINITY);
         if (__any_sync(0xffffffffu, raise)) {
           const float m_new = raise ? top : m_run;
@@ -423,31 +454,30 @@ __global__ void __launch_bounds__(kRowThreads, 2)
         }
         const float m0 = m_run == -INFINITY ? 0.f : m_run;
         // ---- exponentials: P over the columns of S that have been read
+#pragma unroll 1
+        for (int g = 0; g < 8; g += 2) {
 #pragma unroll
-        for (int g = 0; g < 8; ++g) {
-          tmem_ld_wait();
-          tmem_use(w[g & 1]);
-          if (g < 7) tmem_ld16(t_s + (g + 1) * 16, w[(g + 1) & 1]);
-          const uint32_t* s = w[g & 1];
-          const float4 k = sc[(g * 16) >> a.c.page_shift];
-          const float2 c2 = make_float2(cq * k.x, cq * k.x), b2 = make_float2(k.y - m0, k.y - m0);
-          uint32_t h[8];
-          float2 sum = make_float2(0.f, 0.f);
-          const uint32_t bits = masked ? vis[g >> 1] >> (16 * (g & 1)) : 0xffffu;
+          for (int u = 0; u < 2; ++u) {
+            tmem_ld_wait();
+            tmem_use(w[u]);
+            if (u == 0 || g < 6) tmem_ld16(t_s + (g + u + 1) * 16, w[u ^ 1]);
+            const uint32_t* s = w[u];
+            const float4 k = sc[((g + u) * 16) >> a.c.page_shift];
+            const float c = factor(k.x), b = k.y - m0;
+            const float2 c2 = make_float2(c, c), b2 = make_float2(b, b);
+            uint32_t h[8];
+            float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            float2 x = __ffma2_rn(make_float2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), c2, b2);
-            if (masked) {
-              if (!(bits >> (2 * j) & 1)) x.x = -INFINITY;
-              if (!(bits >> (2 * j + 1) & 1)) x.y = -INFINITY;
+            for (int j = 0; j < 8; ++j) {
+              const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), c2, b2);
+              const float2 p = make_float2(ex2(x.x), ex2(x.y));
+              sum = __fadd2_rn(sum, p);
+              h[j] = pack_half2(p.x, p.y);
             }
-            const float2 p = make_float2(ex2(x.x), ex2(x.y));
-            sum = __fadd2_rn(sum, p);
-            h[j] = pack_half2(p.x, p.y);
+            const float part = sum.x + sum.y;
+            l += part == 0.f ? 0.f : part * k.z;   // 0 where a missing page has no factor
+            tmem_st8(t_s + (g + u) * 8, h);
           }
-          const float part = sum.x + sum.y;
-          l += part == 0.f ? 0.f : part * k.z;   // 0 where a missing page has no factor
-          tmem_st8(t_s + g * 8, h);
         }
         if (i == 0) v0 = sc[0].w;
         if (edge) {   // NaN values among the nodes that this row sees
@@ -456,7 +486,7 @@ __global__ void __launch_bounds__(kRowThreads, 2)
           if (*const_cast<volatile uint32_t*>(&s_bad[vb]) == n + 1) {
 #pragma unroll 1
             for (int t = max(0, rq.base - tok0); t < min(kColTile, rq.len - tok0); ++t)
-              if (vis[t >> 5] >> (t & 31) & 1)
+              if (s_vis[tid * 5 + (t >> 5)] >> (t & 31) & 1)
 #pragma unroll
                 for (int j = 0; j < D / 32; ++j) nan_cols[j] |= s_nan[(vb * 128 + t) * (D / 32) + j];
           }

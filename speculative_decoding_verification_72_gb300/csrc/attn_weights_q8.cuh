@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 4 ? 3 : 4) attn_weights_q8
   uint4* s_q = reinterpret_cast<uint4*>(smem + kAttnWarps * kWtStages * kUnit);
   float* s_qs = reinterpret_cast<float*>(s_q + MT * kKs * 32);
   __shared__ AttnLine s_line;
-  __shared__ int64_t s_warp[kAttnWarps];
+  __shared__ int32_t s_warp[kAttnWarps];
 
   grid_dep_wait();
   grid_dep_launch();
@@ -70,32 +70,25 @@ __global__ void __launch_bounds__(kAttnThreads, MT == 4 ? 3 : 4) attn_weights_q8
   const int g = lane >> 2, c = lane & 3;
   const int H = a.c.Hkv, cta = blockIdx.x;
 
-  attn_scan<kAttnThreads>(
-      a.B, [&](int r) { return (weight_req(a, r).len + kAttnTile - 1) / kAttnTile; },
-      [&](int64_t total) {
-        const int64_t n = attn_ctas(a.grid, total * H);
-        return cta < n ? total * H * cta / n : 0;
-      },
-      &s_line, s_warp, H, nullptr);
-  const int64_t TT = s_line.total * H;
-  const int64_t Ge = attn_ctas(a.grid, TT);
+  const AttnRanges ranges = attn_scan<kAttnThreads>(
+      a.B, [&](int r) { return (weight_req(a, r).len + kAttnTile - 1) / kAttnTile; }, a.grid, cta, &s_line, s_warp, H, nullptr);
   const uint32_t ring = smem_u32(smem) + warp * (kWtStages * kUnit);
 
-  if (cta < Ge) {
-    const int64_t lo = TT * cta / Ge, hi = TT * (cta + 1) / Ge;
+  if (cta < ranges.n) {
+    const int lo = ranges.begin(cta), hi = ranges.begin(cta + 1);
     int b = s_line.b;
-    int64_t off = s_line.off;
+    int off = s_line.off;
     AttnReq rq = weight_req(a, b);
-    for (int64_t pos = lo; pos < hi;) {
+    for (int pos = lo; pos < hi;) {
       int tiles = (rq.len + kAttnTile - 1) / kAttnTile;
       while (pos >= (off + tiles) * H) {
         off += tiles;
         rq = weight_req(a, ++b);
         tiles = (rq.len + kAttnTile - 1) / kAttnTile;
       }
-      const int rel = static_cast<int>(pos - off * H);
+      const int rel = pos - off * H;
       const int h = rel / tiles, t0 = rel - h * tiles;
-      const int nt_ = static_cast<int>(min(static_cast<int64_t>(tiles - t0), hi - pos));
+      const int nt_ = min(tiles - t0, hi - pos);
       const int32_t* path = a.path ? a.path + static_cast<int64_t>(b) * a.path_cols : nullptr;
       const float* sc = a.scores + (static_cast<int64_t>(b) * H + h) * a.S;
       float* out = a.out + (static_cast<int64_t>(b) * H + h) * a.S;

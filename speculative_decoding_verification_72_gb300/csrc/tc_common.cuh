@@ -110,13 +110,29 @@ __device__ __forceinline__ bool named_barrier_or(int id, int threads, bool p) {
   return r != 0;
 }
 
+// mbarrier wait that may sleep in hardware for about `ns` before it answers.
+__device__ __forceinline__ bool mbar_try_wait_for(uint32_t bar, uint32_t parity, uint32_t ns) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred P;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 P, [%1], %2, %3;\n\t"
+      "selp.b32 %0, 1, 0, P;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(ns)
+      : "memory");
+  return ok != 0;
+}
+
 // A bounded mbarrier wait that also gives up once another thread has: `fail`
-// is a word of shared memory.
-__device__ __forceinline__ bool wait_or_fail(uint32_t bar, uint32_t parity, volatile uint32_t* fail) {
-  if (mbar_try_wait(bar, parity)) return true;
+// is a word of shared memory. The loop is one function for all waits of a
+// kernel: these kernels' roles run different code at once, and their speed
+// hangs on all of it staying in the instruction cache.
+constexpr uint32_t kWaitSleepNs = 20000;
+
+static __device__ __noinline__ bool wait_or_fail_slow(uint32_t bar, uint32_t parity, volatile uint32_t* fail) {
   uint64_t prev = global_timer_ns(), spent = 0;
   for (uint32_t it = 1; it < kWaitIters; ++it) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait_for(bar, parity, kWaitSleepNs)) return true;
     if (*fail) return false;
     const uint64_t now = global_timer_ns();
     const uint64_t gap = now - prev;
@@ -126,6 +142,10 @@ __device__ __forceinline__ bool wait_or_fail(uint32_t bar, uint32_t parity, vola
   }
   *fail = 1;
   return false;
+}
+
+__device__ __forceinline__ bool wait_or_fail(uint32_t bar, uint32_t parity, volatile uint32_t* fail) {
+  return mbar_try_wait_for(bar, parity, kWaitSleepNs) || wait_or_fail_slow(bar, parity, fail);
 }
 
 }  // namespace sv

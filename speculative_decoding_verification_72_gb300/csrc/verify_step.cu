@@ -217,7 +217,7 @@ sv_status spec_kv_append_q8(const sv_q8_cache* cache, const sv_rows* k_new, cons
 size_t spec_attention_q8_workspace_size(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int32_t D) {
   if (B < 0 || N < 1 || N > SV_MAX_TREE_NODES || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || (D != 64 && D != 128)) return 0;
   return attn_ws_part_bytes(attn_block(static_cast<int64_t>(N) * (Hq / Hkv)), D) + align_up(kAttnGridMost * sizeof(uint32_t), kAlign) +
-         align_up((static_cast<size_t>(B) + 2) * sizeof(int64_t), kAlign);
+         align_up((static_cast<size_t>(B) + 1) * sizeof(int32_t), kAlign);
 }
 
 sv_status spec_attention_q8(const sv_rows* q, int32_t dtype, const sv_q8_cache* cache, int32_t B, int32_t N, int32_t Hq,
@@ -259,10 +259,10 @@ sv_status spec_attention_q8(const sv_rows* q, int32_t dtype, const sv_q8_cache* 
   a.part = static_cast<float*>(workspace);
   uint8_t* after = static_cast<uint8_t*>(workspace) + attn_ws_part_bytes(block, cache->D);
   a.failed = reinterpret_cast<uint32_t*>(after);
-  a.plan = reinterpret_cast<int64_t*>(after + align_up(kAttnGridMost * sizeof(uint32_t), kAlign));
+  a.plan = reinterpret_cast<int32_t*>(after + align_up(kAttnGridMost * sizeof(uint32_t), kAlign));
   const int64_t items = static_cast<int64_t>(B) * cache->Hkv * a.RB;
   const int64_t tiles = (static_cast<int64_t>(cache->max_pages) * cache->page_size + kColTile - 1) / kColTile;
-  if (items * 32 + B > INT32_MAX || cache->Hkv * a.RB * tiles > INT32_MAX) return SV_ERR_INVALID_ARG;
+  if (items * 32 + B > INT32_MAX || items * tiles > INT32_MAX) return SV_ERR_INVALID_ARG;
   a.grid = static_cast<int32_t>(std::min<int64_t>({2 * sm_count(), kAttnGridMost, items * tiles}));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const sv_q8_cache& c = *cache;
@@ -319,7 +319,7 @@ sv_status spec_attention_weights_q8(const sv_rows* q, int32_t dtype, const float
   const int mt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
   const int64_t items = static_cast<int64_t>(B) * cache->Hkv;
   const int64_t tiles = (static_cast<int64_t>(cache->max_pages) * cache->page_size + kAttnTile - 1) / kAttnTile;
-  if (items > INT32_MAX || cache->Hkv * tiles > INT32_MAX) return SV_ERR_INVALID_ARG;
+  if (items > INT32_MAX || items * tiles > INT32_MAX) return SV_ERR_INVALID_ARG;
   a.grid = static_cast<int32_t>(std::min<int64_t>(sm_count() * (mt == 4 ? 3 : 4), items * tiles));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (dtype == SV_BF16)
