@@ -12,15 +12,20 @@
 // on its way from global to shared memory. MMA time per tile: 512 clocks for
 // S (two terms at twice f16's rate) and 512 for P V.
 //
-// Lane = row makes the softmax a thread's own: it reads its row of S from TMEM
-// twice (maximum, then exponentials), writes P over the part of S that it has
-// read, and keeps maximum and sum in registers. O is rescaled in TMEM only when
-// a row's maximum has risen by more than 2^8, by a vote of its warp.
+// Lane = row keeps the softmax within a thread, or two: two groups of four
+// warps take 64 tokens of a tile each, so that a row's exponentials are shared
+// by two threads (at one thread a row they were 2250 of 6000 clocks a tile).
+// A thread reads its half row of S twice: for the maximum, on which the CTA
+// votes (only if a score is more than 2^8 above its row's running maximum do
+// maxima rise and is O rescaled in TMEM), and for the exponentials, which it
+// writes over the part of S that it has read. Holding P in registers between
+// one pass and the vote instead took 88 registers and more a thread, and two
+// CTAs leave 72.
 //
 // S and P share TMEM columns, so within a CTA S, softmax and P V of a tile
 // follow each other; two CTAs an SM fill each other's gaps.
 //
-// Warps 0-3: softmax. 4-7: V. 8: TMA (K) and the pages' scales. 9: MMA.
+// Warps 0-7: softmax. 8-11: V. 12: TMA (K) and the pages' scales. 13: MMA.
 // Masks, NaN codes, scales, work split and join as in attn_q8_cols.cuh; here
 // the rows that see a NaN code note its column in registers.
 #pragma once
@@ -31,7 +36,8 @@
 
 namespace sv {
 
-constexpr int kRowThreads = 320;
+constexpr int kRowThreads = 448;
+constexpr int kRowSoft = 256;          // softmax threads
 constexpr int kRowTmem = 256;
 constexpr float kRowSlack = 8.f;
 
@@ -44,7 +50,7 @@ struct RowLayout {
   static constexpr int kOffK = kQBytes;
   static constexpr int kOffV = kOffK + kKs * kTileBytes;
   static constexpr int kOffMisc = kOffV + kVb * kVBytes;
-  static constexpr int kMiscBytes = kVb * 128 * (D / 32) * 4 + 1024 + 128 * 4 + 128 * 20;
+  static constexpr int kMiscBytes = kVb * 128 * (D / 32) * 4 + 1024 + 128 * 4 + 256 * 12 + 256 * 4;
   static int bytes(int nodes, int words) { return 1024 + kOffMisc + kMiscBytes + nodes * words * 4; }
   static int most() { return bytes(128, SV_MAX_TREE_NODES / 32); }
 };
@@ -79,8 +85,9 @@ __global__ void __launch_bounds__(kRowThreads, 2)
   float4* s_sc = reinterpret_cast<float4*>(smem + L::kOffMisc);          // [8 tiles][8 pages]: ks, log2(vs / v0), v0 / vs, v0
   float* s_cq = reinterpret_cast<float*>(s_sc + 64);                     // [128]
   uint32_t* s_nan = reinterpret_cast<uint32_t*>(s_cq + 128);             // [kVb][128 tokens][D / 32]
-  uint32_t* s_vis = s_nan + L::kVb * 128 * (D / 32);                     // [128 rows][5]: tokens of an edge tile that a row sees
-  uint32_t* s_anc = s_vis + 128 * 5;                                     // [nodes of the block][words]
+  uint32_t* s_vis = s_nan + L::kVb * 128 * (D / 32);                     // [256][3]: tokens of an edge tile that a half row sees
+  float* s_half = reinterpret_cast<float*>(s_vis + 256 * 3);             // [256]
+  uint32_t* s_anc = reinterpret_cast<uint32_t*>(s_half + 256);           // [nodes of the block][words]
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t full_k = smem_u32(s_bar), empty_k = full_k + 8 * L::kKs, v_ready = empty_k + 8 * L::kKs;
@@ -97,13 +104,13 @@ __global__ void __launch_bounds__(kRowThreads, 2)
       mbar_init(v_free + 8 * i, 1);
     }
     mbar_init(s_ready, 1);
-    mbar_init(p_ready, 128);
+    mbar_init(p_ready, kRowSoft);
     mbar_init(o_done, 1);
-    mbar_init(q_ready, 128);
+    mbar_init(q_ready, kRowSoft);
     fence_barrier_init();
   }
-  if (warp == 9) tmem_alloc(smem_u32(&s_tmem), kRowTmem);
-  if (warp == 8 && lane == 0) tma_prefetch_map(&k_map);
+  if (warp == 13) tmem_alloc(smem_u32(&s_tmem), kRowTmem);
+  if (warp == 12 && lane == 0) tma_prefetch_map(&k_map);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -122,7 +129,7 @@ __global__ void __launch_bounds__(kRowThreads, 2)
   uint32_t n = 0;
   volatile uint32_t* fail = &s_fail;
 
-  if (warp == 8) {
+  if (warp == 12) {
     // ------------------------------------------------------------- K, scales
     bool ok = true;
     const int boxes = kColTile >> a.c.page_shift;
@@ -164,7 +171,7 @@ __global__ void __launch_bounds__(kRowThreads, 2)
         sc = sc1;
       }
     }
-  } else if (warp == 9) {
+  } else if (warp == 13) {
     // ------------------------------------------------------------------ MMA
     if (lane == 0) {
       constexpr uint32_t kSw = D == 128 ? 2 : 4, kSbo = 8 * D;
@@ -197,7 +204,7 @@ __global__ void __launch_bounds__(kRowThreads, 2)
           tc_fence_after();
 #pragma unroll
           for (int k = 0; k < kColTile / 16; ++k)
-            tc_mma_f16_ts(tmem + 128, tmem + 8 * k, tc_desc(smem0 + L::kOffV + vb * L::kVBytes + 2048 * k, 16384, 1024, 2), kIdO,
+            tc_mma_f16_ts(tmem + 128, tmem + (k & 3) * 8 + (k >> 2) * 64, tc_desc(smem0 + L::kOffV + vb * L::kVBytes + 2048 * k, 16384, 1024, 2), kIdO,
                           i > 0 || k > 0);
           tc_commit(v_free + 8 * vb);
           tc_commit(o_done);
@@ -207,11 +214,11 @@ __global__ void __launch_bounds__(kRowThreads, 2)
       }
     }
     __syncwarp();
-  } else if (warp >= 4) {
+  } else if (warp >= 8 && warp < 12) {
     // -------------------------------------------------------------------- V
     constexpr int kIts = kColTile * D / 16 / 128;   // 16-byte chunks a thread
     constexpr int kCpr = D / 16;                    // chunks a token
-    const int vt = tid - 128, r0 = vt / kCpr, ch = vt % kCpr;
+    const int vt = tid - kRowSoft, r0 = vt / kCpr, ch = vt % kCpr;
     constexpr int kStep = 128 / kCpr;               // tokens an iteration: 16 or 32
     uint4 v[kIts];
     for (; cur.pos < hi; cur.pos += cur.n) {
@@ -279,17 +286,19 @@ __global__ void __launch_bounds__(kRowThreads, 2)
         pages1 = pages2;
       }
     }
-  } else {
+  } else if (warp < 8) {
     // -------------------------------------------------------------- softmax
     // A wait that gives up ends no loop here: these warps meet at barriers, so all
     // run on to the end (every later wait then returns at once), without meaning.
-    const uint32_t t_s = tmem + (static_cast<uint32_t>(warp * 32) << 16), t_o = t_s + 128;
+    const int half = warp >> 2, row = tid & 127;   // the thread's 64 tokens of a tile, its row
+    const uint32_t t_lane = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t t_s = t_lane + half * 64, t_o = t_lane + 128 + half * (D / 2);
     const int rows_total = a.N * a.G, words = (a.N + 31) / 32, boxes = kColTile >> a.c.page_shift;
     for (; cur.pos < hi; cur.pos += cur.n) {
       cur.piece<kColTile>(a, hi, ipr);
       const AttnReq rq = cur.rq;
       const int row0 = cur.rb * 128, node0 = attn_node(a, row0);
-      const int Rg = row0 + tid, my_at = attn_node(a, Rg);
+      const int Rg = row0 + row, my_at = attn_node(a, Rg);
       const int node = Rg < rows_total && my_at < rq.n ? my_at : -1;
 
       // ---- q as e4m3 terms: D / 8 lanes a row, eight elements each, four loads of a warp in flight
@@ -297,7 +306,7 @@ __global__ void __launch_bounds__(kRowThreads, 2)
       constexpr int kLpr = D / 8, kRpw = 32 / kLpr;
       const int ql = lane % kLpr;
 #pragma unroll 1
-      for (int r0 = warp * 32; r0 < warp * 32 + 32; r0 += 4 * kRpw) {
+      for (int r0 = warp * 16; r0 < warp * 16 + 16; r0 += 4 * kRpw) {
         uint4 raw4[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -341,10 +350,10 @@ __global__ void __launch_bounds__(kRowThreads, 2)
       const bool tail = (cur.t0 + cur.n) * kColTile > rq.base;
       if (tail && a.parents) {
         const int nodes = min(attn_node(a, row0 + 127), a.N - 1) - node0 + 1;
-        for (int i = tid; i < nodes * words; i += 128) s_anc[i] = 0;
-        named_barrier_sync(1, 128);
+        for (int i = tid; i < nodes * words; i += kRowSoft) s_anc[i] = 0;
+        named_barrier_sync(1, kRowSoft);
         const int32_t* par = a.parents + static_cast<int64_t>(cur.b) * a.N;
-        for (int i = tid; i < nodes; i += 128) {
+        for (int i = tid; i < nodes; i += kRowSoft) {
           int m = node0 + i;
           while (m >= 0) {
             s_anc[i * words + (m >> 5)] |= 1u << (m & 31);
@@ -355,8 +364,8 @@ __global__ void __launch_bounds__(kRowThreads, 2)
       }
       fence_async_smem();
       mbar_arrive(q_ready);
-      named_barrier_sync(1, 128);
-      const float cq = s_cq[tid];
+      named_barrier_sync(1, kRowSoft);
+      const float cq = s_cq[row];
       // 32 bits of what the row sees of the nodes, from node 32 k
       auto sees = [&](int k) -> uint32_t {
         if (node < 0 || k < 0 || k >= words) return 0u;
@@ -365,7 +374,13 @@ __global__ void __launch_bounds__(kRowThreads, 2)
         return x < 0 ? 0u : x >= 31 ? 0xffffffffu : (2u << x) - 1u;
       };
 
-      float m_run = -INFINITY, l = 0.f, v0 = 1.f;
+      // A score's factor; 0 would make NaN of -inf.
+      auto factor = [&](float k) {
+        const float c = cq * k;
+        return c == 0.f ? 1e-30f : c;
+      };
+      float m_run = 0.f, l = 0.f, v0 = 1.f;   // m_run means something once the row has seen a token
+      bool seen = false;
       uint32_t nan_cols[D / 32];
 #pragma unroll
       for (int j = 0; j < D / 32; ++j) nan_cols[j] = 0;
@@ -377,14 +392,12 @@ __global__ void __launch_bounds__(kRowThreads, 2)
         tc_fence_after();
         const float4* sc = s_sc + (n & 7) * 8;
         bool whole_pages = true;
-        if (!edge) {
 #pragma unroll 1
-          for (int g = 0; g < boxes; ++g) whole_pages = whole_pages && sc[g].z >= 0.f;
-        }
+        for (int g = 0; g < boxes; ++g) whole_pages = whole_pages && sc[g].z >= 0.f;
         if (edge || !whole_pages) {   // the same for every row: what it does not see becomes -inf in S
 #pragma unroll 1
-          for (int j = 0; j < 4; ++j) {
-            const int m0 = tok0 + 32 * j - rq.base;   // the word's first token, as a node
+          for (int j = 0; j < 2; ++j) {
+            const int c0 = half * 64 + 32 * j, m0 = tok0 + c0 - rq.base;   // the word's first token, as a node
             uint32_t bits = node < 0 ? 0u : 0xffffffffu;
             if (edge && m0 > -32) {
               bits = m0 < 0 ? sees(0) << -m0 | (node < 0 ? 0u : (1u << -m0) - 1u)
@@ -392,9 +405,9 @@ __global__ void __launch_bounds__(kRowThreads, 2)
               const int left = rq.n - m0;   // nodes from the word's first on
               if (left < 32) bits &= left <= 0 ? 0u : (1u << left) - 1u;
             }
-            if (sc[(32 * j) >> a.c.page_shift].z < 0.f) bits &= 0xffff0000u;
-            if (sc[(32 * j + 16) >> a.c.page_shift].z < 0.f) bits &= 0x0000ffffu;
-            s_vis[tid * 5 + j] = bits;
+            if (sc[c0 >> a.c.page_shift].z < 0.f) bits &= 0xffff0000u;
+            if (sc[(c0 + 16) >> a.c.page_shift].z < 0.f) bits &= 0x0000ffffu;
+            s_vis[tid * 3 + j] = bits;
 #pragma unroll 1
             for (int g = 2 * j; g < 2 * j + 2; ++g, bits >>= 16) {
               uint32_t s[16];
@@ -409,39 +422,37 @@ __global__ void __launch_bounds__(kRowThreads, 2)
           tmem_st_wait();
         }
         // ---- maximum
-        // A score's factor; 0 would make NaN of -inf.
-        auto factor = [&](float k) {
-          const float c = cq * k;
-          return c == 0.f ? 1e-30f : c;
-        };
         float top = -INFINITY;
         uint32_t w[2][16];
         tmem_ld16(t_s, w[0]);
 #pragma unroll 1
-        for (int g = 0; g < 8; g += 2) {
+        for (int g = 0; g < 4; g += 2) {
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             tmem_ld_wait();
             tmem_use(w[u]);
-            tmem_ld16(t_s + ((g + u + 1) & 7) * 16, w[u ^ 1]);   // past the last, the first again
+            if (u == 0 || g < 2) tmem_ld16(t_s + (g + u + 1) * 16, w[u ^ 1]);
             float mx[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               mx[j] = fmaxf(fmaxf(__uint_as_float(w[u][4 * j]), __uint_as_float(w[u][4 * j + 1])),
                             fmaxf(__uint_as_float(w[u][4 * j + 2]), __uint_as_float(w[u][4 * j + 3])));
-            const float4 k = sc[((g + u) * 16) >> a.c.page_shift];
-            top = fmaxf(top, fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), factor(k.x), k.y));
+            const float4 k = sc[(half * 64 + (g + u) * 16) >> a.c.page_shift];
+            top = fmaxf(top, fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), factor(k.x), k.y - m_run));
           }
         }
-        const bool raise = top > m_run + kRowSlack || (m_run == -INFINITY && top > -INFINITY);
-        if (__any_sync(0xffffffffu, raise)) {
-          const float m_new = raise ? top : m_run;
-          const float f = m_run == -INFINITY ? 1.f : raise ? ex2(m_run - m_new) : 1.f;
-          m_run = m_new;
+        if (named_barrier_or(1, kRowSoft, top > kRowSlack || (!seen && top > -INFINITY))) {
+          s_half[tid] = top;
+          named_barrier_sync(1, kRowSoft);
+          top = fmaxf(top, s_half[tid ^ 128]);
+          const bool raise = seen ? top > kRowSlack : top > -INFINITY;
+          const float f = raise && seen ? ex2(-top) : 1.f;
+          if (raise) m_run += top;
+          seen = seen || raise;
           l *= f;
           if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll 1
-            for (int g = 0; g < D / 16; ++g) {
+            for (int g = 0; g < D / 32; ++g) {
               uint32_t o[16];
               tmem_ld16(t_o + g * 16, o);
               tmem_ld_wait();
@@ -452,30 +463,30 @@ __global__ void __launch_bounds__(kRowThreads, 2)
             }
           }
         }
-        const float m0 = m_run == -INFINITY ? 0.f : m_run;
         // ---- exponentials: P over the columns of S that have been read
+        tmem_ld16(t_s, w[0]);
 #pragma unroll 1
-        for (int g = 0; g < 8; g += 2) {
+        for (int g = 0; g < 4; g += 2) {
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             tmem_ld_wait();
             tmem_use(w[u]);
-            if (u == 0 || g < 6) tmem_ld16(t_s + (g + u + 1) * 16, w[u ^ 1]);
+            if (u == 0 || g < 2) tmem_ld16(t_s + (g + u + 1) * 16, w[u ^ 1]);
             const uint32_t* s = w[u];
-            const float4 k = sc[((g + u) * 16) >> a.c.page_shift];
-            const float c = factor(k.x), b = k.y - m0;
+            const float4 k = sc[(half * 64 + (g + u) * 16) >> a.c.page_shift];
+            const float c = factor(k.x), b = k.y - m_run;
             const float2 c2 = make_float2(c, c), b2 = make_float2(b, b);
             uint32_t h[8];
-            float2 sum = make_float2(0.f, 0.f);
+            float2 part = make_float2(0.f, 0.f);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), c2, b2);
               const float2 p = make_float2(ex2(x.x), ex2(x.y));
-              sum = __fadd2_rn(sum, p);
+              part = __fadd2_rn(part, p);
               h[j] = pack_half2(p.x, p.y);
             }
-            const float part = sum.x + sum.y;
-            l += part == 0.f ? 0.f : part * k.z;   // 0 where a missing page has no factor
+            const float total = part.x + part.y;
+            l += total == 0.f ? 0.f : total * k.z;   // 0 where a missing page has no factor
             tmem_st8(t_s + (g + u) * 8, h);
           }
         }
@@ -485,8 +496,8 @@ __global__ void __launch_bounds__(kRowThreads, 2)
           wait_or_fail(v_ready + 8 * vb, (n / L::kVb) & 1, fail);
           if (*const_cast<volatile uint32_t*>(&s_bad[vb]) == n + 1) {
 #pragma unroll 1
-            for (int t = max(0, rq.base - tok0); t < min(kColTile, rq.len - tok0); ++t)
-              if (s_vis[tid * 5 + (t >> 5)] >> (t & 31) & 1)
+            for (int t = max(half * 64, rq.base - tok0); t < min(half * 64 + 64, rq.len - tok0); ++t)
+              if (s_vis[tid * 3 + (t >> 5 & 1)] >> (t & 31) & 1)
 #pragma unroll
                 for (int j = 0; j < D / 32; ++j) nan_cols[j] |= s_nan[(vb * 128 + t) * (D / 32) + j];
           }
@@ -495,50 +506,61 @@ __global__ void __launch_bounds__(kRowThreads, 2)
         tc_fence_before();
         mbar_arrive(p_ready);
       }
-      // ---- the piece's rows
+      // ---- the piece's rows: the two halves' sums, D / 2 columns of O each
+      s_half[tid] = l;
       wait_or_fail(o_done, (n - 1) & 1, fail);
+      named_barrier_sync(1, kRowSoft);
+      l += s_half[tid ^ 128];
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) {   // a NaN that either half of the row saw
+        s_vis[tid] = nan_cols[j];
+        named_barrier_sync(1, kRowSoft);
+        nan_cols[j] |= s_vis[tid ^ 128];
+        named_barrier_sync(1, kRowSoft);
+      }
       tc_fence_after();
       const bool whole = cur.n == cur.tiles;
-      const float m_out = m_run == -INFINITY ? 0.f : m_run;
       if (node < 0) l = 0.f;
       const float f = l == 0.f ? 0.f : whole ? v0 / l : v0;
       const int64_t at = (static_cast<int64_t>(cur.b) * a.N + my_at) * a.Hq + cur.h * a.G + (Rg - my_at * a.G);
-      float* part = a.part + (static_cast<int64_t>(2 * cta + (cur.pos == lo ? 0 : 1)) * 128 + tid) * kPitch;
+      float* part = a.part + (static_cast<int64_t>(2 * cta + (cur.pos == lo ? 0 : 1)) * 128 + row) * kPitch;
       const bool mine = Rg < rows_total;
-#pragma unroll 1
-      for (int g = 0; g < D / 16; ++g) {
+#pragma unroll
+      for (int g = 0; g < D / 32; ++g) {
+        const int d0 = half * (D / 2) + g * 16;
         uint32_t o[16];
         tmem_ld16(t_o + g * 16, o);
         tmem_ld_wait();
         tmem_use(o);
         float y[16];
+        uint32_t bits = 0;
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) bits = (d0 >> 5) == k ? nan_cols[k] : bits;
+        bits >>= d0 & 31;
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           y[j] = f == 0.f ? 0.f : __uint_as_float(o[j]) * f;
-          uint32_t bits = 0;
-#pragma unroll
-          for (int k = 0; k < D / 32; ++k) bits = (g >> 1) == k ? nan_cols[k] : bits;
-          if (bits >> (16 * (g & 1) + j) & 1) y[j] = __int_as_float(0x7fc00000);
+          if (bits >> j & 1) y[j] = __int_as_float(0x7fc00000);
         }
         if (mine && whole) {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + (at * D + g * 16) * 2);
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + (at * D + d0) * 2);
           dst[0] = make_uint4(T::pack2(y[0], y[1]), T::pack2(y[2], y[3]), T::pack2(y[4], y[5]), T::pack2(y[6], y[7]));
           dst[1] = make_uint4(T::pack2(y[8], y[9]), T::pack2(y[10], y[11]), T::pack2(y[12], y[13]), T::pack2(y[14], y[15]));
         } else if (mine) {
 #pragma unroll
           for (int j = 0; j < 16; j += 4)
-            *reinterpret_cast<float4*>(part + g * 16 + j) = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
+            *reinterpret_cast<float4*>(part + d0 + j) = make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]);
         }
       }
-      if (mine) {
+      if (mine && half == 0) {
         if (whole) {
-          if (a.lse) a.lse[at] = l == 0.f ? -INFINITY : (m_out + log2f(l)) * kLn2;
+          if (a.lse) a.lse[at] = l == 0.f ? -INFINITY : (m_run + log2f(l)) * kLn2;
         } else {
-          *reinterpret_cast<float2*>(part + D) = make_float2(l == 0.f ? -INFINITY : m_out, l);
+          *reinterpret_cast<float2*>(part + D) = make_float2(l == 0.f ? -INFINITY : m_run, l);
         }
       }
       tc_fence_before();
-      named_barrier_sync(1, 128);   // s_cq and the ancestor sets are free for the next piece
+      named_barrier_sync(1, kRowSoft);   // the shared rows are free for the next piece
     }
   }
   __syncthreads();
@@ -549,7 +571,7 @@ __global__ void __launch_bounds__(kRowThreads, 2)
   }
   __syncthreads();
   if (tid == 0) a.failed[cta] = s_fail;
-  if (warp == 9) tmem_free(tmem, kRowTmem);
+  if (warp == 13) tmem_free(tmem, kRowTmem);
 }
 
 }  // namespace sv
