@@ -23,7 +23,6 @@ namespace sv {
 
 constexpr int kAttnThreads = 128;
 constexpr int kAttnWarps = 4;
-constexpr int kAttnTile = 64;        // tokens per CTA step: 16 per warp
 
 struct AttnArgs {
   const uint8_t* q;
@@ -189,82 +188,6 @@ template <int D>
 __device__ __forceinline__ uint32_t unit_off(int row, int ch) {
   if (D == 128) return row * 128 + ((ch ^ (row & 7)) << 4);
   return row * 64 + ((ch ^ ((row >> 1) & 3)) << 4);
-}
-
-// Q rows of a row block as A fragments of the permuted S product: per m-tile
-// and k step, 16 bytes a lane. Row r's factor (a power of two) goes to s_qs.
-template <typename T, int D, int MT, int TH>
-__device__ __forceinline__ void load_q_frags(const uint8_t* q, int64_t sqn, int64_t sqh, int rows_total, int row0, int G,
-                                             const int32_t* node_of, int n_lim, uint32_t* s_q, float* s_qs) {
-  constexpr int kKs = D / 16, kDpc = D / 4;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int rr = 0; rr < 16 * MT; rr += TH / 32) {
-    const int r = rr + warp;
-    const int R = row0 + r;
-    float f[4] = {0.f, 0.f, 0.f, 0.f};
-    const int d0 = lane * 4;
-    if (R < rows_total && d0 < D) {
-      int n = R / G;
-      const int g = R - n * G;
-      if (node_of) n = node_of[n];
-      if (n >= 0 && n < n_lim) T::load4(q + n * sqn + g * sqh + d0 * 2, f);
-    }
-    float m = fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3])));
-    m = warp_max(m);
-    // 2^x that brings the row's maximum into [2^14, 2^15)
-    const int e = m > 0.f ? static_cast<int>(__float_as_uint(m) >> 23) - 127 : 14;
-    const int x = min(max(14 - e, -126), 126);
-    const float up = exp2_int(x);
-    if (d0 < D) {
-      const int c = d0 / kDpc, ks = (d0 % kDpc) / 4, mt = r >> 4, hi = (r >> 3) & 1;
-      uint32_t* dst = s_q + (((mt * kKs + ks) * 32 + (r & 7) * 4 + c) << 2) + hi;
-      dst[0] = pack_half2(f[0] * up, f[1] * up);
-      dst[2] = pack_half2(f[2] * up, f[3] * up);
-    }
-    if (lane == 0) s_qs[r] = exp2_int(-x);
-  }
-}
-
-// S of 16 tokens (two n-tiles) for MT m-tiles from a unit of K codes in shared memory.
-template <int D, int MT>
-__device__ __forceinline__ void unit_scores(uint32_t k_unit, const uint4* s_q, int lane, float (&s)[MT][2][4]) {
-  constexpr int kKs = D / 16;
-  const int g = lane >> 2, c = lane & 3;
-  uint32_t kw[2][kKs];
-#pragma unroll
-  for (int nt = 0; nt < 2; ++nt) {
-    const int row = nt * 8 + g;
-    if (D == 128) {
-      const uint4 x = lds128(k_unit + unit_off<D>(row, 2 * c)), y = lds128(k_unit + unit_off<D>(row, 2 * c + 1));
-      kw[nt][0] = x.x; kw[nt][1] = x.y; kw[nt][2] = x.z; kw[nt][3] = x.w;
-      kw[nt][4 % kKs] = y.x; kw[nt][5 % kKs] = y.y; kw[nt][6 % kKs] = y.z; kw[nt][7 % kKs] = y.w;
-    } else {
-      const uint4 x = lds128(k_unit + unit_off<D>(row, c));
-      kw[nt][0] = x.x; kw[nt][1] = x.y; kw[nt][2] = x.z; kw[nt][3] = x.w;
-    }
-  }
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-    for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[mt][nt][i] = 0.f;
-#pragma unroll
-  for (int ks = 0; ks < kKs; ++ks) {
-    uint32_t b[2][2];
-#pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
-      b[nt][0] = e4m3x2_lo(kw[nt][ks]);
-      b[nt][1] = e4m3x2_hi(kw[nt][ks]);
-    }
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      const uint4 qa = s_q[(mt * kKs + ks) * 32 + lane];
-      mma_f16(s[mt][0], qa, b[0][0], b[0][1]);
-      mma_f16(s[mt][1], qa, b[1][0], b[1][1]);
-    }
-  }
 }
 
 // Joins the pieces of items that several CTAs shared, one warp a row; B more

@@ -14,10 +14,10 @@
 //   dx_j = (1 / T) [g (1{j = token} - p_j) - h p_j (ln p_j + H)] = p_j (a0 + a1 t'_j) + (g / T) 1{j = token}
 // with t' = (x - m) c - log2 s: one more pass over the row, no sums.
 //
-// Bound by memory: the forward pass reads each row once (the row is cut into
-// 32 KB segments, one CTA each; a thread keeps its eight 16-byte vectors in
-// registers, so maximum, sums and selection are passes over registers), the
-// gradient reads and writes it once.
+// Bound by memory: the forward pass reads each row once, the gradient reads and
+// writes it once. A row is cut into equal segments of at most 32 KB; a thread
+// has up to eight 16-byte vectors of one in registers, so maximum, sums and
+// selection are passes over registers.
 //
 // Top alternatives by (logit, lower index): a bound that at least n_top
 // elements of the segment reach is the n_top-th of the 32 maxima of groups of
@@ -33,6 +33,7 @@
 namespace sv {
 
 constexpr int kLpThreads = 256;
+constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kLpVecs = 8;                                   // 16-byte vectors per thread
 constexpr int kLpSegVecs = kLpThreads * kLpVecs;             // 32 KB
 constexpr int kLpMaxTop = SV_MAX_TOP_ALTERNATIVES;
@@ -47,9 +48,9 @@ struct LogprobArgs {
   const uint8_t* x;
   int64_t stride;              // bytes between rows
   const int32_t* tokens;       // [rows]
-  int32_t rows, V, segs, n_top;
+  int32_t rows, V, segs, per, n_top;   // per: vectors of a segment, a multiple of kLpThreads
   float c, inv_t;              // log2(e) / T, 1 / T
-  LpPartial* part;             // [rows, segs]
+  LpPartial* part;             // [rows, segs, kLpWarps]
   uint64_t* cand;              // [rows, segs, n_top] keys in descending order, 0 past the last
   float* logprob;              // [rows]
   float* entropy;              // [rows] or nullptr
@@ -89,12 +90,8 @@ __device__ __forceinline__ void lp_merge(float& m, float& s, float& w, float m2,
 // The 16-byte vectors of a row's hull that a thread holds: elements outside
 // the row read as -inf, and only vectors wholly inside it are read as vectors.
 template <int ES>
-__device__ __forceinline__ uint4 lp_load(const uint8_t* hull, int64_t vec, const uint8_t* row, const uint8_t* end) {
-  const uint8_t* p = hull + vec * 16;
+__device__ __noinline__ uint4 lp_load_edge(const uint8_t* p, const uint8_t* row, const uint8_t* end) {
   constexpr uint32_t kNeg = ES == 2 ? 0xff80ff80u : 0xff800000u;
-  if (p >= row && p + 16 <= end) return *reinterpret_cast<const uint4*>(p);
-  uint4 v = make_uint4(kNeg, kNeg, kNeg, kNeg);
-  if (p >= end) return v;
   uint32_t w[4] = {kNeg, kNeg, kNeg, kNeg};
 #pragma unroll
   for (int e = 0; e < 16 / ES; ++e) {
@@ -110,144 +107,275 @@ __device__ __forceinline__ uint4 lp_load(const uint8_t* hull, int64_t vec, const
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// A thread's vectors of a segment (per of them for the CTA): without tests
+// where the segment lies inside the row. Else what is not in the row reads as
+// masked; only whole vectors of it are read as vectors, and the one at each of
+// its edges, which one thread has, element by element.
+template <int ES>
+__device__ __forceinline__ void lp_load_all(uint4 (&v)[kLpVecs], const uint8_t* hull, int64_t v0, int per, const uint8_t* row,
+                                            const uint8_t* end) {
+  constexpr uint32_t kNeg = ES == 2 ? 0xff80ff80u : 0xff800000u;
+  const uint8_t* p = hull + v0 * 16;
+  const int first = hull < row;                                     // whole vectors: [first, first + whole)
+  const int whole = static_cast<int>((end - hull) / 16) - first;
+  const int s0 = static_cast<int>(v0) - static_cast<int>(threadIdx.x);
+  if (s0 >= first && s0 + per <= first + whole) {
+#pragma unroll
+    for (int i = 0; i < kLpVecs; ++i) {
+      v[i] = make_uint4(kNeg, kNeg, kNeg, kNeg);
+      if (i * kLpThreads < per) v[i] = *reinterpret_cast<const uint4*>(p + i * kLpThreads * 16);
+    }
+    return;
+  }
+  const int at = static_cast<int>(v0) - first;
+#pragma unroll
+  for (int i = 0; i < kLpVecs; ++i) {
+    v[i] = make_uint4(kNeg, kNeg, kNeg, kNeg);
+    if (i * kLpThreads < per && static_cast<unsigned>(at + i * kLpThreads) < static_cast<unsigned>(max(whole, 0)))
+      v[i] = *reinterpret_cast<const uint4*>(p + i * kLpThreads * 16);
+  }
+  // the vector before the whole ones, and the one after them (the same, where there are none)
+#pragma unroll 1
+  for (int k = 0; k < 2; ++k) {
+    const int vec = k == 0 ? first - 1 : first + max(whole, 0);
+    const int d = vec - static_cast<int>(v0);
+    if (vec < 0 || d < 0 || d % kLpThreads != 0 || d >= per || hull + vec * 16ll >= end) continue;
+    const uint4 e = lp_load_edge<ES>(hull + vec * 16ll, row, end);
+#pragma unroll
+    for (int i = 0; i < kLpVecs; ++i)
+      if (d == i * kLpThreads) v[i] = e;
+  }
+}
+
+// max that hands on NaN.
+__device__ __forceinline__ float lp_max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t lp_max_nan2(uint32_t a, uint32_t b) {   // bf16x2
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// A value of the type at which 2^((x - m) c) is 0, below m.
+template <int ES>
+__device__ __forceinline__ float lp_floor(float m, float c) {
+  // the value of the type next below m
+  const uint32_t one = ES == 2 ? 0x10000u : 1u;
+  const uint32_t b = __float_as_uint(m);
+  const float below = __uint_as_float(m > 0.f ? b - one : m < 0.f ? b + one : 0x80000000u + one);
+  const float far = m + kLpFloor / c;
+  // bf16: cut off to the type's bits, which for a negative number moves it up by less than it lies below
+  return fminf(below, ES == 2 ? __uint_as_float(__float_as_uint(far) & 0xffff0000u) : far);
+}
+
+// Sum of t 2^t over a vector, with t no less than -300.
+template <int ES>
+__device__ __noinline__ float lp_weighted(uint4 v, float m, float c) {
+  float f[16 / ES], w = 0.f;
+  Elem<ES>::unpack(v, f);
+#pragma unroll
+  for (int e = 0; e < 16 / ES; ++e) {
+    const float t = lp_max_nan((f[e] - m) * c, kLpFloor);
+    w = fmaf(ex2(t), t, w);
+  }
+  return w;
+}
+
+// The largest element of a vector (NaN ignored).
+template <int ES>
+__device__ __forceinline__ float lp_vec_max(const uint4& v) {
+  if (ES == 4)
+    return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+  auto max2 = [](uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  };
+  const uint32_t m = max2(max2(v.x, v.y), max2(v.z, v.w));
+  return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+}
+
+// The elements of a vector that reach `bound`, into the CTA's candidates. Out
+// of line: few vectors hold one, and the code for eight inlined copies would
+// crowd the instruction cache.
+template <int ES>
+__device__ __noinline__ void lp_gather(uint4 v, float bound, int j, uint32_t* count, uint64_t* cand) {
+  float f[16 / ES];
+  Elem<ES>::unpack(v, f);
+#pragma unroll
+  for (int e = 0; e < 16 / ES; ++e)
+    if (f[e] >= bound && f[e] > -INFINITY) {
+      const uint32_t at = atomicAdd(count, 1u);
+      if (at < kLpCand) cand[at] = lp_key(f[e], j + e);
+    }
+}
+
+// The largest key of a vector below `last`, or `best` if that is larger.
+template <int ES>
+__device__ __noinline__ uint64_t lp_best_below(uint4 v, int j, uint64_t last, uint64_t best) {
+  float f[16 / ES];
+  Elem<ES>::unpack(v, f);
+#pragma unroll
+  for (int e = 0; e < 16 / ES; ++e) {
+    const uint64_t k = lp_key(f[e], j + e);
+    if (k < last && k > best) best = k;
+  }
+  return best;
+}
+
 template <int ES, bool TOP>
 __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const LogprobArgs a) {
   constexpr int kE = 16 / ES;
-  __shared__ LpPartial s_part[kLpThreads / 32];
   __shared__ float s_group[32];
   __shared__ uint32_t s_count;
   __shared__ uint64_t s_cand[TOP ? kLpCand : 1];
   __shared__ uint64_t s_best[kLpThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int row = blockIdx.x / a.segs, seg = blockIdx.x - row * a.segs;
-  if (tid == 0) s_count = 0;
+  struct {
+    int row, seg, j0;   // j0: row index of the thread's first element
+  } x;
+  x.row = blockIdx.x / a.segs;
+  x.seg = blockIdx.x - x.row * a.segs;
   grid_dep_wait();
   grid_dep_launch();
-  const uint8_t* rp = a.x + row * a.stride;
-  const uint8_t* end = rp + static_cast<int64_t>(a.V) * ES;
-  const uint8_t* hull = reinterpret_cast<const uint8_t*>(reinterpret_cast<uintptr_t>(rp) & ~static_cast<uintptr_t>(15));
-  const int64_t v0 = static_cast<int64_t>(seg) * kLpSegVecs + tid;
   uint4 v[kLpVecs];
-#pragma unroll
-  for (int i = 0; i < kLpVecs; ++i) v[i] = lp_load<ES>(hull, v0 + i * kLpThreads, rp, end);
-
-  float m = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < kLpVecs; ++i) {
-    float f[kE];
-    Elem<ES>::unpack(v[i], f);
-#pragma unroll
-    for (int e = 0; e < kE; ++e) m = fmaxf(m, f[e]);
+  {
+    const uint8_t* rp = a.x + x.row * a.stride;
+    const uint8_t* hull = reinterpret_cast<const uint8_t*>(reinterpret_cast<uintptr_t>(rp) & ~static_cast<uintptr_t>(15));
+    const int64_t v0 = static_cast<int64_t>(x.seg) * a.per + tid;
+    x.j0 = static_cast<int>((hull - rp) / ES + v0 * kE);
+    lp_load_all<ES>(v, hull, v0, a.per, rp, rp + static_cast<int64_t>(a.V) * ES);
   }
-  const float m0 = m == -INFINITY ? 0.f : m;
-  float s = 0.f, w = 0.f;
+  const int its = a.per / kLpThreads;
+  {
+    float m = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < kLpVecs; ++i) {
-    float f[kE];
-    Elem<ES>::unpack(v[i], f);
-#pragma unroll
-    for (int e = 0; e < kE; ++e) {
-      const float t0 = (f[e] - m0) * a.c;
-      const float t = t0 < kLpFloor ? kLpFloor : t0;   // NaN stays
-      const float p = ex2(t);
-      s += p;
-      w = fmaf(p, t, w);
-    }
-  }
-  float mr = m;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    lp_merge(mr, s, w, __shfl_xor_sync(0xffffffffu, mr, o), __shfl_xor_sync(0xffffffffu, s, o),
-             __shfl_xor_sync(0xffffffffu, w, o), a.c);
-  if (lane == 0) s_part[warp] = {mr, s, w, 0.f};
-  if (TOP) {
-    float gm = m;
-    gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, 1));
-    gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, 2));
-    gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, 4));
-    if ((lane & 7) == 0) s_group[tid >> 3] = gm;
-  }
-  __syncthreads();
-  if (warp == 0) {
-    LpPartial q = s_part[lane & 7];
-#pragma unroll
-    for (int o = 4; o > 0; o >>= 1)
-      lp_merge(q.m, q.s, q.w, __shfl_xor_sync(0xffffffffu, q.m, o), __shfl_xor_sync(0xffffffffu, q.s, o),
-               __shfl_xor_sync(0xffffffffu, q.w, o), a.c);
-    if (lane == 0) a.part[static_cast<int64_t>(row) * a.segs + seg] = q;
-  }
-  if (!TOP) return;
-  // ---- the n_top-th of the 32 group maxima (every warp works it out)
-  const float gm = s_group[lane];
-  int rank = 0;
-#pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    const float o = __shfl_sync(0xffffffffu, gm, i);
-    rank += o > gm || (o == gm && i < lane);
-  }
-  const unsigned who = __ballot_sync(0xffffffffu, rank == a.n_top - 1);
-  const float bound = __shfl_sync(0xffffffffu, gm, __ffs(who) - 1);
-  const int64_t j0 = (hull - rp) / ES;   // row index of the hull's first element (<= 0)
-  if (m >= bound && m > -INFINITY) {
+    for (int i = 0; i < kLpVecs; ++i) m = fmaxf(m, lp_vec_max<ES>(v[i]));
+    const float m0 = m == -INFINITY ? 0.f : m;
+    // Masked tokens are lifted to where 2^t is 0 but t is finite (0 * -inf is no 0):
+    // 300 below the maximum, or the value just below it where that rounds to it.
+    float2 s2 = make_float2(0.f, 0.f), w2 = make_float2(0.f, 0.f);
+    const float2 m2 = make_float2(-m0, -m0), c2 = make_float2(a.c, a.c);
+    const float floor1 = lp_floor<ES>(m0, a.c);
+    const uint32_t floor2 = __byte_perm(__float_as_uint(floor1), 0, 0x3232);
 #pragma unroll
     for (int i = 0; i < kLpVecs; ++i) {
+      if (i >= its) break;
+      uint4 q = v[i];
+      if (ES == 2) {
+        q.x = lp_max_nan2(q.x, floor2);
+        q.y = lp_max_nan2(q.y, floor2);
+        q.z = lp_max_nan2(q.z, floor2);
+        q.w = lp_max_nan2(q.w, floor2);
+      }
       float f[kE];
-      Elem<ES>::unpack(v[i], f);
+      Elem<ES>::unpack(q, f);
 #pragma unroll
-      for (int e = 0; e < kE; ++e)
-        if (f[e] >= bound && f[e] > -INFINITY) {
-          const uint32_t at = atomicAdd(&s_count, 1u);
-          if (at < kLpCand) s_cand[at] = lp_key(f[e], static_cast<int>(j0 + (v0 + i * kLpThreads) * kE + e));
+      for (int e = 0; e < kE; e += 2) {
+        if (ES == 4) {
+          f[e] = lp_max_nan(f[e], floor1);
+          f[e + 1] = lp_max_nan(f[e + 1], floor1);
         }
-    }
-  }
-  __syncthreads();
-  const uint32_t n = s_count;
-  uint64_t* out = a.cand + (static_cast<int64_t>(row) * a.segs + seg) * a.n_top;
-  if (n <= kLpCand) {
-    for (uint32_t i = tid; i < n; i += kLpThreads) {
-      const uint64_t k = s_cand[i];
-      int r = 0;
-      for (uint32_t j = 0; j < n; ++j) r += s_cand[j] > k;
-      if (r < a.n_top) out[r] = k;
-    }
-    if (static_cast<uint32_t>(tid) >= n && tid < a.n_top) out[tid] = 0;
-    return;
-  }
-  uint64_t last = ~0ull;
-#pragma unroll 1
-  for (int r = 0; r < a.n_top; ++r) {
-    uint64_t best = 0;
-#pragma unroll
-    for (int i = 0; i < kLpVecs; ++i) {
-      float f[kE];
-      Elem<ES>::unpack(v[i], f);
-#pragma unroll
-      for (int e = 0; e < kE; ++e) {
-        const uint64_t k = lp_key(f[e], static_cast<int>(j0 + (v0 + i * kLpThreads) * kE + e));
-        if (k < last && k > best) best = k;
+        const float2 t = __fmul2_rn(__fadd2_rn(make_float2(f[e], f[e + 1]), m2), c2);
+        const float2 p = make_float2(ex2(t.x), ex2(t.y));
+        s2 = __fadd2_rn(s2, p);
+        w2 = __ffma2_rn(p, t, w2);
       }
     }
+    // the warp's sums, relative to its maximum
+    const float mr = warp_max(m);
+    float s = s2.x + s2.y, w = w2.x + w2.y;
+    if (w != w && s == s) {   // the maximum is the type's lowest value: nothing lies below it to lift -inf to
+      w = 0.f;
+#pragma unroll
+      for (int i = 0; i < kLpVecs; ++i)
+        if (i < its) w += lp_weighted<ES>(v[i], m0, a.c);
+    }
+    const float d = m == -INFINITY ? -INFINITY : (m - mr) * a.c, f = ex2(d);
+    w = f > 0.f ? f * (w + d * s) : s == s ? 0.f : s;
+    s *= f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-      const uint64_t k = __shfl_xor_sync(0xffffffffu, best, o);
-      best = k > best ? k : best;
+      s += __shfl_xor_sync(0xffffffffu, s, o);
+      w += __shfl_xor_sync(0xffffffffu, w, o);
     }
-    __syncthreads();
-    if (lane == 0) s_best[warp] = best;
-    __syncthreads();
+    // A partial a warp: without the top alternatives no warp of a CTA waits for another.
+    if (lane == 0) a.part[(static_cast<int64_t>(x.row) * a.segs + x.seg) * kLpWarps + warp] = {mr, s, w, 0.f};
+    if (TOP) {
+      float gm = m;
+      gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, 1));
+      gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, 2));
+      gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, 4));
+      if ((lane & 7) == 0) s_group[tid >> 3] = gm;
+      if (tid == 0) s_count = 0;
+    }
+    if (TOP) {
+      __syncthreads();
+      // ---- the n_top-th of the 32 group maxima (every warp works it out)
+      const float gm = s_group[lane];
+      int rank = 0;
+#pragma unroll 8
+      for (int i = 0; i < 32; ++i) {
+        const float o = __shfl_sync(0xffffffffu, gm, i);
+        rank += o > gm || (o == gm && i < lane);
+      }
+      const unsigned who = __ballot_sync(0xffffffffu, rank == a.n_top - 1);
+      const float bound = __shfl_sync(0xffffffffu, gm, __ffs(who) - 1);
+      if (m >= bound && m > -INFINITY) {
 #pragma unroll
-    for (int i = 0; i < kLpThreads / 32; ++i) best = s_best[i] > best ? s_best[i] : best;
-    if (tid == 0) out[r] = best;
-    last = best;
+        for (int i = 0; i < kLpVecs; ++i)
+          if (lp_vec_max<ES>(v[i]) >= bound) lp_gather<ES>(v[i], bound, x.j0 + i * kLpThreads * kE, &s_count, s_cand);
+      }
+      __syncthreads();
+      const uint32_t n = s_count;
+      uint64_t* out = a.cand + (static_cast<int64_t>(x.row) * a.segs + x.seg) * a.n_top;
+      if (n <= kLpCand) {
+        for (uint32_t i = tid; i < n; i += kLpThreads) {
+          const uint64_t k = s_cand[i];
+          int r = 0;
+#pragma unroll 4
+          for (uint32_t j = 0; j < n; ++j) r += s_cand[j] > k;
+          if (r < a.n_top) out[r] = k;
+        }
+        if (static_cast<uint32_t>(tid) >= n && tid < a.n_top) out[tid] = 0;
+      } else {
+        uint64_t last = ~0ull;
+#pragma unroll 1
+        for (int r = 0; r < a.n_top; ++r) {
+          uint64_t best = 0;
+#pragma unroll
+          for (int i = 0; i < kLpVecs; ++i) best = lp_best_below<ES>(v[i], x.j0 + i * kLpThreads * kE, last, best);
+#pragma unroll 1
+          for (int o = 16; o > 0; o >>= 1) {
+            const uint64_t k = __shfl_xor_sync(0xffffffffu, best, o);
+            best = k > best ? k : best;
+          }
+          __syncthreads();
+          if (lane == 0) s_best[warp] = best;
+          __syncthreads();
+#pragma unroll 1
+          for (int i = 0; i < kLpThreads / 32; ++i) best = s_best[i] > best ? s_best[i] : best;
+          if (tid == 0) out[r] = best;
+          last = best;
+        }
+      }
+    }
   }
 }
 
-// One warp per row: joins the segments' sums and sorted lists.
+// One warp per row: joins the segments' sums and sorted lists, which it holds
+// in shared memory where they fit (each of the n_top steps needs the head of
+// one list, and that is a load on the way of the next step).
 constexpr int kLpJoinWarps = 4;
+constexpr int kLpJoinKeys = 1024;
 
 template <int ES>
 __global__ void __launch_bounds__(kLpJoinWarps * 32) token_logprobs_join_kernel(const LogprobArgs a) {
+  __shared__ uint64_t s_keys[kLpJoinWarps][kLpJoinKeys];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int row = blockIdx.x * kLpJoinWarps + warp;
   if (row >= a.rows) {
@@ -261,13 +389,22 @@ __global__ void __launch_bounds__(kLpJoinWarps * 32) token_logprobs_join_kernel(
   const float xt = given ? Elem<ES>::load(a.x + row * a.stride, tok) : 0.f;
   grid_dep_wait();
   grid_dep_launch();
-  const LpPartial* part = a.part + static_cast<int64_t>(row) * a.segs;
+  const LpPartial* part = a.part + static_cast<int64_t>(row) * a.segs * kLpWarps;
+  const uint64_t* lists = a.cand + static_cast<int64_t>(row) * a.segs * a.n_top;
+  const int keys = a.segs * a.n_top;
+  const bool held = keys <= kLpJoinKeys;
+  if (held) {
+#pragma unroll 4
+    for (int i = lane; i < keys; i += 32) s_keys[warp][i] = lists[i];
+    lists = s_keys[warp];
+  }
   float m = -INFINITY, s = 0.f, w = 0.f;
-  for (int i = lane; i < a.segs; i += 32) {
+#pragma unroll 1
+  for (int i = lane; i < a.segs * kLpWarps; i += 32) {
     const LpPartial p = part[i];
     lp_merge(m, s, w, p.m, p.s, p.w, a.c);
   }
-#pragma unroll
+#pragma unroll 1
   for (int o = 16; o > 0; o >>= 1)
     lp_merge(m, s, w, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, s, o),
              __shfl_xor_sync(0xffffffffu, w, o), a.c);
@@ -285,17 +422,17 @@ __global__ void __launch_bounds__(kLpJoinWarps * 32) token_logprobs_join_kernel(
     if (a.entropy) a.entropy[row] = bad ? nan : ent;
     if (a.lse) a.lse[row] = bad ? nan : ref * a.inv_t + l2 * kLn2;
     if (a.saved) a.saved[row] = make_float4(bad ? nan : ref, l2, ent, 0.f);
-  }
-  if (a.status) {
-    const int bits = (tok >= a.V || tok < -1 ? SV_STATUS_BAD_TOKEN : 0) | (bad || empty ? SV_STATUS_NONFINITE_ROW : 0);
-    if (lane == 0) a.status[row] = bits;
+    if (a.status)
+      a.status[row] = (tok >= a.V || tok < -1 ? SV_STATUS_BAD_TOKEN : 0) | (bad || empty ? SV_STATUS_NONFINITE_ROW : 0);
   }
   if (a.n_top == 0) return;
+  __syncwarp();
   // heads of the sorted lists, list i with lane i % 32; `at` counts what is taken of the lane's own list
-  const uint64_t* lists = a.cand + static_cast<int64_t>(row) * a.segs * a.n_top;
   uint64_t last = ~0ull;
-  uint64_t head = lane < a.segs ? lists[static_cast<int64_t>(lane) * a.n_top] : 0;
+  uint64_t head = lane < a.segs ? lists[lane * a.n_top] : 0;
+  uint64_t mine = 0;   // the lane's answer: the lane-th largest
   int at = 0;
+#pragma unroll 1
   for (int r = 0; r < a.n_top; ++r) {
     uint64_t best = head;
     if (a.segs > 32)   // more lists than lanes: the largest below the last one taken
@@ -312,13 +449,14 @@ __global__ void __launch_bounds__(kLpJoinWarps * 32) token_logprobs_join_kernel(
     const uint64_t top = static_cast<uint64_t>(hi) << 32 | lo;
     if (top != 0 && head == top) {
       ++at;
-      head = at < a.n_top ? lists[static_cast<int64_t>(lane) * a.n_top + at] : 0;
+      head = at < a.n_top ? lists[lane * a.n_top + at] : 0;
     }
     last = top;
-    if (lane == 0) {
-      a.top_tokens[static_cast<int64_t>(row) * a.n_top + r] = top ? static_cast<int32_t>(0xffffffffu - lo) : -1;
-      a.top_logprobs[static_cast<int64_t>(row) * a.n_top + r] = bad ? nan : top ? logp(lp_key_value(top)) : -INFINITY;
-    }
+    if (lane == r) mine = top;
+  }
+  if (lane < a.n_top) {
+    a.top_tokens[static_cast<int64_t>(row) * a.n_top + lane] = mine ? static_cast<int32_t>(~static_cast<uint32_t>(mine)) : -1;
+    a.top_logprobs[static_cast<int64_t>(row) * a.n_top + lane] = bad ? nan : mine ? logp(lp_key_value(mine)) : -INFINITY;
   }
 }
 
@@ -331,9 +469,23 @@ struct LogprobGradArgs {
   const float4* saved;         // [rows]
   const float* g;              // [rows]
   const float* h;              // [rows] or nullptr
-  int32_t rows, V, segs;
+  int32_t rows, V, segs, per;
   float c, inv_t;
 };
+
+// The elements of a vector that lie in the row.
+template <int ES>
+__device__ __noinline__ void lp_store_edge(uint8_t* dp, int64_t j, int V, uint4 v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int e = 0; e < 16 / ES; ++e) {
+    if (j + e < 0 || j + e >= V) continue;
+    if (ES == 4)
+      reinterpret_cast<uint32_t*>(dp)[j + e] = w[e & 3];
+    else
+      reinterpret_cast<uint16_t*>(dp)[j + e] = static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
+  }
+}
 
 // Eight 16-byte vectors a thread, as in the forward pass, if x and dx rows
 // start at the same place within 16 bytes; else one element at a time.
@@ -348,12 +500,9 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_grad_kernel(cons
   uint8_t* dp = a.dx + row * a.dstride;
   const uint8_t* end = rp + static_cast<int64_t>(a.V) * ES;
   const uint8_t* hull = reinterpret_cast<const uint8_t*>(reinterpret_cast<uintptr_t>(rp) & ~static_cast<uintptr_t>(15));
-  const int64_t v0 = static_cast<int64_t>(seg) * kLpSegVecs + tid;
+  const int64_t v0 = static_cast<int64_t>(seg) * a.per + tid;
   uint4 v[kLpVecs];
-  if (VEC) {
-#pragma unroll
-    for (int i = 0; i < kLpVecs; ++i) v[i] = lp_load<ES>(hull, v0 + i * kLpThreads, rp, end);
-  }
+  if (VEC) lp_load_all<ES>(v, hull, v0, a.per, rp, end);
   const int tok = a.tokens[row];
   const float4 st = a.saved[row];
   const bool empty = st.y == -INFINITY;   // no token left: no gradient
@@ -362,14 +511,13 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_grad_kernel(cons
   const float ref = st.x, l2 = empty ? 0.f : st.y;
   const float a0 = -(g + h * st.z), a1 = -h * kLn2;
   auto grad = [&](float x, int64_t j) {
-    const float t0 = fmaf(x - ref, a.c, -l2);
-    const float t = t0 < kLpFloor ? kLpFloor : t0;
+    const float t = lp_max_nan(fmaf(x - ref, a.c, -l2), kLpFloor);
     const float d = ex2(t) * fmaf(a1, t, a0);
     return j == tok ? d + g : d;
   };
   if (!VEC) {
-    for (int64_t j = static_cast<int64_t>(seg) * kLpSegVecs * kE + tid;
-         j < a.V && j < (seg + 1) * static_cast<int64_t>(kLpSegVecs) * kE; j += kLpThreads) {
+    for (int64_t j = static_cast<int64_t>(seg) * a.per * kE + tid; j < a.V && j < (seg + 1) * static_cast<int64_t>(a.per) * kE;
+         j += kLpThreads) {
       const float d = grad(Elem<ES>::load(rp, static_cast<int>(j)), j);
       if (ES == 4)
         reinterpret_cast<float*>(dp)[j] = d;
@@ -378,39 +526,37 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_grad_kernel(cons
     }
     return;
   }
-  const int64_t j0 = (hull - rp) / ES;
+  const int64_t j0 = (hull - rp) / ES + v0 * kE;
 #pragma unroll
   for (int i = 0; i < kLpVecs; ++i) {
-    const int64_t vec = v0 + i * kLpThreads;
-    const uint8_t* p = hull + vec * 16;
-    if (p >= end) continue;
+    const uint8_t* p = hull + (v0 + i * kLpThreads) * 16;
+    if (i * kLpThreads >= a.per || p >= end) continue;
     float f[kE];
     Elem<ES>::unpack(v[i], f);
-    const int64_t j = j0 + vec * kE;
+    const int64_t j = j0 + i * kLpThreads * kE;
 #pragma unroll
-    for (int e = 0; e < kE; ++e) f[e] = grad(f[e], j + e);
-    if (p >= rp && p + 16 <= end) {
-      uint4 o;
-      if (ES == 4) {
-        o = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-      } else {
-        uint32_t q[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          asm("cvt.rn.bf16x2.f32 %0, %2, %1;" : "=r"(q[e]) : "f"(f[(2 * e) % kE]), "f"(f[(2 * e + 1) % kE]));
-        o = make_uint4(q[0], q[1], q[2], q[3]);
-      }
-      *reinterpret_cast<uint4*>(dp + j * ES) = o;
-    } else {
-#pragma unroll
-      for (int e = 0; e < kE; ++e) {
-        if (j + e < 0 || j + e >= a.V) continue;
-        if (ES == 4)
-          reinterpret_cast<float*>(dp)[j + e] = f[e];
-        else
-          reinterpret_cast<__nv_bfloat16*>(dp)[j + e] = __float2bfloat16_rn(f[e]);
-      }
+    for (int e = 0; e < kE; ++e) {
+      const float t = lp_max_nan(fmaf(f[e] - ref, a.c, -l2), kLpFloor);
+      f[e] = ex2(t) * fmaf(a1, t, a0);
     }
+    if (tok >= j && tok < j + kE) {
+#pragma unroll
+      for (int e = 0; e < kE; ++e) f[e] += tok == j + e ? g : 0.f;
+    }
+    uint4 o;
+    if (ES == 4) {
+      o = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    } else {
+      uint32_t q[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        asm("cvt.rn.bf16x2.f32 %0, %2, %1;" : "=r"(q[e]) : "f"(f[(2 * e) % kE]), "f"(f[(2 * e + 1) % kE]));
+      o = make_uint4(q[0], q[1], q[2], q[3]);
+    }
+    if (p >= rp && p + 16 <= end)
+      *reinterpret_cast<uint4*>(dp + j * ES) = o;
+    else
+      lp_store_edge<ES>(dp, j, a.V, o);
   }
 }
 

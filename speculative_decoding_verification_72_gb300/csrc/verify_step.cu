@@ -136,11 +136,19 @@ cudaError_t launch_cols(const sv_q8_cache& c, const AttnArgs& a, int64_t items, 
   return e != cudaSuccess ? e : launch_join<T, D, MT>(a, items, st);
 }
 
-template <typename T, int D>
-cudaError_t launch_weights(const WeightArgs& a, int mt, cudaStream_t st) {
-  return mt == 1   ? launch_smem<attn_weights_q8_kernel<T, D, 1>>(a.grid, kAttnThreads, weight_smem_bytes<D, 1>(), weight_smem_bytes<D, 1>(), st, a)
-         : mt == 2 ? launch_smem<attn_weights_q8_kernel<T, D, 2>>(a.grid, kAttnThreads, weight_smem_bytes<D, 2>(), weight_smem_bytes<D, 2>(), st, a)
-                   : launch_smem<attn_weights_q8_kernel<T, D, 4>>(a.grid, kAttnThreads, weight_smem_bytes<D, 4>(), weight_smem_bytes<D, 4>(), st, a);
+template <typename T, int D, int MT, int NT>
+cudaError_t launch_weights(const sv_q8_cache& c, const WeightArgs& a, cudaStream_t st) {
+  CUtensorMap k;
+  if (!code_map(c, c.k, &k)) return cudaErrorInvalidValue;
+  constexpr int kSmem = WtLayout<D, MT, NT>::kBytes;
+  return launch_smem<attn_weights_q8_kernel<T, D, MT, NT>>(a.grid, kWtThreads, kSmem, kSmem, st, k, a);
+}
+
+template <typename T, int D, int NT>
+cudaError_t launch_weights(const sv_q8_cache& c, const WeightArgs& a, int64_t rows, cudaStream_t st) {
+  return rows <= 16   ? launch_weights<T, D, 1, NT>(c, a, st)
+         : rows <= 32 ? launch_weights<T, D, 2, NT>(c, a, st)
+                      : launch_weights<T, D, 4, NT>(c, a, st);
 }
 
 size_t attn_ws_part_bytes(int block, int D) {
@@ -149,23 +157,22 @@ size_t attn_ws_part_bytes(int block, int D) {
 
 // ---------------------------------------------------------------- logprobs
 
-int lp_segs(int64_t V, int es) {
-  const int64_t vecs = (V * es + 30) / 16;   // a row's hull, wherever it starts
-  return static_cast<int>((vecs + kLpSegVecs - 1) / kLpSegVecs);
-}
+int64_t lp_vecs(int64_t V, int es) { return (V * es + 30) / 16; }   // a row's hull, wherever it starts
 
 bool valid_t(float t) { return std::isfinite(t) && t >= 1e-4f; }
 
 struct LpPlan {
-  int segs = 0;
+  int segs = 0, per = 0;   // equal segments, in vectors
   size_t off_cand = 0, total = 0;
 };
 
 bool lp_plan(int64_t rows, int64_t V, int es, int n_top, LpPlan* p) {
   if (rows < 0 || V < 1 || es == 0 || n_top < 0 || n_top > SV_MAX_TOP_ALTERNATIVES) return false;
-  p->segs = lp_segs(V, es);
+  const int64_t vecs = lp_vecs(V, es);
+  p->segs = static_cast<int>((vecs + kLpSegVecs - 1) / kLpSegVecs);
+  p->per = static_cast<int>(align_up((vecs + p->segs - 1) / p->segs, kLpThreads));
   if (rows * p->segs > INT32_MAX) return false;
-  p->off_cand = align_up(static_cast<size_t>(rows) * p->segs * sizeof(LpPartial), kAlign);
+  p->off_cand = align_up(static_cast<size_t>(rows) * p->segs * kLpWarps * sizeof(LpPartial), kAlign);
   p->total = p->off_cand + align_up(static_cast<size_t>(rows) * p->segs * n_top * sizeof(uint64_t), kAlign);
   if (p->total < kAlign) p->total = kAlign;
   return true;
@@ -315,16 +322,17 @@ sv_status spec_attention_weights_q8(const sv_rows* q, int32_t dtype, const float
   a.coef = static_cast<float>(static_cast<double>(sm_scale) * 1.4426950408889634);
   a.decay = decay;
   const int64_t rows = static_cast<int64_t>(path_nodes ? std::min(path_cols, N) : N) * a.G;
-  if (rows > INT32_MAX) return SV_ERR_INVALID_ARG;
-  const int mt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+  if (rows > SV_MAX_TREE_NODES * 1024) return SV_ERR_INVALID_ARG;
+  a.inv_g = ((1ull << 32) + a.G - 1) / a.G;
   const int64_t items = static_cast<int64_t>(B) * cache->Hkv;
-  const int64_t tiles = (static_cast<int64_t>(cache->max_pages) * cache->page_size + kAttnTile - 1) / kAttnTile;
+  const int64_t tiles = (static_cast<int64_t>(cache->max_pages) * cache->page_size + kColTile - 1) / kColTile;
   if (items > INT32_MAX || items * tiles > INT32_MAX) return SV_ERR_INVALID_ARG;
-  a.grid = static_cast<int32_t>(std::min<int64_t>(sm_count() * (mt == 4 ? 3 : 4), items * tiles));
+  a.grid = static_cast<int32_t>(std::min<int64_t>(2 * sm_count(), items * tiles));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const sv_q8_cache& c = *cache;
   if (dtype == SV_BF16)
-    return done(cache->D == 128 ? launch_weights<TypeBf16, 128>(a, mt, st) : launch_weights<TypeBf16, 64>(a, mt, st));
-  return done(cache->D == 128 ? launch_weights<TypeF16, 128>(a, mt, st) : launch_weights<TypeF16, 64>(a, mt, st));
+    return done(c.D == 128 ? launch_weights<TypeBf16, 128, 2>(c, a, rows, st) : launch_weights<TypeBf16, 64, 2>(c, a, rows, st));
+  return done(c.D == 128 ? launch_weights<TypeF16, 128, 3>(c, a, rows, st) : launch_weights<TypeF16, 64, 3>(c, a, rows, st));
 }
 
 size_t spec_kv_evict_q8_workspace_size(int32_t B, int32_t Hkv, int32_t keep) {
@@ -405,6 +413,7 @@ sv_status spec_token_logprobs(const void* logits, int32_t dtype, int64_t row_str
   a.rows = rows;
   a.V = V;
   a.segs = p.segs;
+  a.per = p.per;
   a.n_top = n_top;
   a.c = static_cast<float>(1.4426950408889634 / temperature);
   a.inv_t = static_cast<float>(1.0 / temperature);
@@ -457,6 +466,7 @@ sv_status spec_token_logprobs_backward(const void* logits, int32_t dtype, int64_
   a.rows = rows;
   a.V = V;
   a.segs = p.segs;
+  a.per = p.per;
   a.c = static_cast<float>(1.4426950408889634 / temperature);
   a.inv_t = static_cast<float>(1.0 / temperature);
   const bool vec = (reinterpret_cast<uintptr_t>(logits) - reinterpret_cast<uintptr_t>(out_grad)) % 16 == 0 &&

@@ -84,6 +84,16 @@ def test_ties_masks_and_ranges(kind, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+def test_the_lowest_value_beside_masked_tokens(dtype):
+    x = torch.full((1, 3, 9000), -float("inf"))
+    low = torch.finfo(dtype).min
+    x[0, 0, ::3] = low                  # the row's maximum is the lowest value
+    x[0, 1, ::3], x[0, 1, 4001] = low, 1.0
+    x[0, 2, ::2], x[0, 2, 1::4] = -0.0, low
+    check(x.to(dtype), [[3, 0, 1]], 1.0, 6)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 def test_rows_that_are_not_finite(dtype):
     x = torch.randn((1, 6, 3000))
     x[0, 0, 7] = float("nan")
