@@ -15,15 +15,16 @@
 // with t' = (x - m) c - log2 s: one more pass over the row, no sums.
 //
 // Bound by memory: the forward pass reads each row once, the gradient reads and
-// writes it once. A row is cut into equal segments of at most 32 KB; a thread
+// writes it once. A row is cut into equal segments of at most 16 KB (32 with
+// alternatives); a thread
 // has up to eight 16-byte vectors of one in registers, so maximum, sums and
 // selection are passes over registers.
 //
 // Top alternatives by (logit, lower index): a bound that at least n_top
-// elements of the segment reach is the n_top-th of the 32 maxima of groups of
-// eight threads; the few elements that reach it are gathered and ranked. If
-// they overflow the buffer (many equal logits) the segment takes n_top rounds
-// of block-wide maxima instead. Masked (-inf) tokens are no alternatives.
+// elements of the segment reach is the n_top-th of the 64 maxima of groups of
+// four threads; the few elements that reach it are gathered and ranked. If
+// they overflow the buffer (many equal logits, or all but some hundred masked)
+// the segment takes n_top rounds of CTA-wide maxima instead. Masked (-inf) tokens are no alternatives.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -32,12 +33,18 @@
 
 namespace sv {
 
-constexpr int kLpThreads = 256;
-constexpr int kLpWarps = kLpThreads / 32;
+// Threads of a CTA: the selection's cost is one per CTA, so it has larger ones
+// (192 rows of 128256 bf16, 20 alternatives: 29.8 us with 256, 33.3 with 128);
+// without it smaller ones start and end more evenly (2048 rows of 50257 bf16,
+// forward and gradient: 115 us with 128, 121 with 256).
+constexpr int kLpThreads = 128;
+constexpr int kLpTopThreads = 256;
 constexpr int kLpVecs = 8;                                   // 16-byte vectors per thread
-constexpr int kLpSegVecs = kLpThreads * kLpVecs;             // 32 KB
+constexpr int kLpGroup = 4;                                  // threads of a group
+constexpr int kLpGroups = kLpTopThreads / kLpGroup;
 constexpr int kLpMaxTop = SV_MAX_TOP_ALTERNATIVES;
-constexpr int kLpCand = 512;
+constexpr int kLpHits = 320;                                 // vectors that reach the bound
+constexpr int kLpCand = 512;                                 // elements that do
 constexpr float kLpFloor = -300.f;                           // 2^-300 is 0 in fp32
 
 struct __align__(16) LpPartial {
@@ -48,9 +55,9 @@ struct LogprobArgs {
   const uint8_t* x;
   int64_t stride;              // bytes between rows
   const int32_t* tokens;       // [rows]
-  int32_t rows, V, segs, per, n_top;   // per: vectors of a segment, a multiple of kLpThreads
+  int32_t rows, V, segs, per, n_top;   // per: vectors of a segment, a multiple of the CTA's threads
   float c, inv_t;              // log2(e) / T, 1 / T
-  LpPartial* part;             // [rows, segs, kLpWarps]
+  LpPartial* part;             // [rows, segs, warps of the CTA]
   uint64_t* cand;              // [rows, segs, n_top] keys in descending order, 0 past the last
   float* logprob;              // [rows]
   float* entropy;              // [rows] or nullptr
@@ -111,7 +118,7 @@ __device__ __noinline__ uint4 lp_load_edge(const uint8_t* p, const uint8_t* row,
 // where the segment lies inside the row. Else what is not in the row reads as
 // masked; only whole vectors of it are read as vectors, and the one at each of
 // its edges, which one thread has, element by element.
-template <int ES>
+template <int ES, int T>
 __device__ __forceinline__ void lp_load_all(uint4 (&v)[kLpVecs], const uint8_t* hull, int64_t v0, int per, const uint8_t* row,
                                             const uint8_t* end) {
   constexpr uint32_t kNeg = ES == 2 ? 0xff80ff80u : 0xff800000u;
@@ -123,7 +130,7 @@ __device__ __forceinline__ void lp_load_all(uint4 (&v)[kLpVecs], const uint8_t* 
 #pragma unroll
     for (int i = 0; i < kLpVecs; ++i) {
       v[i] = make_uint4(kNeg, kNeg, kNeg, kNeg);
-      if (i * kLpThreads < per) v[i] = *reinterpret_cast<const uint4*>(p + i * kLpThreads * 16);
+      if (i * T < per) v[i] = *reinterpret_cast<const uint4*>(p + i * T * 16);
     }
     return;
   }
@@ -131,19 +138,19 @@ __device__ __forceinline__ void lp_load_all(uint4 (&v)[kLpVecs], const uint8_t* 
 #pragma unroll
   for (int i = 0; i < kLpVecs; ++i) {
     v[i] = make_uint4(kNeg, kNeg, kNeg, kNeg);
-    if (i * kLpThreads < per && static_cast<unsigned>(at + i * kLpThreads) < static_cast<unsigned>(max(whole, 0)))
-      v[i] = *reinterpret_cast<const uint4*>(p + i * kLpThreads * 16);
+    if (i * T < per && static_cast<unsigned>(at + i * T) < static_cast<unsigned>(max(whole, 0)))
+      v[i] = *reinterpret_cast<const uint4*>(p + i * T * 16);
   }
   // the vector before the whole ones, and the one after them (the same, where there are none)
 #pragma unroll 1
   for (int k = 0; k < 2; ++k) {
     const int vec = k == 0 ? first - 1 : first + max(whole, 0);
     const int d = vec - static_cast<int>(v0);
-    if (vec < 0 || d < 0 || d % kLpThreads != 0 || d >= per || hull + vec * 16ll >= end) continue;
+    if (vec < 0 || d < 0 || d % T != 0 || d >= per || hull + vec * 16ll >= end) continue;
     const uint4 e = lp_load_edge<ES>(hull + vec * 16ll, row, end);
 #pragma unroll
     for (int i = 0; i < kLpVecs; ++i)
-      if (d == i * kLpThreads) v[i] = e;
+      if (d == i * T) v[i] = e;
   }
 }
 
@@ -199,21 +206,6 @@ __device__ __forceinline__ float lp_vec_max(const uint4& v) {
   return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
 }
 
-// The elements of a vector that reach `bound`, into the CTA's candidates. Out
-// of line: few vectors hold one, and the code for eight inlined copies would
-// crowd the instruction cache.
-template <int ES>
-__device__ __noinline__ void lp_gather(uint4 v, float bound, int j, uint32_t* count, uint64_t* cand) {
-  float f[16 / ES];
-  Elem<ES>::unpack(v, f);
-#pragma unroll
-  for (int e = 0; e < 16 / ES; ++e)
-    if (f[e] >= bound && f[e] > -INFINITY) {
-      const uint32_t at = atomicAdd(count, 1u);
-      if (at < kLpCand) cand[at] = lp_key(f[e], j + e);
-    }
-}
-
 // The largest key of a vector below `last`, or `best` if that is larger.
 template <int ES>
 __device__ __noinline__ uint64_t lp_best_below(uint4 v, int j, uint64_t last, uint64_t best) {
@@ -228,12 +220,16 @@ __device__ __noinline__ uint64_t lp_best_below(uint4 v, int j, uint64_t last, ui
 }
 
 template <int ES, bool TOP>
-__global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const LogprobArgs a) {
+__global__ void __launch_bounds__(TOP ? kLpTopThreads : kLpThreads, TOP ? 4 : 8) token_logprobs_kernel(const LogprobArgs a) {
   constexpr int kE = 16 / ES;
-  __shared__ float s_group[32];
-  __shared__ uint32_t s_count;
+  constexpr int T = TOP ? kLpTopThreads : kLpThreads;
+  __shared__ __align__(16) float s_group[kLpGroups];
+  __shared__ float s_bound;
+  __shared__ uint32_t s_hits, s_count;
+  __shared__ uint4 s_hit[TOP ? kLpHits : 1];
+  __shared__ int32_t s_hit_at[TOP ? kLpHits : 1];
   __shared__ uint64_t s_cand[TOP ? kLpCand : 1];
-  __shared__ uint64_t s_best[kLpThreads / 32];
+  __shared__ uint64_t s_best[2][T / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   struct {
     int row, seg, j0;   // j0: row index of the thread's first element
@@ -248,13 +244,20 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const Log
     const uint8_t* hull = reinterpret_cast<const uint8_t*>(reinterpret_cast<uintptr_t>(rp) & ~static_cast<uintptr_t>(15));
     const int64_t v0 = static_cast<int64_t>(x.seg) * a.per + tid;
     x.j0 = static_cast<int>((hull - rp) / ES + v0 * kE);
-    lp_load_all<ES>(v, hull, v0, a.per, rp, rp + static_cast<int64_t>(a.V) * ES);
+    lp_load_all<ES, T>(v, hull, v0, a.per, rp, rp + static_cast<int64_t>(a.V) * ES);
   }
-  const int its = a.per / kLpThreads;
+  const int its = a.per / T;
   {
     float m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < kLpVecs; ++i) m = fmaxf(m, lp_vec_max<ES>(v[i]));
+    if (TOP) {
+      float gm = m;
+#pragma unroll
+      for (int o = 1; o < kLpGroup; o <<= 1) gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, o));
+      if (lane % kLpGroup == 0) s_group[tid / kLpGroup] = gm;
+      if (tid == 0) s_hits = s_count = 0;
+    }
     const float m0 = m == -INFINITY ? 0.f : m;
     // Masked tokens are lifted to where 2^t is 0 but t is finite (0 * -inf is no 0):
     // 300 below the maximum, or the value just below it where that rounds to it.
@@ -304,63 +307,89 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_kernel(const Log
       w += __shfl_xor_sync(0xffffffffu, w, o);
     }
     // A partial a warp: without the top alternatives no warp of a CTA waits for another.
-    if (lane == 0) a.part[(static_cast<int64_t>(x.row) * a.segs + x.seg) * kLpWarps + warp] = {mr, s, w, 0.f};
-    if (TOP) {
-      float gm = m;
-      gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, 1));
-      gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, 2));
-      gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, 4));
-      if ((lane & 7) == 0) s_group[tid >> 3] = gm;
-      if (tid == 0) s_count = 0;
-    }
+    if (lane == 0) a.part[(static_cast<int64_t>(x.row) * a.segs + x.seg) * (T / 32) + warp] = {mr, s, w, 0.f};
     if (TOP) {
       __syncthreads();
-      // ---- the n_top-th of the 32 group maxima (every warp works it out)
-      const float gm = s_group[lane];
-      int rank = 0;
-#pragma unroll 8
-      for (int i = 0; i < 32; ++i) {
-        const float o = __shfl_sync(0xffffffffu, gm, i);
-        rank += o > gm || (o == gm && i < lane);
+      // ---- the n_top-th of the group maxima: a group's threads rank its own
+      {
+        const int i = tid / kLpGroup;
+        const float gm = s_group[i];
+        int r = 0;
+#pragma unroll
+        for (int q = 0; q < kLpGroups / kLpGroup / 4; ++q) {
+          const int j = (tid % kLpGroup + q * kLpGroup) * 4;
+          const float4 o = *reinterpret_cast<const float4*>(s_group + j);
+          // equal maxima rank by their index
+          r += (j < i ? o.x >= gm : o.x > gm) + (j + 1 < i ? o.y >= gm : o.y > gm) + (j + 2 < i ? o.z >= gm : o.z > gm) +
+               (j + 3 < i ? o.w >= gm : o.w > gm);
+        }
+#pragma unroll
+        for (int o = 1; o < kLpGroup; o <<= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
+        if (r == a.n_top - 1) s_bound = gm;
       }
-      const unsigned who = __ballot_sync(0xffffffffu, rank == a.n_top - 1);
-      const float bound = __shfl_sync(0xffffffffu, gm, __ffs(who) - 1);
+      __syncthreads();
+      // ---- vectors that hold one that reaches it, then their elements, a thread each
+      const float bound = s_bound;
       if (m >= bound && m > -INFINITY) {
 #pragma unroll
         for (int i = 0; i < kLpVecs; ++i)
-          if (lp_vec_max<ES>(v[i]) >= bound) lp_gather<ES>(v[i], bound, x.j0 + i * kLpThreads * kE, &s_count, s_cand);
+          if (lp_vec_max<ES>(v[i]) >= bound) {
+            const uint32_t at = atomicAdd(&s_hits, 1u);
+            if (at < kLpHits) {
+              s_hit[at] = v[i];
+              s_hit_at[at] = x.j0 + i * T * kE;
+            }
+          }
+      }
+      __syncthreads();
+      const uint32_t hits = s_hits;
+#pragma unroll 1
+      for (uint32_t i = tid; i < min(hits, kLpHits) * kE; i += T) {
+        const uint32_t e = i % kE;
+        const float f = ES == 2 ? __uint_as_float(reinterpret_cast<const uint16_t*>(s_hit)[i] << 16)
+                                : reinterpret_cast<const float*>(s_hit)[i];
+        if (f >= bound && f > -INFINITY) {
+          const uint32_t at = atomicAdd(&s_count, 1u);
+          if (at < kLpCand) s_cand[at] = lp_key(f, s_hit_at[i / kE] + e);
+        }
       }
       __syncthreads();
       const uint32_t n = s_count;
       uint64_t* out = a.cand + (static_cast<int64_t>(x.row) * a.segs + x.seg) * a.n_top;
-      if (n <= kLpCand) {
-        for (uint32_t i = tid; i < n; i += kLpThreads) {
-          const uint64_t k = s_cand[i];
+      if (hits <= kLpHits && n <= kLpCand) {
+        // ranks by counting, eight lanes a candidate
+#pragma unroll 1
+        for (uint32_t i0 = 0; i0 < n; i0 += T / 8) {
+          const uint32_t i = i0 + (tid >> 3);
+          const uint64_t k = i < n ? s_cand[i] : 0;
           int r = 0;
-#pragma unroll 4
-          for (uint32_t j = 0; j < n; ++j) r += s_cand[j] > k;
-          if (r < a.n_top) out[r] = k;
+          for (uint32_t j = tid & 7; j < n; j += 8) r += s_cand[j] > k;
+          r += __shfl_xor_sync(0xffffffffu, r, 1);
+          r += __shfl_xor_sync(0xffffffffu, r, 2);
+          r += __shfl_xor_sync(0xffffffffu, r, 4);
+          if (i < n && r < a.n_top && (tid & 7) == 0) out[r] = k;
         }
         if (static_cast<uint32_t>(tid) >= n && tid < a.n_top) out[tid] = 0;
       } else {
-        uint64_t last = ~0ull;
+        // n_top times the CTA's largest; the thread that had it looks for its next
+        uint64_t mine = 0;
+#pragma unroll
+        for (int i = 0; i < kLpVecs; ++i) mine = lp_best_below<ES>(v[i], x.j0 + i * T * kE, ~0ull, mine);
 #pragma unroll 1
         for (int r = 0; r < a.n_top; ++r) {
+          const uint32_t hi = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(mine >> 32));
+          const uint32_t lo = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(mine >> 32) == hi ? static_cast<uint32_t>(mine) : 0u);
+          if (lane == 0) s_best[r & 1][warp] = static_cast<uint64_t>(hi) << 32 | lo;
+          __syncthreads();
           uint64_t best = 0;
 #pragma unroll
-          for (int i = 0; i < kLpVecs; ++i) best = lp_best_below<ES>(v[i], x.j0 + i * kLpThreads * kE, last, best);
-#pragma unroll 1
-          for (int o = 16; o > 0; o >>= 1) {
-            const uint64_t k = __shfl_xor_sync(0xffffffffu, best, o);
-            best = k > best ? k : best;
-          }
-          __syncthreads();
-          if (lane == 0) s_best[warp] = best;
-          __syncthreads();
-#pragma unroll 1
-          for (int i = 0; i < kLpThreads / 32; ++i) best = s_best[i] > best ? s_best[i] : best;
+          for (int i = 0; i < T / 32; ++i) best = s_best[r & 1][i] > best ? s_best[r & 1][i] : best;
           if (tid == 0) out[r] = best;
-          last = best;
+          if (best != 0 && mine == best) {
+            mine = 0;
+#pragma unroll
+            for (int i = 0; i < kLpVecs; ++i) mine = lp_best_below<ES>(v[i], x.j0 + i * T * kE, best, mine);
+          }
         }
       }
     }
@@ -389,7 +418,8 @@ __global__ void __launch_bounds__(kLpJoinWarps * 32) token_logprobs_join_kernel(
   const float xt = given ? Elem<ES>::load(a.x + row * a.stride, tok) : 0.f;
   grid_dep_wait();
   grid_dep_launch();
-  const LpPartial* part = a.part + static_cast<int64_t>(row) * a.segs * kLpWarps;
+  const int parts = a.segs * ((a.n_top ? kLpTopThreads : kLpThreads) / 32);
+  const LpPartial* part = a.part + static_cast<int64_t>(row) * parts;
   const uint64_t* lists = a.cand + static_cast<int64_t>(row) * a.segs * a.n_top;
   const int keys = a.segs * a.n_top;
   const bool held = keys <= kLpJoinKeys;
@@ -400,7 +430,7 @@ __global__ void __launch_bounds__(kLpJoinWarps * 32) token_logprobs_join_kernel(
   }
   float m = -INFINITY, s = 0.f, w = 0.f;
 #pragma unroll 1
-  for (int i = lane; i < a.segs * kLpWarps; i += 32) {
+  for (int i = lane; i < parts; i += 32) {
     const LpPartial p = part[i];
     lp_merge(m, s, w, p.m, p.s, p.w, a.c);
   }
@@ -490,7 +520,7 @@ __device__ __noinline__ void lp_store_edge(uint8_t* dp, int64_t j, int V, uint4 
 // Eight 16-byte vectors a thread, as in the forward pass, if x and dx rows
 // start at the same place within 16 bytes; else one element at a time.
 template <int ES, bool VEC>
-__global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_grad_kernel(const LogprobGradArgs a) {
+__global__ void __launch_bounds__(kLpThreads, 8) token_logprobs_grad_kernel(const LogprobGradArgs a) {
   constexpr int kE = 16 / ES;
   const int tid = threadIdx.x;
   const int row = blockIdx.x / a.segs, seg = blockIdx.x - row * a.segs;
@@ -502,7 +532,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) token_logprobs_grad_kernel(cons
   const uint8_t* hull = reinterpret_cast<const uint8_t*>(reinterpret_cast<uintptr_t>(rp) & ~static_cast<uintptr_t>(15));
   const int64_t v0 = static_cast<int64_t>(seg) * a.per + tid;
   uint4 v[kLpVecs];
-  if (VEC) lp_load_all<ES>(v, hull, v0, a.per, rp, end);
+  if (VEC) lp_load_all<ES, kLpThreads>(v, hull, v0, a.per, rp, end);
   const int tok = a.tokens[row];
   const float4 st = a.saved[row];
   const bool empty = st.y == -INFINITY;   // no token left: no gradient

@@ -162,17 +162,19 @@ int64_t lp_vecs(int64_t V, int es) { return (V * es + 30) / 16; }   // a row's h
 bool valid_t(float t) { return std::isfinite(t) && t >= 1e-4f; }
 
 struct LpPlan {
-  int segs = 0, per = 0;   // equal segments, in vectors
+  int threads = 0, segs = 0, per = 0;   // CTAs' threads, equal segments, in vectors
   size_t off_cand = 0, total = 0;
 };
 
 bool lp_plan(int64_t rows, int64_t V, int es, int n_top, LpPlan* p) {
   if (rows < 0 || V < 1 || es == 0 || n_top < 0 || n_top > SV_MAX_TOP_ALTERNATIVES) return false;
   const int64_t vecs = lp_vecs(V, es);
-  p->segs = static_cast<int>((vecs + kLpSegVecs - 1) / kLpSegVecs);
-  p->per = static_cast<int>(align_up((vecs + p->segs - 1) / p->segs, kLpThreads));
+  p->threads = n_top ? kLpTopThreads : kLpThreads;
+  const int most = p->threads * kLpVecs;
+  p->segs = static_cast<int>((vecs + most - 1) / most);
+  p->per = static_cast<int>(align_up((vecs + p->segs - 1) / p->segs, p->threads));
   if (rows * p->segs > INT32_MAX) return false;
-  p->off_cand = align_up(static_cast<size_t>(rows) * p->segs * kLpWarps * sizeof(LpPartial), kAlign);
+  p->off_cand = align_up(static_cast<size_t>(rows) * p->segs * (p->threads / 32) * sizeof(LpPartial), kAlign);
   p->total = p->off_cand + align_up(static_cast<size_t>(rows) * p->segs * n_top * sizeof(uint64_t), kAlign);
   if (p->total < kAlign) p->total = kAlign;
   return true;
@@ -338,7 +340,7 @@ sv_status spec_attention_weights_q8(const sv_rows* q, int32_t dtype, const float
 size_t spec_kv_evict_q8_workspace_size(int32_t B, int32_t Hkv, int32_t keep) {
   if (B < 0 || Hkv < 1 || keep < 1) return 0;
   const size_t bh = static_cast<size_t>(B) * Hkv;
-  return align_up((3 * bh * keep + bh) * sizeof(int32_t), kAlign) + kAlign;
+  return align_up((2 * bh * keep + bh) * sizeof(int32_t), kAlign) + kAlign;
 }
 
 sv_status spec_kv_evict_q8(const sv_q8_cache* cache, int32_t B, const int32_t* seq_len, const float* scores,
@@ -347,7 +349,8 @@ sv_status spec_kv_evict_q8(const sv_q8_cache* cache, int32_t B, const int32_t* s
                            int32_t* out_status, void* workspace, size_t workspace_bytes, void* stream) {
   if (B < 0 || S < 1 || keep < 1) return SV_ERR_INVALID_ARG;
   if (B == 0) return SV_OK;
-  if (!valid_cache(cache) || keep % cache->page_size != 0 || keep > S ||
+  if (!valid_cache(cache) || keep % cache->page_size != 0 || keep > S || S > 1 << 30 ||
+      static_cast<int64_t>(cache->num_pages) * cache->Hkv > (int64_t{1} << 32) / cache->page_size ||
       keep > static_cast<int64_t>(cache->max_pages) * cache->page_size || !seq_len || !scores || !positions ||
       !out_scores || !out_positions || !out_len || !workspace || !aligned(seq_len, 4) || !aligned(scores, 4) ||
       !aligned(positions, 4) || !aligned(protect_from, 4) || !aligned(out_scores, 4) || !aligned(out_positions, 4) ||
@@ -355,7 +358,8 @@ sv_status spec_kv_evict_q8(const sv_q8_cache* cache, int32_t B, const int32_t* s
     return SV_ERR_INVALID_ARG;
   if (workspace_bytes < spec_kv_evict_q8_workspace_size(B, cache->Hkv, keep)) return SV_ERR_WORKSPACE_TOO_SMALL;
   const int64_t bh = static_cast<int64_t>(B) * cache->Hkv;
-  const int64_t groups = (keep / cache->page_size + kMvWarps - 1) / kMvWarps;
+  const int64_t per_cta = static_cast<int64_t>(kMvWarps) * std::max(cache->page_size, 32);
+  const int64_t groups = (keep + per_cta - 1) / per_cta;
   if (bh * groups > INT32_MAX) return SV_ERR_INVALID_ARG;
   EvictArgs a;
   a.c = view(*cache);
@@ -367,18 +371,18 @@ sv_status spec_kv_evict_q8(const sv_q8_cache* cache, int32_t B, const int32_t* s
   a.out_positions = out_positions;
   a.out_len = out_len;
   a.status = out_status;
-  a.src = static_cast<int32_t*>(workspace);
+  a.src = static_cast<uint32_t*>(workspace);
   a.movers = a.src + bh * keep;
-  a.holes = a.movers + bh * keep;
-  a.n_moves = a.holes + bh * keep;
+  a.n_moves = reinterpret_cast<int32_t*>(a.movers + bh * keep);
   a.B = B;
   a.S = S;
   a.keep = keep;
   a.sinks = sinks;
   a.n_keys = std::min(S, kEvMaxKeys);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const size_t smem = (kEvBins + static_cast<size_t>(kEvMaxKeys)) * sizeof(uint32_t);
-  cudaError_t e = launch_smem<kv_evict_select_kernel>(static_cast<int>(bh), kEvThreads, smem, smem, st, a);
+  const size_t smem = (kEvBins + static_cast<size_t>(a.n_keys)) * sizeof(uint32_t);
+  const size_t most = (kEvBins + static_cast<size_t>(kEvMaxKeys)) * sizeof(uint32_t);
+  cudaError_t e = launch_smem<kv_evict_select_kernel>(static_cast<int>(bh), kEvThreads, smem, most, st, a);
   if (e != cudaSuccess) return SV_ERR_CUDA;
   const int grid = static_cast<int>(bh * groups);
   return done(cache->D == 128 ? launch(kv_evict_move_kernel<128>, grid, kMvWarps * 32, 0, st, true, a)
@@ -430,11 +434,11 @@ sv_status spec_token_logprobs(const void* logits, int32_t dtype, int64_t row_str
   const int grid = rows * p.segs, join = (rows + kLpJoinWarps - 1) / kLpJoinWarps;
   cudaError_t e;
   if (es == 2)
-    e = n_top ? launch(token_logprobs_kernel<2, true>, grid, kLpThreads, 0, st, true, a)
-              : launch(token_logprobs_kernel<2, false>, grid, kLpThreads, 0, st, true, a);
+    e = n_top ? launch(token_logprobs_kernel<2, true>, grid, p.threads, 0, st, true, a)
+              : launch(token_logprobs_kernel<2, false>, grid, p.threads, 0, st, true, a);
   else
-    e = n_top ? launch(token_logprobs_kernel<4, true>, grid, kLpThreads, 0, st, true, a)
-              : launch(token_logprobs_kernel<4, false>, grid, kLpThreads, 0, st, true, a);
+    e = n_top ? launch(token_logprobs_kernel<4, true>, grid, p.threads, 0, st, true, a)
+              : launch(token_logprobs_kernel<4, false>, grid, p.threads, 0, st, true, a);
   if (e != cudaSuccess) return SV_ERR_CUDA;
   return done(es == 2 ? launch(token_logprobs_join_kernel<2>, join, kLpJoinWarps * 32, 0, st, true, a)
                       : launch(token_logprobs_join_kernel<4>, join, kLpJoinWarps * 32, 0, st, true, a));
@@ -474,10 +478,10 @@ sv_status spec_token_logprobs_backward(const void* logits, int32_t dtype, int64_
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int grid = rows * p.segs;
   if (es == 2)
-    return done(vec ? launch(token_logprobs_grad_kernel<2, true>, grid, kLpThreads, 0, st, true, a)
-                    : launch(token_logprobs_grad_kernel<2, false>, grid, kLpThreads, 0, st, true, a));
-  return done(vec ? launch(token_logprobs_grad_kernel<4, true>, grid, kLpThreads, 0, st, true, a)
-                  : launch(token_logprobs_grad_kernel<4, false>, grid, kLpThreads, 0, st, true, a));
+    return done(vec ? launch(token_logprobs_grad_kernel<2, true>, grid, p.threads, 0, st, true, a)
+                    : launch(token_logprobs_grad_kernel<2, false>, grid, p.threads, 0, st, true, a));
+  return done(vec ? launch(token_logprobs_grad_kernel<4, true>, grid, p.threads, 0, st, true, a)
+                  : launch(token_logprobs_grad_kernel<4, false>, grid, p.threads, 0, st, true, a));
 }
 
 }  // extern "C"

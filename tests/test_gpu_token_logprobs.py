@@ -83,6 +83,18 @@ def test_ties_masks_and_ranges(kind, dtype):
     check(x.to(dtype), [[17000, 2]], 1.0, 20)
 
 
+@pytest.mark.parametrize("n_top", [1, 20, 32])
+@pytest.mark.parametrize("left", [33, 500, 900, 4000])
+def test_a_range_of_tokens_left(left, n_top):
+    """All but a short range masked: few groups of threads have a maximum, and many elements reach their lowest."""
+    V = 70001
+    g = torch.Generator().manual_seed(left)
+    x = torch.randn((1, 3, V), generator=g).to(BF)
+    for r, at in enumerate((0, 16300, V - left)):
+        x[0, r, :at], x[0, r, at + left:] = -float("inf"), -float("inf")
+    check(x, [[0, 16300, 5]], 1.0, n_top)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_the_lowest_value_beside_masked_tokens(dtype):
     x = torch.full((1, 3, 9000), -float("inf"))
