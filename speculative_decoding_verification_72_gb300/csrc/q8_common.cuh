@@ -85,15 +85,18 @@ __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
 // Element types of q / new rows / outputs.
 struct TypeF32 {
   static constexpr int kBytes = 4;
-  // eight consecutive elements at a 16-byte aligned address
-  __device__ static void load8(const void* p, float* f) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w; f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-  }
 };
 struct TypeBf16 {
   static constexpr int kBytes = 2;
-  __device__ static void load8(const void* p, float* f) { Elem<2>::unpack(*reinterpret_cast<const uint4*>(p), f); }
+  __device__ static void unpack8(const uint4& w, float* f) { Elem<2>::unpack(w, f); }
+  // max that hands on NaN
+  __device__ static uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  __device__ static float value(uint16_t bits) { return __uint_as_float(static_cast<uint32_t>(bits) << 16); }
+  __device__ static void load8(const void* p, float* f) { unpack8(*reinterpret_cast<const uint4*>(p), f); }
   __device__ static void load4(const void* p, float* f) {
     const uint2 w = *reinterpret_cast<const uint2*>(p);
     f[0] = __uint_as_float(w.x << 16);
@@ -109,8 +112,14 @@ struct TypeBf16 {
 };
 struct TypeF16 {
   static constexpr int kBytes = 2;
-  __device__ static void load8(const void* p, float* f) {
-    const uint4 w = *reinterpret_cast<const uint4*>(p);
+  __device__ static uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  __device__ static float value(uint16_t bits) { return __half2float(__ushort_as_half(bits)); }
+  __device__ static void load8(const void* p, float* f) { unpack8(*reinterpret_cast<const uint4*>(p), f); }
+  __device__ static void unpack8(const uint4& w, float* f) {
     const float2 a = half2_bits(w.x), b = half2_bits(w.y), c = half2_bits(w.z), d = half2_bits(w.w);
     f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y; f[4] = c.x; f[5] = c.y; f[6] = d.x; f[7] = d.y;
   }

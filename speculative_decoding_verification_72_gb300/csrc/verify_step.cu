@@ -55,18 +55,29 @@ int esize(int32_t dtype) { return dtype == SV_F32 ? 4 : dtype == SV_BF16 || dtyp
 
 // ------------------------------------------------------------------ append
 
+// Passes of a CTA's threads over rows: as many as the new rows can touch, up to
+// four of 16-bit rows or two of 32-bit ones (64 or 128 bytes a thread held in
+// registers), and a page at least. Measured with 3 prompts of 4099 tokens, 8
+// heads of 128: bf16, pages of 16, four passes 17.4 us, two 18.4, one 20.5;
+// fp32, pages of 64, two passes 21.6 us, four 24.5.
+int append_passes(int64_t N, int P, int D, int es) {
+  const int per = kAppendThreads / (D / kAppendEls);
+  const int64_t rows = std::max<int64_t>(std::min<int64_t>(P - 1 + N, 8 / es * per), P);
+  const int passes = static_cast<int>((rows + per - 1) / per);
+  return passes == 3 ? 4 : passes;
+}
+
 template <typename T, int D>
-cudaError_t launch_append(const AppendArgs& a, int grid, int P, cudaStream_t st) {
-  const int passes = P * D / 8 / kAppendThreads;   // rows of a page over rows per pass
-  return passes <= 1   ? launch(kv_append_q8_kernel<T, D, 1>, grid, kAppendThreads, 0, st, true, a)
+cudaError_t launch_append(const AppendArgs& a, int passes, cudaStream_t st) {
+  const int grid = 2 * a.B * a.c.Hkv * a.W;
+  return passes == 1   ? launch(kv_append_q8_kernel<T, D, 1>, grid, kAppendThreads, 0, st, true, a)
          : passes == 2 ? launch(kv_append_q8_kernel<T, D, 2>, grid, kAppendThreads, 0, st, true, a)
-         : passes == 4 ? launch(kv_append_q8_kernel<T, D, 4>, grid, kAppendThreads, 0, st, true, a)
-                       : launch(kv_append_q8_kernel<T, D, 8>, grid, kAppendThreads, 0, st, true, a);
+                       : launch(kv_append_q8_kernel<T, D, 4>, grid, kAppendThreads, 0, st, true, a);
 }
 
 template <typename T>
-cudaError_t launch_append(const AppendArgs& a, int grid, int P, int D, cudaStream_t st) {
-  return D == 128 ? launch_append<T, 128>(a, grid, P, st) : launch_append<T, 64>(a, grid, P, st);
+cudaError_t launch_append(const AppendArgs& a, int passes, int D, cudaStream_t st) {
+  return D == 128 ? launch_append<T, 128>(a, passes, st) : launch_append<T, 64>(a, passes, st);
 }
 
 // --------------------------------------------------------------- attention
@@ -210,17 +221,18 @@ sv_status spec_kv_append_q8(const sv_q8_cache* cache, const sv_rows* k_new, cons
   a.num_acc = num_accepted;
   a.path_cols = path_cols;
   a.N = N;
-  const int64_t W = (static_cast<int64_t>(N) + cache->page_size - 1) / cache->page_size + 1;
-  a.W = static_cast<int32_t>(std::min<int64_t>(W, cache->max_pages));
+  const int P = cache->page_size, D = cache->D, passes = append_passes(N, P, D, es);
+  const int64_t rows = std::min<int64_t>(P - 1 + static_cast<int64_t>(N), static_cast<int64_t>(cache->max_pages) * P);
+  const int tile = passes * (kAppendThreads / (D / kAppendEls));
+  a.W = static_cast<int32_t>((rows + tile - 1) / tile);
+  a.B = B;
   a.out_len = out_len;
   a.status = out_status;
-  const int64_t grid = 2ll * B * cache->Hkv * a.W;
-  if (grid > INT32_MAX) return SV_ERR_INVALID_ARG;
+  if (2ll * B * cache->Hkv * a.W > INT32_MAX) return SV_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const int g = static_cast<int>(grid), P = cache->page_size, D = cache->D;
-  return done(dtype == SV_F32    ? launch_append<TypeF32>(a, g, P, D, st)
-              : dtype == SV_BF16 ? launch_append<TypeBf16>(a, g, P, D, st)
-                                 : launch_append<TypeF16>(a, g, P, D, st));
+  return done(dtype == SV_F32    ? launch_append<TypeF32>(a, passes, D, st)
+              : dtype == SV_BF16 ? launch_append<TypeBf16>(a, passes, D, st)
+                                 : launch_append<TypeF16>(a, passes, D, st));
 }
 
 size_t spec_attention_q8_workspace_size(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int32_t D) {
