@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kWtThreads, 2)
           const uint32_t m = n + i;
           const int tok = (cur.t0 + i) * kColTile + row;
           const float next = old_of(i + 2);
-          wait_or_fail(s_ready + 8 * set, (m / 2) & 1, fail);
+          const bool there = wait_or_fail(s_ready + 8 * set, (m / 2) & 1, fail);
           tc_fence_after();
           const float2 s = s_sc[(m & 15) * 8 + (row >> a.c.page_shift)];
           const bool edge = (cur.t0 + i + 1) * kColTile > rq.base;
@@ -337,7 +337,9 @@ __global__ void __launch_bounds__(kWtThreads, 2)
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(s_free + 8 * set);
-          if (tok < rq.len) out[tok] = old + (s.y != 0.f && rows_total > 0 ? w.x + w.y : 0.f);
+          float add = s.y != 0.f && rows_total > 0 ? w.x + w.y : 0.f;
+          if (!there) add = __int_as_float(0x7fc00000);   // no product came: NaN, whatever becomes of the status bit
+          if (tok < rq.len) out[tok] = old + add;
           old = next;
         }
         n += cur.n;
@@ -372,8 +374,9 @@ __global__ void __launch_bounds__(kWtThreads, 2)
       if (tid == 0) a.status[b] = bad ? SV_STATUS_BAD_PAGE : 0;
     }
   __syncthreads();
-  // A wait that gave up makes every request of the CTA's range suspect; the CTA
-  // that reports a request may be another, so the flag goes to all of them.
+  // A wait that gave up: its scores are NaN, and the flag goes to all requests.
+  // A CTA that reports a request later than this may write over the bit; the
+  // NaN stays.
   if (late && a.status)
     for (int b = tid; b < a.B; b += kWtThreads) atomicOr(&a.status[b], SV_STATUS_TIMEOUT);
   if (warp == 9) tmem_free(tmem, L::kTmem);
