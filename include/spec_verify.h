@@ -437,10 +437,12 @@ sv_status spec_verify_greedy_host(const void* target_logits, int32_t dtype, int6
  * accumulated attention weight, and eviction by it.
  *
  * K and V are e4m3 codes [num_pages, Hkv, page_size, D], contiguous, with fp32
- * scales [num_pages, Hkv]; a code stands for code * scale. Position p of
- * request b is slot p % page_size of page page_table[b, p / page_size].
+ * scales [num_pages, Hkv], not negative; a code stands for code * scale.
+ * Position p of request b is slot p % page_size of page page_table[b, p / page_size].
  * page_size is 16, 32, 64 or 128; D is 64 or 128; codes are 16-byte aligned.
- * Offsets into a cache are 64-bit. Entries of page_table past a request's
+ * Offsets into a cache are 64-bit. A call counts its work in 32 bits and
+ * returns SV_ERR_INVALID_ARG past that: B * Hkv * max_pages * page_size / 128
+ * must stay below 2^31 in the attention calls. Entries of page_table past a request's
  * length are not read. A page id outside [0, num_pages), a position outside
  * the page table or a node id outside [0, N) sets SV_STATUS_BAD_PAGE.
  * status pointers may be NULL. */
@@ -517,8 +519,8 @@ sv_status spec_attention_weights_q8(const sv_rows* q, int32_t dtype, const float
  * slots >= keep move, in order, into the slots < keep whose tokens go; a
  * page's scales become the largest of its slots' source pages' scales.
  * out_scores / out_positions [B, Hkv, S] follow the tokens (0 and -1 past
- * out_len[b] = min(seq_len[b], keep)) and may be the inputs. Requests no
- * longer than keep, or with a bad page, keep their tokens. */
+ * out_len[b] = min(seq_len[b], keep)) and may be the inputs; S is at most
+ * 2^30 and num_pages * Hkv * page_size at most 2^32. Requests no longer than keep, or with a bad page, keep their tokens. */
 size_t spec_kv_evict_q8_workspace_size(int32_t B, int32_t Hkv, int32_t keep);
 sv_status spec_kv_evict_q8(const sv_q8_cache* cache, int32_t B, const int32_t* seq_len, const float* scores,
                            const int32_t* positions, int32_t S, int32_t keep, int32_t sinks,
