@@ -82,10 +82,10 @@ cudaError_t launch_append(const AppendArgs& a, int passes, int D, cudaStream_t s
 
 // --------------------------------------------------------------- attention
 
-// Rows of a block: all of a kv head's as columns where they are at most 32
-// (in one or two groups of 16), else blocks of 128 lanes. At 33 to 64 rows the
-// row kernel's lanes are half empty, but two column kernels' traffic would cost
-// as much again.
+// Rows of a block: all of a kv head's as columns where they are at most 32 (in
+// one or two groups of 16), else blocks of 128 lanes. 32 requests of up to 8192
+// tokens, 8 heads of 128: 16 rows take 82 us in one group, 93 in two, 136 as
+// lanes; 24 rows 96 and 138 us, 32 rows 98 and 140; 64 rows 145 as lanes.
 int attn_block(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 128; }
 
 constexpr int kAttnGridMost = 320;   // CTAs a workspace is sized for: two an SM of 152, whatever the device
