@@ -35,6 +35,11 @@
 // taken out and their rows and columns noted for the end.
 //
 // Work split, partials and their join are attn_q8.cuh's.
+//
+// Measured: 32 requests of 6 rows over up to 8192 tokens, 32 heads on 8 of 128,
+// bf16: 95 us, 339 MB, 3.6 TB/s (without any softmax 89); one request of 1000
+// tokens, one row: 11 us. A tile costs its bytes; about 35 us a call are fixed:
+// first and edge tiles, query terms, the join.
 #pragma once
 
 #include <cuda.h>

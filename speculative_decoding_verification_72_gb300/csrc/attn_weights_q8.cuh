@@ -19,6 +19,9 @@
 // row, exact down to 2^-22 of the row's largest element; weights are formed and
 // summed in fp32. 64 rows a pass over the keys; more take more passes.
 //
+// Measured (the longest case of the operators' table, heads of 64, f16): 64 us,
+// bound by exponentials and TMEM reads; the bytes alone would take 28.
+//
 // Warps 0-3 take even tiles, 4-7 odd ones; 8: TMA; 9: MMA. Two CTAs an SM.
 #pragma once
 

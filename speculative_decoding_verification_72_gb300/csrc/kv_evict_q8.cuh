@@ -25,6 +25,10 @@
 // (24 requests of 8 heads are 192 CTAs: one wave, not two).
 // kv_evict_move_kernel, one warp per destination page (two pages of 16), moves
 // the rows.
+//
+// Measured: 24 prompts of up to 8192 tokens down to 4096, 8 heads of 128: 35 us
+// (17 select, 16 move), bound by latencies in a row (the bytes would take 14);
+// 2 requests of 1090 down to 1024: 11.8 us.
 #pragma once
 
 #include "q8_common.cuh"

