@@ -155,6 +155,9 @@ cudaError_t launch_weights(const sv_q8_cache& c, const WeightArgs& a, cudaStream
   return launch_smem<attn_weights_q8_kernel<T, D, MT, NT>>(a.grid, kWtThreads, kSmem, kSmem, st, k, a);
 }
 
+// Columns for the rows there are: 8 requests of up to 65536 tokens, 64 query
+// heads on 8 of 64, 16 rows 56.4 us (57.9 with columns for 64), 32 rows 58.4
+// (59.8).
 template <typename T, int D, int NT>
 cudaError_t launch_weights(const sv_q8_cache& c, const WeightArgs& a, int64_t rows, cudaStream_t st) {
   return rows <= 16   ? launch_weights<T, D, 1, NT>(c, a, st)
