@@ -156,8 +156,8 @@ cudaError_t launch_weights(const sv_q8_cache& c, const WeightArgs& a, cudaStream
 }
 
 // Columns for the rows there are: 8 requests of up to 65536 tokens, 64 query
-// heads on 8 of 64, 16 rows 56.4 us (57.9 with columns for 64), 32 rows 58.4
-// (59.8).
+// heads on 8 of 64, 16 rows 46.7 us (49.4 with columns for 64), 32 rows 53.1
+// (54.9).
 template <typename T, int D, int NT>
 cudaError_t launch_weights(const sv_q8_cache& c, const WeightArgs& a, int64_t rows, cudaStream_t st) {
   return rows <= 16   ? launch_weights<T, D, 1, NT>(c, a, st)
