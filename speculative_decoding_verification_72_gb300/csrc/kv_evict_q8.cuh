@@ -276,7 +276,9 @@ __global__ void __launch_bounds__(kEvThreads, 2) kv_evict_select_kernel(const Ev
     uint32_t at[kEvStep];
 #pragma unroll
     for (int i = 0; i < kEvStep; ++i) {
-      const int j = min(jj + i * kEvThreads, keep - 1);
+      // Past the budget: the thread's own first slot again. Another thread's mark may
+      // be gone by now, with a row of the pool in its place (src past n_keys).
+      const int j = jj + i * kEvThreads < keep ? jj + i * kEvThreads : jj;
       uint32_t fr = j < a.n_keys ? s_key[j] : src[j];
       if (fr & kEvHole) fr = movers[fr & ~kEvHole];
       at[i] = fr;

@@ -194,3 +194,13 @@ def test_attention_does_not_depend_on_the_order_of_slots():
     x = q64[0, 0] @ k.T * 0.125
     p = np.exp(x - x.max(1, keepdims=True))
     assert np.abs(got[0, 0] - p / p.sum(1, keepdims=True) @ v).max() < 2.0 ** -9 * 2
+
+
+def test_evict_several_heads_past_the_keys_held_in_shared_memory():
+    """Marks past the keys that fit lie in the list of rows itself, which each slot's thread overwrites: with several
+    heads and requests the rows there are far past a head's slots, and a budget that ends inside the last batch of slots
+    has threads with nothing to fetch beside others that write."""
+    lens, keep = [45000, 43100], 43072          # 43072 = 10 * 4096 + 2112
+    rng, c, t, s, pos = evict_problem(12, lens, keep, 3, 64, 64)
+    c["ks"][:], c["vs"][:] = 2.0 ** -7, 2.0 ** -6
+    run_evict(c, t, lens, s, pos, keep, sinks=4, protect=[n - 100 for n in lens])
