@@ -18,7 +18,9 @@
 // page's scales are scalars, sums over tokens stay in its registers until the
 // end, and P is one 16-byte store per 16 rows and term. The running maximum is
 // raised only when a score exceeds it by 2^6 (a vote per tile), which takes the
-// slow path: maxima across the CTA and a rescale of O^T in TMEM.
+// slow path: maxima across the CTA and a rescale of O^T in TMEM. So does every
+// tile until each row has seen a position, as a row's first maximum may lie
+// anywhere (the first positions of a piece may all be on no page).
 //
 // A token's vs is part of its exponent, P = 2^(s + log2 vs - m), with m the
 // maximum of s + log2 vs: whatever the pages' scales, a row's P fills e4m3's
@@ -329,7 +331,7 @@ __global__ void __launch_bounds__(ColLayout<D, MT, NT>::kThreads, 2)
 #pragma unroll
       for (int r = 0; r < 8; ++r) l[r] = make_float2(0.f, 0.f);
       float v0 = 1.f, iv0 = 1.f;
-      bool any_nan = false;
+      bool any_nan = false, unseen = true;   // unseen: a row with a node has seen no position yet
       // The products of tile m have read its P.
       auto p_done = [&](uint32_t m) { wait_or_fail(p_free + 8 * (m % L::kPb), (m / L::kPb) & 1, fail); };
 #pragma unroll 1
@@ -378,7 +380,7 @@ __global__ void __launch_bounds__(ColLayout<D, MT, NT>::kThreads, 2)
             top = fmaxf(fmaxf(top, x[r / 2].x), x[r / 2].y);
           }
         }
-        if (named_barrier_or(bar, 128, top > kColSlack + 2.f || !valid || edge || i == 0)) {
+        if (named_barrier_or(bar, 128, top > kColSlack + 2.f || !valid || edge || unseen)) {
           // ---- slow path: masks, maxima, V rows that must not be read
           uint32_t see = valid ? 0xffffu : 0u;
           const bool special = named_barrier_or(bar, 128, edge || !valid);   // the same for every group
@@ -461,6 +463,7 @@ __global__ void __launch_bounds__(ColLayout<D, MT, NT>::kThreads, 2)
             s_seen[r00 + row] = seen || mx != -INFINITY;
           }
           const bool changed = named_barrier_or(bar, 128, row < 16 && s_f[r00 + (row & 15)] != 1.f);
+          unseen = __any_sync(0xffffffffu, lane < 16 && s_node[r00 + (lane & 15)] >= 0 && !s_seen[r00 + (lane & 15)]);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const float2 up = reinterpret_cast<const float2*>(s_up + r00)[j];

@@ -255,3 +255,21 @@ def test_weights_of_bad_requests():
     r = sv.spec_attention_weights_q8(q, lse, cache, i32(t), bs, s, path_nodes=i32(path), num_accepted=i32([2, 2, 2]))
     assert r["status"].tolist() == [0, sv.STATUS_BAD_PAGE, sv.STATUS_BAD_PAGE]
     assert torch.equal(r["scores"][1, 0, :16], s[1, 0, :16]) and torch.isfinite(r["scores"]).all()
+
+
+@pytest.mark.parametrize("offset", [0.0, -60.0, 60.0])
+@pytest.mark.parametrize("N,G,dtype,D", [(1, 2, BF, 64), (6, 4, BF, 128), (6, 2, HF, 64), (9, 4, BF, 64)])
+def test_first_positions_on_no_page(N, G, dtype, D, offset):
+    """A request whose first 128 positions have no page (a prefix that was dropped), and some later ones: the rest is
+    attended to as if alone, however high or low its scores. Enough requests that a CTA has several tiles of one."""
+    B, P = 240, 64
+    base = [500] * B
+    rng, c, t, q, q64 = problem(40 + N, base, N, 2, G, D, P, dtype, q_std=1.0)
+    c["k"][..., 0], c["ks"][:] = K.encode(128.0), 2.0 ** -7      # every key begins with 1
+    q[..., 0] = offset * D ** 0.5                               # so that this adds `offset` to every score
+    q64 = q.double().cpu().numpy()
+    t[:, :2] = -1
+    t[::3, 2] = -1
+    r = sv.spec_attention_q8(q, to_gpu(c), i32(t), i32(base))
+    check_attention(r, K.attention(q64, c, t, base, sm=D ** -0.5), dtype)
+    assert r["status"].tolist() == [sv.STATUS_BAD_PAGE] * B
