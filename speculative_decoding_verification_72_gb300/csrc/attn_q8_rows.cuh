@@ -37,6 +37,8 @@
 // the rows that see a NaN code note its column in registers.
 #pragma once
 
+#include <algorithm>
+
 #include <cuda.h>
 
 #include "attn_q8_cols.cuh"
@@ -58,8 +60,10 @@ struct RowLayout {
   static constexpr int kOffV = kOffK + kKs * kTileBytes;
   static constexpr int kOffMisc = kOffV + kVb * kVBytes;
   static constexpr int kMiscBytes = kVb * 128 * (D / 32) * 4 + 1024 + 128 * 4 + 256 * 12 + 256 * 4;
+  // Nodes that a block's 128 rows can belong to, G rows a node.
+  static int nodes(int N, int G) { return std::min(N, (126 + G) / G + 1); }
   static int bytes(int nodes, int words) { return 1024 + kOffMisc + kMiscBytes + nodes * words * 4; }
-  static int most() { return bytes(128, SV_MAX_TREE_NODES / 32); }
+  static int most() { return bytes(nodes(SV_MAX_TREE_NODES, 1), SV_MAX_TREE_NODES / 32); }
 };
 
 // O (TMEM) = P (TMEM, f16) V (shared memory, f16) (+ O if acc).

@@ -132,7 +132,7 @@ cudaError_t launch_rows(const sv_q8_cache& c, AttnArgs& a, int64_t items, cudaSt
   CUtensorMap k;
   if (!code_map(c, c.k, &k)) return cudaErrorInvalidValue;
   using L = RowLayout<D, NT>;
-  const int smem = L::bytes(std::min(a.N, 127 / a.G + 2), (a.N + 31) / 32);
+  const int smem = L::bytes(L::nodes(a.N, a.G), (a.N + 31) / 32);
   if (2 * (smem + 1024) > 228 * 1024) a.grid = std::min(a.grid, sm_count());   // one CTA an SM
   const cudaError_t e = launch_smem<attn_q8_rows_kernel<T, D, NT>>(a.grid, kRowThreads, smem, L::most(), st, k, a);
   return e != cudaSuccess ? e : launch_join<T, D, 8>(a, items, st);

@@ -273,3 +273,15 @@ def test_first_positions_on_no_page(N, G, dtype, D, offset):
     r = sv.spec_attention_q8(q, to_gpu(c), i32(t), i32(base))
     check_attention(r, K.attention(q64, c, t, base, sm=D ** -0.5), dtype)
     assert r["status"].tolist() == [sv.STATUS_BAD_PAGE] * B
+
+
+@pytest.mark.parametrize("N,D,dtype,tree", [(992, 64, BF, False), (993, 64, HF, True), (1000, 128, BF, False), (1024, 128, HF, False),
+                                            (1024, 128, BF, True), (1024, 64, BF, True)])
+def test_most_nodes_of_a_single_head(N, D, dtype, tree):
+    """One query head a kv head, so that a block's 128 rows are 128 nodes, up to the most nodes there can be."""
+    base = [70]
+    rng, c, t, q, q64 = problem(50, base, N, 1, 1, D, 64, dtype)
+    par = np.array([[-1] + [int(rng.integers(0, n)) for n in range(1, N)]]) if tree else None
+    r = sv.spec_attention_q8(q, to_gpu(c), i32(t), i32(base), parents=None if par is None else i32(par))
+    check_attention(r, K.attention(q64, c, t, base, par, sm=D ** -0.5), dtype)
+    assert r["status"].tolist() == [0]
