@@ -264,6 +264,7 @@ __global__ void __launch_bounds__(ColLayout<D, MT, NT>::kThreads, 2)
     const int rows_total = a.N * a.G, words = (a.N + 31) / 32;
     float* max_w = s_max + warp * 20;
     const float* max_g = s_max + grp * 80;
+    uint32_t* unseen = reinterpret_cast<uint32_t*>(s_max + grp * 80 + 16);   // whether a row with a node has seen no position yet
     // A wait that gives up ends no loop here: these warps meet at barriers, so all
     // run on to the end (every later wait then returns at once), without meaning.
     for (; cur.pos < hi; cur.pos += cur.n) {
@@ -307,6 +308,7 @@ __global__ void __launch_bounds__(ColLayout<D, MT, NT>::kThreads, 2)
         }
       }
       for (int i = tid; i < R * (D / 32); i += kSoft) s_nan[i] = 0;
+      if (row == 0) *unseen = 1;
       const bool tail = (cur.t0 + cur.n) * kColTile > rq.base;
       if (tail && a.parents) {
         const int nodes = min(attn_node(a, row0 + R - 1), a.N - 1) - node0 + 1;
@@ -331,7 +333,7 @@ __global__ void __launch_bounds__(ColLayout<D, MT, NT>::kThreads, 2)
 #pragma unroll
       for (int r = 0; r < 8; ++r) l[r] = make_float2(0.f, 0.f);
       float v0 = 1.f, iv0 = 1.f;
-      bool any_nan = false, unseen = true;   // unseen: a row with a node has seen no position yet
+      bool any_nan = false;
       // The products of tile m have read its P.
       auto p_done = [&](uint32_t m) { wait_or_fail(p_free + 8 * (m % L::kPb), (m / L::kPb) & 1, fail); };
 #pragma unroll 1
@@ -380,7 +382,7 @@ __global__ void __launch_bounds__(ColLayout<D, MT, NT>::kThreads, 2)
             top = fmaxf(fmaxf(top, x[r / 2].x), x[r / 2].y);
           }
         }
-        if (named_barrier_or(bar, 128, top > kColSlack + 2.f || !valid || edge || unseen)) {
+        if (named_barrier_or(bar, 128, top > kColSlack + 2.f || !valid || edge || *unseen)) {
           // ---- slow path: masks, maxima, V rows that must not be read
           uint32_t see = valid ? 0xffffu : 0u;
           const bool special = named_barrier_or(bar, 128, edge || !valid);   // the same for every group
@@ -461,9 +463,10 @@ __global__ void __launch_bounds__(ColLayout<D, MT, NT>::kThreads, 2)
             s_f[r00 + row] = seen ? ex2(-up) : 1.f;
             s_m0[r00 + row] += up;
             s_seen[r00 + row] = seen || mx != -INFINITY;
+            const uint32_t none = __ballot_sync(0xffffu, s_node[r00 + row] >= 0 && !seen && mx == -INFINITY);
+            if (row == 0) *unseen = none;
           }
           const bool changed = named_barrier_or(bar, 128, row < 16 && s_f[r00 + (row & 15)] != 1.f);
-          unseen = __any_sync(0xffffffffu, lane < 16 && s_node[r00 + (lane & 15)] >= 0 && !s_seen[r00 + (lane & 15)]);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const float2 up = reinterpret_cast<const float2*>(s_up + r00)[j];
