@@ -9,7 +9,7 @@ import ctypes
 
 import torch
 
-from .verify import _SIGS
+from .verify import SpecVerifyError, _SIGS
 from .kv_q8 import binding
 
 MAX_TOP_ALTERNATIVES = 32
@@ -52,10 +52,23 @@ class _TokenLogprobs(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, g, h):
-        logits, tokens, saved = ctx.saved_tensors
-        return spec_token_logprobs_backward(logits, tokens, saved, g, h, ctx.temperature), None, None
+        return _TokenLogprobsGrad.apply(*ctx.saved_tensors, g, h, ctx.temperature), None, None
+
+
+class _TokenLogprobsGrad(torch.autograd.Function):
+    """The gradient, with an error in place of the second derivative: with create_graph=True the gradient depends on
+    logits even where g and h do not require one, and must not count as a constant."""
+
+    @staticmethod
+    def forward(ctx, logits, tokens, saved, g, h, temperature):
+        return spec_token_logprobs_backward(logits, tokens, saved, g, h, temperature)
+
+    @staticmethod
+    def backward(ctx, d):
+        raise SpecVerifyError("token_logprobs can be differentiated once, not twice")
 
 
 def token_logprobs(logits, tokens, temperature=1.0):
-    """(logprob, entropy), each [B, R] float32, of spec_token_logprobs; differentiable with respect to logits."""
+    """(logprob, entropy), each [B, R] float32, of spec_token_logprobs; differentiable with respect to logits, once (a
+    second derivative raises SpecVerifyError)."""
     return _TokenLogprobs.apply(logits, tokens, temperature)

@@ -203,3 +203,17 @@ def test_graph_and_own_buffers():
     torch.cuda.synchronize()
     for k in want:
         assert torch.equal(out[k], want[k]), k
+
+
+@pytest.mark.parametrize("of", ["logprob", "entropy", "product"])
+def test_a_second_derivative_is_an_error(of):
+    """Also where the upstream gradients are constants, as a sum's are: the gradient still depends on the logits."""
+    x = torch.randn((1, 2, 40), generator=torch.Generator().manual_seed(11)).to(DEV).requires_grad_()
+    tok = torch.tensor([[3, 39]], dtype=torch.int32, device=DEV)
+    lp, ent = sv.token_logprobs(x, tok)
+    loss = dict(logprob=lp, entropy=ent, product=lp * ent)[of].sum()
+    first, = torch.autograd.grad(loss, x, retain_graph=True)
+    again, = torch.autograd.grad(loss, x, create_graph=True)
+    assert torch.equal(first, again) and not first.requires_grad
+    with pytest.raises(sv.SpecVerifyError):
+        (sv.token_logprobs(x, tok)[0].sum() + (again ** 2).sum()).backward()
