@@ -17,6 +17,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGraphsC10Utils.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -130,7 +131,9 @@ struct Outputs {
 };
 
 // One workspace per device and stream, grown as needed (never shared by calls
-// that can overlap); kept for the life of the process.
+// that can overlap); kept for the life of the process. A call that is being
+// captured in a graph gets one of its own from the graph's memory: replays go on
+// using its address, whatever becomes of the kept one.
 at::Tensor workspace(PyObject* own, size_t need, at::Device dev, void* stream) {
   if (need == 0) refuse("invalid sizes");
   if (given(own)) {
@@ -139,6 +142,8 @@ at::Tensor workspace(PyObject* own, size_t need, at::Device dev, void* stream) {
       refuse("workspace must be a contiguous CUDA tensor of at least " + std::to_string(need) + " bytes");
     return t;
   }
+  auto fresh = [&] { return at::empty({static_cast<int64_t>(need)}, at::TensorOptions().dtype(at::kByte).device(dev)); };
+  if (c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None) return fresh();
   struct Key {
     int dev;
     void* stream;
@@ -149,8 +154,7 @@ at::Tensor workspace(PyObject* own, size_t need, at::Device dev, void* stream) {
   };
   static auto* kept = new std::unordered_map<Key, at::Tensor, Hash>();   // guarded by the GIL
   at::Tensor& t = (*kept)[Key{dev.index(), stream}];
-  if (!t.defined() || t.nbytes() < need)
-    t = at::empty({static_cast<int64_t>(need)}, at::TensorOptions().dtype(at::kByte).device(dev));
+  if (!t.defined() || t.nbytes() < need) t = fresh();
   return t;
 }
 

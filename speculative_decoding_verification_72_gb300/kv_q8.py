@@ -4,9 +4,11 @@ spec_attention_weights_q8 and spec_kv_evict_q8 (include/spec_verify.h).
 As in ``verify``: torch CUDA tensors in, outputs and workspaces allocated by
 the call unless given, work enqueued on the current stream of the cache's
 device, SpecVerifyError on anything the call cannot take. With ``out`` (and
-``workspace``, where a function has one) given, a call allocates nothing and
-can be captured in a CUDA graph. The arguments are checked and marshalled by
-csrc/binding.cpp; ``_SIGS`` declares the C entry points for direct use.
+``workspace``, where a function has one) given, a call allocates nothing.
+Calls can be captured in a CUDA graph (torch.cuda.graph); what they allocate
+then, a workspace among it, is the graph's own. The arguments are checked and
+marshalled by csrc/binding.cpp; ``_SIGS`` declares the C entry points for
+direct use.
 """
 
 from __future__ import annotations
