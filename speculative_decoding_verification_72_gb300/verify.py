@@ -181,6 +181,10 @@ def _f32(t, name, shape, device):
 
 
 def _workspace(nbytes, device, stream):
+    # A call that is being captured in a graph gets one of its own from the graph's memory: replays
+    # go on using its address, whatever becomes of the one kept for the stream.
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
     key = (device.index, stream)
     ws = _WS.get(key)
     if ws is None or ws.numel() < nbytes:

@@ -48,7 +48,23 @@ def logprobs(large):
     return (lambda: sv.spec_token_logprobs(x, tok, n_top=8)), lib.spec_token_logprobs_workspace_size(2 * R, V, 1, 8)
 
 
-CALLS = [attention, evict, logprobs]
+def greedy(large):
+    B, K, V = (64, 5, 60000) if large else (2, 5, 9000)
+    x = torch.randn((B, K + 1, V), generator=torch.Generator().manual_seed(3)).to(BF).to(DEV)
+    d = x[:, :K].argmax(-1).int()
+    d[0, 2] = 0
+    lib = sv.load_library()
+    return (lambda: sv.spec_verify_greedy(x, d)), lib.spec_verify_greedy_workspace_size(B, K, V, 1)
+
+
+def tree_build(large):
+    B, V = (16, 60000) if large else (2, 9000)
+    x = torch.randn((B, 9, V), generator=torch.Generator().manual_seed(4)).to(BF).to(DEV)
+    lib = sv.load_library()
+    return (lambda: sv.spec_tree_build(x, 3, 4, 16)), lib.spec_tree_build_workspace_size(B, 3, 4, V)
+
+
+CALLS = [attention, evict, logprobs, greedy, tree_build]
 
 
 @pytest.mark.parametrize("warm", [True, False])
