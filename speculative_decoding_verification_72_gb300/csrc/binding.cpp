@@ -11,6 +11,8 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
+#include <algorithm>
+#include <cstdint>
 #include <string>
 #include <unordered_map>
 #include <utility>
@@ -64,6 +66,8 @@ double real(PyObject* o) {
 bool same_shape(c10::IntArrayRef a, c10::IntArrayRef b) { return a == b; }
 
 // int32 contiguous tensor on dev: the caller's own where it is one, else a copy.
+// Wider integers are brought into int32's range, not cut off to its bits: past
+// it a position, length or token is as far out of range as at its end.
 at::Tensor ints(PyObject* o, const char* name, c10::IntArrayRef shape, at::Device dev) {
   at::Tensor t;
   if (THPVariable_Check(o)) {
@@ -76,6 +80,7 @@ at::Tensor ints(PyObject* o, const char* name, c10::IntArrayRef shape, at::Devic
   }
   if (!same_shape(t.sizes(), shape)) refuse(std::string(name) + " must have shape " + show(shape) + ", got " + show(t.sizes()));
   if (t.scalar_type() == at::kInt && t.device() == dev && t.is_contiguous()) return t;
+  if (t.scalar_type() == at::kLong) t = t.clamp(INT32_MIN, INT32_MAX);
   return t.to(dev, at::kInt).contiguous();
 }
 
@@ -318,7 +323,7 @@ PyObject* kv_evict(PyObject* const* a) {
   const c10::cuda::CUDAGuard guard(c.dev);
   check_dense(scores, "scores", {B, c.H, S}, at::kFloat, c.dev);
   check_dense(positions, "positions", {B, c.H, S}, at::kInt, c.dev);
-  const int64_t keep = integer(a[5]), sinks = integer(a[6]);
+  const int64_t keep = integer(a[5]), sinks = std::min<int64_t>(std::max<int64_t>(integer(a[6]), INT32_MIN), INT32_MAX);
   if (keep < c.P || keep % c.P != 0 || keep > S)
     refuse("keep must be a positive multiple of the page size " + std::to_string(c.P) + ", at most " + std::to_string(S));
   const at::Tensor n = ints(a[2], "seq_len", {B}, c.dev);

@@ -204,3 +204,23 @@ def test_evict_several_heads_past_the_keys_held_in_shared_memory():
     rng, c, t, s, pos = evict_problem(12, lens, keep, 3, 64, 64)
     c["ks"][:], c["vs"][:] = 2.0 ** -7, 2.0 ** -6
     run_evict(c, t, lens, s, pos, keep, sinks=4, protect=[n - 100 for n in lens])
+
+
+@pytest.mark.parametrize("sinks,protect", [(10 ** 12, None), (-10 ** 12, None), (0, 2 ** 63 - 1), (0, -2 ** 63), (0, 2 ** 32 + 150)])
+def test_evict_integers_past_32_bits(sinks, protect):
+    lens, keep = [200], 64
+    rng, c, t, s, pos = evict_problem(13, lens, keep, 1, 64, 16)
+    want = K.evict(c, t, lens, s, pos, keep, sinks, None if protect is None else [protect])
+    r = sv.spec_kv_evict_q8(to_gpu(c), i32(t), i32(lens), torch.from_numpy(s).to(DEV), torch.from_numpy(pos).to(DEV), keep, sinks,
+                            None if protect is None else torch.tensor([protect], device=DEV))
+    assert np.array_equal(r["positions"].cpu().numpy(), want[2])
+
+
+def test_lengths_past_32_bits_are_out_of_range():
+    rng = np.random.default_rng(14)
+    c, t = host_cache(rng, 4, 1, 16, 64), table(rng, [20, 20], 16, 4)
+    k, k64 = rows(rng, (2, 4, 1, 64), BF)
+    cache = to_gpu(c)
+    r = sv.spec_kv_append_q8(cache, k, k, i32(t), torch.tensor([2 ** 32 + 5, -2 ** 32 + 5]))
+    assert r["status"].tolist() == [sv.STATUS_BAD_PAGE] * 2
+    same_cache(to_host(cache), c)

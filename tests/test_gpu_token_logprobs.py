@@ -217,3 +217,10 @@ def test_a_second_derivative_is_an_error(of):
     assert torch.equal(first, again) and not first.requires_grad
     with pytest.raises(sv.SpecVerifyError):
         (sv.token_logprobs(x, tok)[0].sum() + (again ** 2).sum()).backward()
+
+
+def test_tokens_past_32_bits_are_out_of_range():
+    x = torch.randn((1, 3, 50), generator=torch.Generator().manual_seed(12)).to(DEV)
+    r = sv.spec_token_logprobs(x, torch.tensor([[2 ** 32 + 3, 3, -2 ** 32 + 3]], device=DEV))
+    bad = sv.STATUS_BAD_TOKEN
+    assert r["status"].tolist() == [[bad, 0, bad]] and r["logprob"][0, 0] == 0 and r["logprob"][0, 2] == 0
