@@ -203,22 +203,24 @@ Cache cache_of(PyObject* o, PyObject* table, int64_t B) {
   return r;
 }
 
-// A [B, N, heads, D] tensor as it lies, or a copy where the kernels cannot read it so.
+// A [B, N, heads, D] tensor as it lies, or a copy where the kernels cannot read it so. The stride of a dimension of
+// one is never taken, whatever it is.
 std::pair<sv_rows, at::Tensor> rows_of(const at::Tensor& given_t, const char* name, int64_t heads, int64_t D, at::Device dev) {
   at::Tensor t = given_t;
   if (t.dim() != 4 || t.size(2) != heads || t.size(3) != D || t.device() != dev)
     refuse(std::string(name) + " must be [B, N, " + std::to_string(heads) + ", " + std::to_string(D) + "] on " + dev.str() +
            ", got " + show(t.sizes()) + " on " + t.device().str());
   const int64_t es = t.element_size();
+  auto stride = [&](int64_t d) { return t.size(d) == 1 ? 0 : t.stride(d); };
   auto lies_well = [&] {
-    return t.stride(3) == 1 && reinterpret_cast<uintptr_t>(t.data_ptr()) % 16 == 0 && t.stride(0) * es % 16 == 0 &&
-           t.stride(1) * es % 16 == 0 && t.stride(2) * es % 16 == 0;
+    return t.stride(3) == 1 && reinterpret_cast<uintptr_t>(t.data_ptr()) % 16 == 0 && stride(0) * es % 16 == 0 &&
+           stride(1) * es % 16 == 0 && stride(2) * es % 16 == 0;
   };
   if (!lies_well()) {
     t = t.contiguous();
     if (!lies_well()) t = t.clone();
   }
-  return {sv_rows{t.data_ptr(), t.stride(0), t.stride(1), t.stride(2)}, t};
+  return {sv_rows{t.data_ptr(), stride(0), stride(1), stride(2)}, t};
 }
 
 struct Path {

@@ -285,3 +285,20 @@ def test_most_nodes_of_a_single_head(N, D, dtype, tree):
     r = sv.spec_attention_q8(q, to_gpu(c), i32(t), i32(base), parents=None if par is None else i32(par))
     check_attention(r, K.attention(q64, c, t, base, par, sm=D ** -0.5), dtype)
     assert r["status"].tolist() == [0]
+
+
+def test_dimensions_of_one_have_any_stride():
+    base = [40]
+    rng, c, t, q, q64 = problem(51, base, 1, 1, 4, 64, 16, BF)
+    cache, tab, bs = to_gpu(c), i32(t), i32(base)
+    odd = q.as_strided(q.shape, (3, 5, 64, 1))
+    r = sv.spec_attention_q8(odd, cache, tab, bs)
+    check_attention(r, K.attention(q64, c, t, base, sm=0.125), BF)
+    s = torch.zeros((1, 1, t.shape[1] * 16), device=DEV)
+    w = [sv.spec_attention_weights_q8(x, r["lse"], cache, tab, bs, s)["scores"] for x in (q, odd)]
+    assert torch.equal(*w)
+    k = q[:, :, :1]
+    caches = [to_gpu(c), to_gpu(c)]
+    for x, into in zip((k.contiguous(), k.as_strided(k.shape, (3, 5, 7, 1))), caches):
+        assert sv.spec_kv_append_q8(into, x, x, tab, bs)["status"].tolist() == [0]
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(*caches))
