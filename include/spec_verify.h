@@ -502,7 +502,8 @@ sv_status spec_attention_q8(const sv_rows* q, int32_t dtype, const sv_q8_cache* 
  * or all N if NULL) of request b is node path_nodes[b, i] (or i) of the verify
  * pass, at position seq_base[b] + i, and sees the positions up to its own. w[b, hk, j] is the
  * sum over those rows and the heads of group hk of exp(score - lse), with lse
- * [B, N, Hq] from spec_attention_q8. out_scores [B, Hkv, S] = decay * scores +
+ * [B, N, Hq] from spec_attention_q8; a row whose lse is -inf saw nothing and
+ * gives nothing. out_scores [B, Hkv, S] = decay * scores +
  * w below seq_base, w from there to the last row's position, 0 past it.
  * out_scores may be scores. */
 sv_status spec_attention_weights_q8(const sv_rows* q, int32_t dtype, const float* lse, const sv_q8_cache* cache,

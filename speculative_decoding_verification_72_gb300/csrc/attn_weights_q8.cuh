@@ -295,7 +295,9 @@ __global__ void __launch_bounds__(kWtThreads, 2)
             // Infinities saturate in e4m3, so the factor makes their row NaN (NaN codes stay NaN).
             s_cq[r] = m == INFINITY ? __int_as_float(0x7fc00000) : exp2_int(-x) * a.coef;
             s_at[r] = node >= 0 ? at : -1;
-            s_l2[r] = node >= 0 ? a.lse[(static_cast<int64_t>(cur.b) * a.N + node) * a.Hq + cur.h * a.G + g] * kLog2e : INFINITY;
+            // A row that saw nothing (lse -inf) gives no weight, like one that does not count.
+            const float l2 = node >= 0 ? a.lse[(static_cast<int64_t>(cur.b) * a.N + node) * a.Hq + cur.h * a.G + g] * kLog2e : INFINITY;
+            s_l2[r] = l2 == -INFINITY ? INFINITY : l2;
           }
         }
         fence_async_smem();

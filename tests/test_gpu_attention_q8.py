@@ -302,3 +302,18 @@ def test_dimensions_of_one_have_any_stride():
     for x, into in zip((k.contiguous(), k.as_strided(k.shape, (3, 5, 7, 1))), caches):
         assert sv.spec_kv_append_q8(into, x, x, tab, bs)["status"].tolist() == [0]
     assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(*caches))
+
+
+@pytest.mark.parametrize("N,G,D", [(4, 4, 64), (6, 2, 128), (20, 4, 64)])
+def test_weights_of_rows_that_saw_nothing(N, G, D):
+    """Rows past n_nodes, whose lse is -inf, give no weight where all rows are counted."""
+    base = [40, 0, 70, 3]
+    rng, c, t, q, q64 = problem(52, base, N, 2, G, D, 16, BF)
+    cache, tab, bs, nn = to_gpu(c), i32(t), i32(base), i32([2, 0, N, 0])
+    lse = sv.spec_attention_q8(q, cache, tab, bs, n_nodes=nn)["lse"]
+    s = torch.from_numpy(rng.random((4, 2, t.shape[1] * 16)).astype(np.float32)).to(DEV)
+    got = sv.spec_attention_weights_q8(q, lse, cache, tab, bs, s)
+    want = sv.spec_attention_weights_q8(q, lse, cache, tab, bs, s, num_accepted=nn - 1)
+    assert torch.isfinite(got["scores"]).all() and torch.equal(got["scores"], want["scores"])
+    assert torch.equal(got["scores"][3, :, :3], s[3, :, :3])
+    assert got["status"].tolist() == want["status"].tolist() == [0] * 4
