@@ -82,6 +82,13 @@ cudaError_t launch_append(const AppendArgs& a, int passes, int D, cudaStream_t s
 
 // --------------------------------------------------------------- attention
 
+// Rows of a kv head that a call takes. A row's node is the high word of a product
+// with inv_g, which is over 2^32 / G by `over` / G: exact for rows below 2^32 / over.
+bool valid_row_count(int64_t rows, int64_t G, uint64_t inv_g) {
+  const int64_t over = static_cast<int64_t>(inv_g * G - (uint64_t{1} << 32));
+  return rows <= SV_MAX_TREE_NODES * 1024 && rows * over <= int64_t{1} << 32;
+}
+
 // Rows of a block: all of a kv head's as columns where they are at most 32 (in
 // one or two groups of 16), else blocks of 128 lanes. 32 requests of up to 8192
 // tokens, 8 heads of 128: 16 rows take 82 us in one group, 93 in two, 136 as
@@ -276,7 +283,7 @@ sv_status spec_attention_q8(const sv_rows* q, int32_t dtype, const sv_q8_cache* 
   a.G = Hq / cache->Hkv;
   a.inv_g = ((1ull << 32) + a.G - 1) / a.G;
   const int64_t rows = static_cast<int64_t>(N) * a.G;
-  if (rows > SV_MAX_TREE_NODES * 1024) return SV_ERR_INVALID_ARG;
+  if (!valid_row_count(rows, a.G, a.inv_g)) return SV_ERR_INVALID_ARG;
   const int block = attn_block(rows);
   a.RB = static_cast<int32_t>((rows + block - 1) / block);
   a.coef = static_cast<float>(static_cast<double>(sm_scale) * 1.4426950408889634);
@@ -339,8 +346,8 @@ sv_status spec_attention_weights_q8(const sv_rows* q, int32_t dtype, const float
   a.coef = static_cast<float>(static_cast<double>(sm_scale) * 1.4426950408889634);
   a.decay = decay;
   const int64_t rows = static_cast<int64_t>(path_nodes ? std::min(path_cols, N) : N) * a.G;
-  if (rows > SV_MAX_TREE_NODES * 1024) return SV_ERR_INVALID_ARG;
   a.inv_g = ((1ull << 32) + a.G - 1) / a.G;
+  if (!valid_row_count(rows, a.G, a.inv_g)) return SV_ERR_INVALID_ARG;
   const int64_t items = static_cast<int64_t>(B) * cache->Hkv;
   const int64_t tiles = (static_cast<int64_t>(cache->max_pages) * cache->page_size + kColTile - 1) / kColTile;
   if (items > INT32_MAX || items * tiles > INT32_MAX) return SV_ERR_INVALID_ARG;

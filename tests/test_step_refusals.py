@@ -165,3 +165,14 @@ def test_binding_refuses_cpu_tensors_and_wrong_shapes(lib):
         sv.spec_token_logprobs(torch.zeros((1, 1, 8)), torch.zeros((1, 1), dtype=torch.int32))
     with pytest.raises(sv.SpecVerifyError):
         sv.q8_cache(4, 2, 24, 64)
+
+
+def test_rows_whose_node_is_not_exact(lib):
+    """A row's node is a product with 2^32 / G rounded up, which is exact for few enough rows: 131071 heads on one kv head
+    were taken, and the last row of node 0 went to node 1."""
+    g = 131071
+    assert (g - 1) * -(-(1 << 32) // g) >> 32 == 1
+    one = cache(Hkv=1)
+    for n, heads in ((8, g), (1, g), (8, 30011), (1, 1 << 21)):
+        assert attention(lib, one, N=n, Hq=heads) == INVALID, (n, heads)
+        assert weights(lib, one, N=n, Hq=heads) == INVALID, (n, heads)
