@@ -440,7 +440,8 @@ sv_status spec_verify_greedy_host(const void* target_logits, int32_t dtype, int6
  * scales [num_pages, Hkv], not negative; a code stands for code * scale.
  * Position p of request b is slot p % page_size of page page_table[b, p / page_size].
  * page_size is 16, 32, 64 or 128; D is 64 or 128; codes are 16-byte aligned.
- * Offsets into a cache are 64-bit. A call counts its work in 32 bits and
+ * Offsets into a cache are 64-bit; max_pages * page_size, the positions of a
+ * request, is at most 2^31 - 256. A call counts its work in 32 bits and
  * returns SV_ERR_INVALID_ARG past that: B * Hkv * max_pages * page_size / 128
  * must stay below 2^31 in the attention calls. Entries of page_table past a request's
  * length are not read. A page id outside [0, num_pages), a position outside

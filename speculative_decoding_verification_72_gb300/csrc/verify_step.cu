@@ -29,7 +29,7 @@ bool valid_cache(const sv_q8_cache* c) {
          aligned(c->k_scale, 4) && aligned(c->v_scale, 4) && aligned(c->page_table, 4) && c->num_pages >= 1 &&
          c->Hkv >= 1 && (c->D == 64 || c->D == 128) &&
          (c->page_size == 16 || c->page_size == 32 || c->page_size == 64 || c->page_size == 128) && c->max_pages >= 1 &&
-         static_cast<int64_t>(c->max_pages) * c->page_size <= INT32_MAX;
+         static_cast<int64_t>(c->max_pages) * c->page_size <= INT32_MAX - 255;   // positions and the ends of their tiles fit
 }
 
 Q8View view(const sv_q8_cache& c) {

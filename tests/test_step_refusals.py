@@ -176,3 +176,11 @@ def test_rows_whose_node_is_not_exact(lib):
     for n, heads in ((8, g), (1, g), (8, 30011), (1, 1 << 21)):
         assert attention(lib, one, N=n, Hq=heads) == INVALID, (n, heads)
         assert weights(lib, one, N=n, Hq=heads) == INVALID, (n, heads)
+
+
+def test_positions_whose_tiles_end_past_32_bits(lib):
+    """A length of 2^31 - 100 is 2^24 tiles of 128, the last of which ends past 2^31: counted in 32 bits it came out as one."""
+    for page, most in ((16, (1 << 31) // 16 - 16), (128, (1 << 31) // 128 - 2)):
+        for pages in (most + 1, (1 << 31) // page - 1):
+            c = cache(page_size=page, max_pages=pages, Hkv=1)
+            assert append(lib, c) == attention(lib, c) == weights(lib, c) == evict(lib, c) == INVALID, (page, pages)
