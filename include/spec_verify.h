@@ -474,7 +474,8 @@ typedef struct sv_rows {
  * new rows, or stays if that is larger and the page holds positions below
  * seq_base; codes of those are rescaled when it grows. Rounding is to nearest
  * even; infinities saturate, NaN stays NaN, neither counts in the maximum.
- * out_len[b] = seq_base[b] + row count. A request with a bad page, position or
+ * out_len[b] = seq_base[b] + row count. out_len is neither seq_base nor
+ * num_accepted (SV_ERR_INVALID_ARG: the call reads them to its end). A request with a bad page, position or
  * node is left untouched (out_len = seq_base). Requests must not share the
  * pages written. */
 sv_status spec_kv_append_q8(const sv_q8_cache* cache, const sv_rows* k_new, const sv_rows* v_new, int32_t dtype,
@@ -521,7 +522,8 @@ sv_status spec_attention_weights_q8(const sv_rows* q, int32_t dtype, const float
  * slots >= keep move, in order, into the slots < keep whose tokens go; a
  * page's scales become the largest of its slots' source pages' scales.
  * out_scores / out_positions [B, Hkv, S] follow the tokens (0 and -1 past
- * out_len[b] = min(seq_len[b], keep)) and may be the inputs; S is at most
+ * out_len[b] = min(seq_len[b], keep)) and may be the inputs; out_len is neither
+ * seq_len nor protect_from (SV_ERR_INVALID_ARG); S is at most
  * 2^30 and num_pages * Hkv * page_size at most 2^32. Requests no longer than keep, or with a bad page, keep their tokens. */
 size_t spec_kv_evict_q8_workspace_size(int32_t B, int32_t Hkv, int32_t keep);
 sv_status spec_kv_evict_q8(const sv_q8_cache* cache, int32_t B, const int32_t* seq_len, const float* scores,

@@ -239,6 +239,7 @@ sv_status spec_kv_append_q8(const sv_q8_cache* cache, const sv_rows* k_new, cons
   a.out_len = out_len;
   a.status = out_status;
   if (2ll * B * cache->Hkv * a.W > INT32_MAX) return SV_ERR_INVALID_ARG;
+  if (out_len == seq_base || out_len == num_accepted) return SV_ERR_INVALID_ARG;   // read by CTAs that start later
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return done(dtype == SV_F32    ? launch_append<TypeF32>(a, passes, D, st)
               : dtype == SV_BF16 ? launch_append<TypeBf16>(a, passes, D, st)
@@ -379,6 +380,7 @@ sv_status spec_kv_evict_q8(const sv_q8_cache* cache, int32_t B, const int32_t* s
       !aligned(out_len, 4) || !aligned(out_status, 4) || !aligned(workspace, 16))
     return SV_ERR_INVALID_ARG;
   if (workspace_bytes < spec_kv_evict_q8_workspace_size(B, cache->Hkv, keep)) return SV_ERR_WORKSPACE_TOO_SMALL;
+  if (out_len == seq_len || out_len == protect_from) return SV_ERR_INVALID_ARG;   // read by CTAs that start later
   const int64_t bh = static_cast<int64_t>(B) * cache->Hkv;
   const int64_t per_cta = static_cast<int64_t>(kMvWarps) * std::max(cache->page_size, 32);
   const int64_t groups = (keep + per_cta - 1) / per_cta;

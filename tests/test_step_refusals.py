@@ -184,3 +184,10 @@ def test_positions_whose_tiles_end_past_32_bits(lib):
         for pages in (most + 1, (1 << 31) // page - 1):
             c = cache(page_size=page, max_pages=pages, Hkv=1)
             assert append(lib, c) == attention(lib, c) == weights(lib, c) == evict(lib, c) == INVALID, (page, pages)
+
+
+def test_lengths_in_place(lib):
+    """out_len is written by a request's first CTA while others may still have to read the length."""
+    other = 2 * FAKE
+    assert append(lib, base=FAKE, out=FAKE) == append(lib, base=other, path=FAKE, cols=3, n=FAKE, out=FAKE) == INVALID
+    assert evict(lib, n=FAKE, out=FAKE) == evict(lib, n=other, pf=FAKE, out=FAKE) == INVALID
