@@ -468,16 +468,20 @@ typedef struct sv_rows {
  * becomes position seq_base[b] + i. With path_nodes [B, path_cols] row i is
  * row path_nodes[b, i] of the new rows, and with num_accepted row count is
  * num_accepted[b] + 1 (else N): a verify pass appends all of its nodes, and
- * afterwards the accepted path again over them, which leaves the cache as if
- * only the accepted tokens had been appended. Per page and head touched, the
- * scale becomes the smallest power of two with max |x| <= 448 scale over the
- * new rows, or stays if that is larger and the page holds positions below
- * seq_base; codes of those are rescaled when it grows. Rounding is to nearest
- * even; infinities saturate, NaN stays NaN, neither counts in the maximum.
- * out_len[b] = seq_base[b] + row count. out_len is neither seq_base nor
- * num_accepted (SV_ERR_INVALID_ARG: the call reads them to its end). A request with a bad page, position or
- * node is left untouched (out_len = seq_base). Requests must not share the
- * pages written. */
+ * afterwards the accepted path again over them. That leaves the positions and
+ * lengths of the accepted tokens alone, and on pages that hold nothing below
+ * seq_base their codes and scales too; the page that does keeps the largest
+ * scale it ever had, so a rejected node of larger magnitude can leave that page
+ * (positions below seq_base and the accepted ones) rounded more coarsely, by at
+ * most half of e4m3's smallest step, scale * 2^-10, beside its relative 2^-4.
+ * Per page and head touched, the scale becomes the smallest power of two with
+ * max |x| <= 448 scale over the new rows, or stays if that is larger and the
+ * page holds positions below seq_base; codes of those are rescaled when it
+ * grows. Rounding is to nearest even; infinities saturate, NaN stays NaN,
+ * neither counts in the maximum. out_len[b] = seq_base[b] + row count; it is
+ * neither seq_base nor num_accepted (SV_ERR_INVALID_ARG: the call reads them to
+ * its end). A request with a bad page, position or node is left untouched
+ * (out_len = seq_base). Requests must not share the pages written. */
 sv_status spec_kv_append_q8(const sv_q8_cache* cache, const sv_rows* k_new, const sv_rows* v_new, int32_t dtype,
                             int32_t B, int32_t N, const int32_t* seq_base, const int32_t* path_nodes,
                             int32_t path_cols, const int32_t* num_accepted, int32_t* out_len, int32_t* out_status,
@@ -524,7 +528,10 @@ sv_status spec_attention_weights_q8(const sv_rows* q, int32_t dtype, const float
  * out_scores / out_positions [B, Hkv, S] follow the tokens (0 and -1 past
  * out_len[b] = min(seq_len[b], keep)) and may be the inputs; out_len is neither
  * seq_len nor protect_from (SV_ERR_INVALID_ARG); S is at most
- * 2^30 and num_pages * Hkv * page_size at most 2^32. Requests no longer than keep, or with a bad page, keep their tokens. */
+ * 2^30 and num_pages * Hkv * page_size at most 2^32. Requests no longer than
+ * keep, or with a bad page, keep their tokens. Pages are rewritten in place:
+ * a request longer than keep must not share any of its pages with another (a
+ * prefix that several requests hold in common is copied first). */
 size_t spec_kv_evict_q8_workspace_size(int32_t B, int32_t Hkv, int32_t keep);
 sv_status spec_kv_evict_q8(const sv_q8_cache* cache, int32_t B, const int32_t* seq_len, const float* scores,
                            const int32_t* positions, int32_t S, int32_t keep, int32_t sinks,

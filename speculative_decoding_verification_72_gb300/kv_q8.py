@@ -100,7 +100,8 @@ def spec_kv_append_q8(cache, k_new, v_new, page_table, seq_base, path_nodes=None
     """Write new key / value rows into the cache (modified in place). k_new, v_new [B, N, kv heads, head dim] (fp32,
     bf16 or fp16; any strides that are multiples of 16 bytes); row i of request b becomes position seq_base[b] + i.
     After a verify pass, path_nodes and num_accepted (spec_verify_tree's nodes and num_accepted) write the accepted
-    rows again over the pass's nodes. Returns dict(out_len [B], status [B]); out["out_len"] is another tensor than
+    rows again over the pass's nodes (the page that also holds earlier positions keeps the largest scale it had, a rejected
+    node's among them). Requests must not share the pages written. Returns dict(out_len [B], status [B]); out["out_len"] is another tensor than
     seq_base and num_accepted."""
     return binding().kv_append(cache, k_new, v_new, page_table, seq_base, path_nodes, num_accepted, out)
 
@@ -126,7 +127,7 @@ def spec_attention_weights_q8(q, lse, cache, page_table, seq_base, scores, path_
 def spec_kv_evict_q8(cache, page_table, seq_len, scores, positions, keep, sinks=0, protect_from=None, workspace=None,
                      out=None):
     """Evict down to `keep` slots (a multiple of the page size) per request and head by score (the cache is modified in
-    place; pages past keep fall free). scores [B, kv heads, S] float32, positions [B, kv heads, S] int32 (the token each
+    place; pages past keep fall free; a request that is evicted from must not share its pages with another). scores [B, kv heads, S] float32, positions [B, kv heads, S] int32 (the token each
     slot holds); tokens at positions below `sinks` or from protect_from[b] on are kept first. Returns dict(scores,
     positions [B, kv heads, S], out_len [B], status [B]); out["scores"] / out["positions"] may be the inputs,
     out["out_len"] not seq_len or protect_from."""

@@ -224,3 +224,37 @@ def test_lengths_past_32_bits_are_out_of_range():
     r = sv.spec_kv_append_q8(cache, k, k, i32(t), torch.tensor([2 ** 32 + 5, -2 ** 32 + 5]))
     assert r["status"].tolist() == [sv.STATUS_BAD_PAGE] * 2
     same_cache(to_host(cache), c)
+
+
+@pytest.mark.parametrize("outlier", [1.0, 300.0, 1e4])
+def test_what_a_rejected_node_leaves_behind(outlier):
+    """All nodes and then the accepted ones, against the accepted ones alone: pages that begin with new rows are the same;
+    the page that also holds earlier positions may have a larger scale, never a smaller one, and its values then differ by
+    the two roundings (2^-4 of the value each, half of the smallest step under each scale)."""
+    rng = np.random.default_rng(15)
+    base, N, P, D = [20, 13], 24, 16, 64
+    lens = [b + N for b in base]
+    c, t = host_cache(rng, 10, 2, P, D), table(rng, lens, P, 10)
+    k, _ = rows(rng, (2, N, 2, D), BF)
+    k[:, 1] *= outlier                                         # node 1 lies in the page of base and is rejected
+    path, n_acc = np.array([[0] + list(range(2, 22))] * 2), [20, 20]
+    acc = torch.stack([k[b, path[b]] for b in range(2)])
+    both, alone = to_gpu(c), to_gpu(c)
+    sv.spec_kv_append_q8(both, k, -k, i32(t), i32(base))
+    r = sv.spec_kv_append_q8(both, k, -k, i32(t), i32(base), path_nodes=i32(path), num_accepted=i32(n_acc))
+    w = sv.spec_kv_append_q8(alone, acc, -acc, i32(t), i32(base))
+    assert r["out_len"].tolist() == w["out_len"].tolist() == [b + 21 for b in base]
+    a, b = to_host(both), to_host(alone)
+    for codes, scales in (("k", "ks"), ("v", "vs")):
+        for req, n in enumerate(b + 21 for b in base):
+            for lp in range(-(-n // P)):
+                page, m, first = t[req, lp], min(P, n - lp * P), lp == base[req] // P
+                s, s0 = a[scales][page], b[scales][page]
+                x = K.decode(a[codes][page, :, :m]) * s[:, None, None]
+                y = K.decode(b[codes][page, :, :m]) * s0[:, None, None]
+                if not first:
+                    assert np.array_equal(s, s0) and np.array_equal(a[codes][page, :, :m], b[codes][page, :, :m])
+                    continue
+                assert (s >= s0).all() and ((s > s0).all() if outlier > 100 else True)
+                big = np.maximum(np.abs(x), np.abs(y))
+                assert (np.abs(x - y) <= 2.0 ** -3 * big + 2.0 ** -10 * (s + s0)[:, None, None]).all()
