@@ -355,10 +355,11 @@ sv_status spec_verify_check_status(const int32_t* status_host, int32_t B);
 
 /* Self-test of the kernels' failure path, for health checks: enqueues one
  * one-thread-block kernel that waits on an mbarrier phase nothing completes,
- * with the same bounded wait the verification kernels use. The wait gives up
- * after its limit (about 20 ms), the kernel writes SV_STATUS_TIMEOUT to
- * out_status[0] (device memory, int32) and returns normally, so the context
- * stays usable. No bulk copy or other asynchronous work is outstanding when
+ * with the bounded wait that the verification kernels use and then with the
+ * 8-bit cache kernels'. Each gives up after its limit (about 20 ms), the kernel
+ * writes SV_STATUS_TIMEOUT to out_status[0] (device memory, int32; 0 if a wait
+ * did not give up as it should) and returns normally, so the context stays
+ * usable. No bulk copy or other asynchronous work is outstanding when
  * the kernel exits. Returns SV_ERR_INVALID_ARG for a NULL or misaligned
  * out_status, SV_ERR_CUDA if the launch fails. */
 sv_status spec_verify_selftest_wait(int32_t* out_status, void* stream);
@@ -497,7 +498,9 @@ sv_status spec_kv_append_q8(const sv_q8_cache* cache, const sv_rows* k_new, cons
  * lse -inf. Scores are sm_scale q.k; out [B, N, Hq, D] in the queries' type,
  * out_lse [B, N, Hq] the natural log of the sum of exponentials (may be
  * NULL). A parent outside [0, n) ends the path there and sets
- * SV_STATUS_BAD_PARENT; positions on a bad page are not seen. */
+ * SV_STATUS_BAD_PARENT; positions on a bad page are not seen. A wait inside
+ * the kernels that gave up sets SV_STATUS_TIMEOUT, and the output and lse of
+ * the rows that it may have touched are NaN. */
 size_t spec_attention_q8_workspace_size(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int32_t D);
 sv_status spec_attention_q8(const sv_rows* q, int32_t dtype, const sv_q8_cache* cache, int32_t B, int32_t N, int32_t Hq,
                             const int32_t* seq_base, const int32_t* parents, const int32_t* n_nodes, float sm_scale,

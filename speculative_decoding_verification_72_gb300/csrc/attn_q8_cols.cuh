@@ -266,7 +266,8 @@ __global__ void __launch_bounds__(ColLayout<D, MT, NT>::kThreads, 2)
     const float* max_g = s_max + grp * 80;
     uint32_t* unseen = reinterpret_cast<uint32_t*>(s_max + grp * 80 + 16);   // whether a row with a node has seen no position yet
     // A wait that gives up ends no loop here: these warps meet at barriers, so all
-    // run on to the end (every later wait then returns at once), without meaning.
+    // run on to the end (every later wait then returns at once), without meaning:
+    // the rows of every piece that ends after it are NaN.
     for (; cur.pos < hi; cur.pos += cur.n) {
       cur.piece<kColTile>(a, hi, ipr);
       const AttnReq rq = cur.rq;
@@ -548,7 +549,9 @@ __global__ void __launch_bounds__(ColLayout<D, MT, NT>::kThreads, 2)
       float* part = a.part + static_cast<int64_t>(2 * cta + (cur.pos == lo ? 0 : 1)) * R * AttnLayout<D>::kPitch;
       if (row < 16) {
         const int r = r00 + row, Rg = row0 + r, node = attn_node(a, Rg);
-        const float sum = s_node[r] < 0 ? 0.f : (max_g[row] + max_g[20 + row]) + (max_g[40 + row] + max_g[60 + row]);
+        const float sum = s_node[r] < 0 ? 0.f
+                          : *fail       ? __int_as_float(0x7fc00000)
+                                        : (max_g[row] + max_g[20 + row]) + (max_g[40 + row] + max_g[60 + row]);
         const int64_t at = (static_cast<int64_t>(cur.b) * a.N + node) * a.Hq + cur.h * a.G + (Rg - node * a.G);
         const float f = sum == 0.f ? 0.f : 0.25f * v0;   // a row that saw nothing is zero
         if (Rg < rows_total) {

@@ -302,7 +302,8 @@ __global__ void __launch_bounds__(kRowThreads, 2)
   } else if (warp < 8) {
     // -------------------------------------------------------------- softmax
     // A wait that gives up ends no loop here: these warps meet at barriers, so all
-    // run on to the end (every later wait then returns at once), without meaning.
+    // run on to the end (every later wait then returns at once), without meaning:
+    // the rows of every piece that ends after it are NaN.
     const int half = warp >> 2, row = tid & 127;   // the thread's 64 tokens of a tile, its row
     const uint32_t t_lane = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t t_s = t_lane + half * 64, t_o = t_lane + 128 + half * (D / 2);
@@ -533,6 +534,7 @@ __global__ void __launch_bounds__(kRowThreads, 2)
       }
       tc_fence_after();
       const bool whole = cur.n == cur.tiles;
+      if (*fail) l = __int_as_float(0x7fc00000);
       if (node < 0) l = 0.f;
       const float f = l == 0.f ? 0.f : whole ? v0 / l : v0;
       const int64_t at = (static_cast<int64_t>(cur.b) * a.N + my_at) * a.Hq + cur.h * a.G + (Rg - my_at * a.G);

@@ -125,3 +125,14 @@ def test_bounded_wait_gives_up_and_the_context_stays_usable():
     got = sv.spec_verify_greedy(ci.target, ci.draft_tokens)
     compare(got, O.verify_greedy(f64(ci.target), host(ci.draft_tokens)))
     assert sv.spec_verify_check_status(got["status"]) == 0
+
+
+def test_both_bounded_waits_give_up():
+    """The self-test runs out the verification kernels' wait and the 8-bit cache kernels', about 20 ms each."""
+    sv.spec_verify_selftest_wait()
+    torch.cuda.synchronize()
+    t0 = time.perf_counter()
+    st = sv.spec_verify_selftest_wait()
+    torch.cuda.synchronize()
+    assert time.perf_counter() - t0 > 0.035
+    assert int(st.item()) == sv.STATUS_TIMEOUT
