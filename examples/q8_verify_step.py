@@ -117,7 +117,8 @@ def decode(model, prompt, n, guesses=None, budget=None, seed=1, report=None):
     """n tokens after prompt [B, L]; guesses [B, >= n] (a drafter's) are offered to the verify passes. Returns tokens
     [B, n], their log-probs and the decoder."""
     B, L = prompt.shape
-    d = Decoder(model, B, L + 2 * n + len(TREE) + 64, budget=budget)
+    # a request may take four tokens a pass while another takes one
+    d = Decoder(model, B, L + 4 * n + len(TREE), budget=budget)
     d.prefill(prompt[:, :-1])
     g = torch.Generator().manual_seed(seed)
     out, lps, last = [[] for _ in range(B)], [[] for _ in range(B)], prompt[:, -1].clone()

@@ -54,3 +54,16 @@ def test_a_budget_bounds_the_cache():
 
     E.decode(model, prompt, 20, budget=96, report=report)
     assert max(longest) <= 96
+
+
+def test_requests_that_accept_unequally():
+    """One request's drafts are all right, the other's none: the first runs far ahead and stays within its pages."""
+    import q8_verify_step as E
+    model = E.Model()
+    prompt = torch.randint(0, model.vocab, (2, 30), generator=torch.Generator().manual_seed(7), dtype=torch.int32).cuda()
+    plain, _, _ = E.decode(model, prompt, 280)
+    guesses = plain.int()
+    guesses[1] = -1
+    tokens, _, d = E.decode(model, prompt, 70, guesses=guesses)
+    assert int(d.seen[0]) > 30 + 2 * 70 + 72
+    assert d.seen.tolist() == d.length.tolist() and tokens.shape == (2, 70)
