@@ -71,4 +71,4 @@ class _TokenLogprobsGrad(torch.autograd.Function):
 def token_logprobs(logits, tokens, temperature=1.0):
     """(logprob, entropy), each [B, R] float32, of spec_token_logprobs; differentiable with respect to logits, once (a
     second derivative raises SpecVerifyError)."""
-    return _TokenLogprobs.apply(logits, tokens, temperature)
+    return _TokenLogprobs.apply(logits, torch.as_tensor(tokens), temperature)

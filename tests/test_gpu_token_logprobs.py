@@ -224,3 +224,12 @@ def test_tokens_past_32_bits_are_out_of_range():
     r = sv.spec_token_logprobs(x, torch.tensor([[2 ** 32 + 3, 3, -2 ** 32 + 3]], device=DEV))
     bad = sv.STATUS_BAD_TOKEN
     assert r["status"].tolist() == [[bad, 0, bad]] and r["logprob"][0, 0] == 0 and r["logprob"][0, 2] == 0
+
+
+def test_tokens_of_the_differentiable_call_may_be_a_list():
+    x = torch.randn((1, 2, 40), generator=torch.Generator().manual_seed(13)).to(DEV).requires_grad_()
+    grads = []
+    for tok in ([[3, -1]], torch.tensor([[3, -1]]), torch.tensor([[3, -1]], dtype=torch.int32, device=DEV)):
+        lp, ent = sv.token_logprobs(x, tok)
+        grads.append(torch.autograd.grad((lp + ent).sum(), x)[0])
+    assert torch.equal(grads[0], grads[1]) and torch.equal(grads[0], grads[2])
