@@ -190,6 +190,19 @@ __device__ __forceinline__ uint32_t unit_off(int row, int ch) {
   return row * 64 + ((ch ^ ((row >> 1) & 3)) << 4);
 }
 
+// A partial's (max, sum) for the join, its sum brought into [1, 2): the exponent
+// goes into the maximum and out of `f`, the factor of o. A piece's own maximum
+// counts V's scales relative to its first page, so the maxima of two pieces may
+// lie further apart than fp32's exponents reach where their weights do not (a
+// page of zeros has scale 2^-100).
+__device__ __forceinline__ float2 attn_partial(float m, float l, float& f) {
+  if (l == 0.f) return make_float2(-INFINITY, 0.f);
+  const int e = min(max(static_cast<int>(__float_as_uint(l) >> 23) - 127, -126), 126);
+  const float down = exp2_int(-e);
+  f *= down;
+  return make_float2(m + static_cast<float>(e), l * down);
+}
+
 // Joins the pieces of items that several CTAs shared, one warp a row; B more
 // CTAs check the requests' pages, lengths and trees. All loads of a row's first
 // eight pieces go out together, after one for the plan.

@@ -553,12 +553,12 @@ __global__ void __launch_bounds__(ColLayout<D, MT, NT>::kThreads, 2)
                           : *fail       ? __int_as_float(0x7fc00000)
                                         : (max_g[row] + max_g[20 + row]) + (max_g[40 + row] + max_g[60 + row]);
         const int64_t at = (static_cast<int64_t>(cur.b) * a.N + node) * a.Hq + cur.h * a.G + (Rg - node * a.G);
-        const float f = sum == 0.f ? 0.f : 0.25f * v0;   // a row that saw nothing is zero
+        float f = sum == 0.f ? 0.f : 0.25f * v0;   // a row that saw nothing is zero
         if (Rg < rows_total) {
           if (whole) {
             if (a.lse) a.lse[at] = sum == 0.f ? -INFINITY : (s_m0[r] + log2f(sum)) * kLn2;
           } else {
-            *reinterpret_cast<float2*>(part + r * AttnLayout<D>::kPitch + D) = make_float2(sum == 0.f ? -INFINITY : s_m0[r], sum);
+            *reinterpret_cast<float2*>(part + r * AttnLayout<D>::kPitch + D) = attn_partial(s_m0[r], sum, f);
           }
         }
         s_out[r] = make_int4(static_cast<int>(at & 0xffffffff), static_cast<int>(at >> 32),

@@ -536,7 +536,9 @@ __global__ void __launch_bounds__(kRowThreads, 2)
       const bool whole = cur.n == cur.tiles;
       if (*fail) l = __int_as_float(0x7fc00000);
       if (node < 0) l = 0.f;
-      const float f = l == 0.f ? 0.f : whole ? v0 / l : v0;
+      float f = l == 0.f ? 0.f : whole ? v0 / l : v0;
+      float2 ml = make_float2(m_run, l);
+      if (!whole) ml = attn_partial(m_run, l, f);
       const int64_t at = (static_cast<int64_t>(cur.b) * a.N + my_at) * a.Hq + cur.h * a.G + (Rg - my_at * a.G);
       float* part = a.part + (static_cast<int64_t>(2 * cta + (cur.pos == lo ? 0 : 1)) * 128 + row) * kPitch;
       const bool mine = Rg < rows_total;
@@ -571,7 +573,7 @@ __global__ void __launch_bounds__(kRowThreads, 2)
         if (whole) {
           if (a.lse) a.lse[at] = l == 0.f ? -INFINITY : (m_run + log2f(l)) * kLn2;
         } else {
-          *reinterpret_cast<float2*>(part + D) = make_float2(l == 0.f ? -INFINITY : m_run, l);
+          *reinterpret_cast<float2*>(part + D) = ml;
         }
       }
       tc_fence_before();

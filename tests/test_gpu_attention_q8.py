@@ -317,3 +317,24 @@ def test_weights_of_rows_that_saw_nothing(N, G, D):
     assert torch.isfinite(got["scores"]).all() and torch.equal(got["scores"], want["scores"])
     assert torch.equal(got["scores"][3, :, :3], s[3, :, :3])
     assert got["status"].tolist() == want["status"].tolist() == [0] * 4
+
+
+def scale_problem(seed, B, N, H, G, D, P, dtype, tree=False):
+    rng, c, t, q, q64 = problem(seed, [300 + 37 * b for b in range(B)], N, H, G, D, P, dtype)
+    par = trees(rng, B, N) if tree else None
+    return rng, c, t, q, q64, [300 + 37 * b for b in range(B)], par
+
+
+@pytest.mark.parametrize("N,G,D,dtype", [(5, 3, 128, HF), (1, 2, 64, BF), (6, 4, 64, BF), (40, 2, 128, BF)])
+def test_pages_of_zeros_and_pages_that_are_not_there(N, G, D, dtype):
+    """A page of zeros has scale 2^-100. Pieces of a request that begin on a missing page, on such a page and on others
+    count scales from different references, and weigh the same together all the same."""
+    P, B = 16, 7
+    rng, c, t, q, q64, base, _ = scale_problem(60, B, N, 3, G, D, P, dtype)
+    q *= 0.05
+    q64 = q.double().cpu().numpy()
+    zero = rng.random(c["vs"].shape) < 0.3
+    c["vs"][zero], c["v"][zero] = 2.0 ** -100, 0
+    t[rng.random(t.shape) < 0.5] = -1
+    r = sv.spec_attention_q8(q, to_gpu(c), i32(t), i32(base))
+    check_attention(r, K.attention(q64, c, t, base, sm=D ** -0.5), dtype)
