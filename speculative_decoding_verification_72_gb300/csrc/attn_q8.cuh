@@ -190,6 +190,11 @@ __device__ __forceinline__ uint32_t unit_off(int row, int ch) {
   return row * 64 + ((ch ^ ((row >> 1) & 3)) << 4);
 }
 
+// V's scale as an exponent counts it: no less than the smallest that is written.
+// Zero would be infinitely far below the others, and the weights that it shares
+// an exponent with would be lost; what its codes add is below 2^-91.
+__device__ __forceinline__ float attn_v_scale(float vs) { return vs >= 0.f && vs < 0x1p-100f ? 0x1p-100f : vs; }
+
 // A partial's (max, sum) for the join, its sum brought into [1, 2): the exponent
 // goes into the maximum and out of `f`, the factor of o. A piece's own maximum
 // counts V's scales relative to its first page, so the maxima of two pieces may

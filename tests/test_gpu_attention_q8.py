@@ -338,3 +338,19 @@ def test_pages_of_zeros_and_pages_that_are_not_there(N, G, D, dtype):
     t[rng.random(t.shape) < 0.5] = -1
     r = sv.spec_attention_q8(q, to_gpu(c), i32(t), i32(base))
     check_attention(r, K.attention(q64, c, t, base, sm=D ** -0.5), dtype)
+
+
+@pytest.mark.parametrize("missing", [0.0, 0.4])
+@pytest.mark.parametrize("N,G,D,dtype", [(5, 3, 128, HF), (1, 2, 64, BF), (6, 4, 64, BF), (40, 2, 128, BF), (33, 3, 64, HF)])
+def test_pages_of_scale_zero(N, G, D, dtype, missing):
+    """Scales of zero beside pages of zeros as append writes them: their values are nothing, their weights count."""
+    P, B = 16, 7
+    rng, c, t, q, q64, base, par = scale_problem(61, B, N, 3, G, D, P, dtype, tree=N == 40)
+    kind = rng.random(c["vs"].shape)
+    c["vs"][kind < 0.6] = 2.0 ** -100
+    c["v"][kind < 0.6] = 0
+    c["vs"][kind < 0.3] = 0.0
+    c["v"][kind < 0.15] = K.encode(100.0)
+    t[rng.random(t.shape) < missing] = -1
+    r = sv.spec_attention_q8(q, to_gpu(c), i32(t), i32(base), parents=None if par is None else i32(par))
+    check_attention(r, K.attention(q64, c, t, base, par, sm=D ** -0.5), dtype)
