@@ -438,8 +438,9 @@ sv_status spec_verify_greedy_host(const void* target_logits, int32_t dtype, int6
  * accumulated attention weight, and eviction by it.
  *
  * K and V are e4m3 codes [num_pages, Hkv, page_size, D], contiguous, with fp32
- * scales [num_pages, Hkv], not negative; a code stands for code * scale (to
- * attention a scale of V below 2^-100, the smallest that append writes, is 2^-100).
+ * scales [num_pages, Hkv], not negative; a code stands for code * scale.
+ * Attention takes a V scale of at most 2^-100 for a page of zeros (append gives
+ * those 2^-100), and what codes it has for less than 2^-51 of the largest scale.
  * Position p of request b is slot p % page_size of page page_table[b, p / page_size].
  * page_size is 16, 32, 64 or 128; D is 64 or 128; codes are 16-byte aligned.
  * Offsets into a cache are 64-bit; max_pages * page_size, the positions of a

@@ -190,10 +190,21 @@ __device__ __forceinline__ uint32_t unit_off(int row, int ch) {
   return row * 64 + ((ch ^ ((row >> 1) & 3)) << 4);
 }
 
-// V's scale as an exponent counts it: no less than the smallest that is written.
-// Zero would be infinitely far below the others, and the weights that it shares
-// an exponent with would be lost; what its codes add is below 2^-91.
-__device__ __forceinline__ float attn_v_scale(float vs) { return vs >= 0.f && vs < 0x1p-100f ? 0x1p-100f : vs; }
+// V's scale as an exponent counts it, for a warp whose lanes hold pages' scales
+// (there: whether the lane has a page). A page of zeros has scale 2^-100, or 0 if
+// it was never written: as an exponent that far below the others the weights of
+// its positions would fall out of fp32's range. It counts as 2^60 below the
+// largest scale so far (`most`, a lane's own, kept by the caller), or as 2^-100;
+// codes that are not zero under such a scale add less than 2^-51 of that scale.
+__device__ __forceinline__ float attn_v_scale(float vs, bool there, float& most) {
+  most = fmaxf(most, vs);
+  const bool zeros = there && vs >= 0.f && vs <= 0x1p-100f;
+  if (__any_sync(0xffffffffu, zeros)) {
+    const float m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
+    if (zeros) vs = fmaxf(0x1p-100f, fminf(m, 0x1p126f) * 0x1p-60f);
+  }
+  return vs;
+}
 
 // A partial's (max, sum) for the join, its sum brought into [1, 2): the exponent
 // goes into the maximum and out of `f`, the factor of o. A piece's own maximum

@@ -182,10 +182,11 @@ __global__ void __launch_bounds__(ColLayout<D, MT, NT>::kThreads, 2)
       };
       auto scales_of = [&](int p) {
         const int64_t o = static_cast<int64_t>(max(p, 0)) * a.c.Hkv + cur.h;
-        return p >= 0 ? make_float4(a.c.ks[o], attn_v_scale(a.c.vs[o]), 1.f, 0.f) : make_float4(0.f, 0.f, 0.f, 0.f);
+        return p >= 0 ? make_float4(a.c.ks[o], a.c.vs[o], 1.f, 0.f) : make_float4(0.f, 0.f, 0.f, 0.f);
       };
       int page = page_of(0), page1 = page_of(1);
       float4 sc = scales_of(page);
+      float most = 0.f;
       for (int i = 0; i < cur.n; ++i, ++n) {
         const int page2 = page_of(i + 2);
         const float4 sc1 = scales_of(page1);
@@ -199,6 +200,7 @@ __global__ void __launch_bounds__(ColLayout<D, MT, NT>::kThreads, 2)
           ok = __shfl_sync(0xffffffffu, ok, 0);
           if (!ok) break;
           if (kv == 0) {
+            sc.y = attn_v_scale(sc.y, page >= 0, most);
             if (lane < 8) s_sc[(n & 7) * 8 + lane] = sc;
             __syncwarp();
           }

@@ -153,12 +153,11 @@ __global__ void __launch_bounds__(kRowThreads, 2)
       };
       auto scales_of = [&](int p) {
         const int64_t o = static_cast<int64_t>(max(p, 0)) * a.c.Hkv + cur.h;
-        return p >= 0 ? make_float2(a.c.ks[o], attn_v_scale(a.c.vs[o])) : make_float2(0.f, 0.f);
+        return p >= 0 ? make_float2(a.c.ks[o], a.c.vs[o]) : make_float2(0.f, 0.f);
       };
       int page = page_of(0), page1 = page_of(1);
       float2 sc = scales_of(page);
-      float v0 = __shfl_sync(0xffffffffu, sc.y, 0);
-      v0 = v0 > 0.f && v0 < INFINITY ? v0 : 1.f;
+      float v0 = 1.f, most = 0.f;
       for (int i = 0; i < cur.n; ++i, ++n) {
         const int page2 = page_of(i + 2);
         const float2 sc1 = scales_of(page1);
@@ -168,6 +167,11 @@ __global__ void __launch_bounds__(kRowThreads, 2)
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
         const bool whole = __popc(__ballot_sync(0xffffffffu, page >= 0)) == boxes;
+        sc.y = attn_v_scale(sc.y, page >= 0, most);
+        if (i == 0) {
+          v0 = __shfl_sync(0xffffffffu, sc.y, 0);
+          v0 = v0 > 0.f && v0 < INFINITY ? v0 : 1.f;
+        }
         if (lane == 0) s_whole[n & 7] = whole;
         if (lane < 8) {
           const float rel = sc.y / v0;

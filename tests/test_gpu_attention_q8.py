@@ -354,3 +354,24 @@ def test_pages_of_scale_zero(N, G, D, dtype, missing):
     t[rng.random(t.shape) < missing] = -1
     r = sv.spec_attention_q8(q, to_gpu(c), i32(t), i32(base), parents=None if par is None else i32(par))
     check_attention(r, K.attention(q64, c, t, base, par, sm=D ** -0.5), dtype)
+
+
+@pytest.mark.parametrize("first", [True, False])
+@pytest.mark.parametrize("N,G,D,dtype", [(5, 3, 128, BF), (1, 2, 64, BF), (40, 2, 128, BF), (33, 4, 64, BF)])
+def test_pages_of_zeros_beside_large_values(N, G, D, dtype, first):
+    """Values of 10^7 beside pages of zeros whose positions have scores some bits lower but are many."""
+    P, B = 16, 5
+    rng, c, t, q, q64, _, par = scale_problem(62, B, N, 2, G, D, P, dtype, tree=N == 40)
+    base = [300 + 37 * b for b in range(B)]
+    c["ks"][:], c["k"][..., :32] = 2.0 ** -7, K.encode(128.0)
+    c["vs"][:] *= 2.0 ** 22
+    q *= 0.05
+    q[..., :32] = 9.0 / 32 * D ** 0.5              # a score of 9 where a key begins with ones, 0 where with zeros
+    q64 = q.double().cpu().numpy()
+    for b in range(B):                              # most pages hold zeros and score 13 bits lower
+        for lp in range(base[b] // P):
+            if (lp % 6 != 0) == first and lp > 0 or (lp == 0 and first):
+                p = t[b, lp]
+                c["v"][p], c["vs"][p], c["k"][p, :, :, :32] = 0, 2.0 ** -100, 0
+    r = sv.spec_attention_q8(q, to_gpu(c), i32(t), i32(base), parents=None if par is None else i32(par))
+    check_attention(r, K.attention(q64, c, t, base, par, sm=D ** -0.5), dtype)
