@@ -500,7 +500,10 @@ sv_status spec_kv_append_q8(const sv_q8_cache* cache, const sv_rows* k_new, cons
  * lse -inf. Scores are sm_scale q.k; out [B, N, Hq, D] in the queries' type,
  * out_lse [B, N, Hq] the natural log of the sum of exponentials (may be
  * NULL). A parent outside [0, n) ends the path there and sets
- * SV_STATUS_BAD_PARENT; positions on a bad page are not seen. A wait inside
+ * SV_STATUS_BAD_PARENT; positions on a bad page are not seen. Scores, maxima
+ * and sums are fp32; q is taken to 2^-17 of each row's largest element (2^-22
+ * where Hq / Hkv * N is at most 32), and the softmax's terms are rounded to f16
+ * where they multiply V (2^-11 of a term), not in their sum. A wait inside
  * the kernels that gave up sets SV_STATUS_TIMEOUT, and the output and lse of
  * the rows that it may have touched are NaN. */
 size_t spec_attention_q8_workspace_size(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int32_t D);

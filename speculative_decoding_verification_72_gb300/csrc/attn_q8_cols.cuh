@@ -5,9 +5,11 @@
 // not, are few here: they are split into sums of e4m3 terms instead,
 //   q = qs (q1 + q2 / 32 [+ q3 / 1024]),  P = (p1 + p2 / 32 + p3 / 1024) / 4,
 // each term the rounding of 32 times what the one before left. Two terms hold a
-// bf16 q and three an f16 q exactly (down to 2^-14 of the row's maximum); three
-// terms of P leave 2^-13 of its value or 2^-22 of the row's maximum, finer than
-// an f16 P. The terms are columns of one product, with tokens as its 128 rows:
+// bf16 q and three an f16 q exactly (down to 2^-14 of the row's maximum). P is
+// rounded to f16 first, 2^-11 of its value at most, since packed f16 halves the
+// instructions of the split; its three terms hold that exactly, or leave 2^-22 of
+// the row's largest P. Sums of P (the softmax's) take it before it is rounded.
+// The terms are columns of one product, with tokens as its 128 rows:
 //   S^T [128 tokens, terms x rows] = K [tokens, D] q^T,
 //   O^T [D, 3 x rows] += V^T [D, tokens] P.
 // A tile of 128 tokens is the A operand of both, K as it lies (K-major), V
@@ -39,9 +41,12 @@
 // Work split, partials and their join are attn_q8.cuh's.
 //
 // Measured: 32 requests of 6 rows over up to 8192 tokens, 32 heads on 8 of 128,
-// bf16: 95 us, 339 MB, 3.6 TB/s (without any softmax 89); one request of 1000
-// tokens, one row: 11 us. A tile costs its bytes; about 35 us a call are fixed:
-// first and edge tiles, query terms, the join.
+// 339 MB: bf16 92 us, 3.7 TB/s, f16 89; one request of 1000 tokens, one row: 11
+// us. The softmax is not the bound (without any, 89 us of what then were 95), nor
+// are the pipes (tensor 15 %, exponentials 7 %, an instruction issued in half of
+// the clocks): most warps wait for memory. A CTA has two stages each of K and V,
+// which one warp fills in order, so that a V still in use holds back the next K,
+// and it looks up pages and scales a tile at a time.
 #pragma once
 
 #include <cuda.h>

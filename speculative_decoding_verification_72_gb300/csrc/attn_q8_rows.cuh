@@ -8,9 +8,11 @@
 // q's terms (two for bf16, three for f16) add up in one accumulator; they leave
 // 2^-17 of the row's largest element. P in e4m3 terms would need its columns
 // per term twice over in TMEM, and there are 128 x 128 of them a tile, so P is
-// f16 and V, of which there are 128 x D, is converted (exactly) by four warps
-// on its way from global to shared memory. MMA time per tile: 512 clocks for
-// S (two terms at twice f16's rate) and 512 for P V.
+// f16 (rounded by 2^-11 of its value at most, or by 2^-25 below f16's normal
+// numbers, where the row's largest is 1 to 2^8) and V, of which there are 128 x
+// D, is converted (exactly) by four warps on its way from global to shared
+// memory. Sums of P take it before it is rounded. MMA time per tile: 512 clocks
+// for S (two terms at twice f16's rate) and 512 for P V.
 //
 // Lane = row keeps the softmax within a thread, or two: two groups of four
 // warps take 64 tokens of a tile each, so that a row's exponentials are shared
@@ -26,7 +28,8 @@
 // follow each other; two CTAs an SM fill each other's gaps.
 //
 // Measured: 16 requests of 64-node trees over about 5100 tokens, 32 heads on 8
-// of 128, bf16: 158 us, 0.54 PFLOP/s of the products that the mask leaves. What
+// of 128: bf16 158 us, 0.54 PFLOP/s of the products that the mask leaves; f16 229
+// (its third term of q leaves room for one CTA an SM with heads of 128). What
 // bounds it is the softmax warps' own pace, about 5.6 clocks an instruction at
 // seven warps a scheduler; the tensor pipe is a third busy. Halves of a tile
 // with barriers of their own, one's products under the other's softmax, took

@@ -16,11 +16,14 @@
 // q as e4m3 terms in columns. Lane = token makes a weight one thread's sum over
 // its rows of S^T: no thread talks to another. q's first term and the rest
 // (scaled by 32; for f16 in two terms of that one scale) take two columns a
-// row, exact down to 2^-22 of the row's largest element; weights are formed and
+// row, which leave 2^-22 of the row's largest element; weights are formed and
 // summed in fp32. 64 rows a pass over the keys; more take more passes.
 //
-// Measured (the longest case of the operators' table, heads of 64, f16): 64 us,
-// bound by exponentials and TMEM reads; the bytes alone would take 28.
+// Measured: 8 requests of up to 65536 tokens, 64 query heads on 8 of 64: f16 48
+// rows 64 us, 32 rows 53, 16 rows 47, bf16 48 rows 63; the bytes alone would take
+// 28. Exponentials are not the bound (their pipe is at 16 %, an instruction
+// issues in half of the clocks): the warps, two CTAs of eight an SM, wait for
+// TMEM reads, which they await a group of 16 rows at a time, and for scales.
 //
 // Warps 0-3 take even tiles, 4-7 odd ones; 8: TMA; 9: MMA. Two CTAs an SM.
 #pragma once

@@ -15,9 +15,10 @@
 // several small pages, each with a maximum of its own. All loads that need only
 // base go out before the barrier that carries the maxima; what few rows need
 // (rescaling, a scale that is no power of two, infinities) is out of line.
-// Sixteen elements a thread: the instructions around them are what bounds the
-// kernel next (3 prompts of 4099 bf16 tokens, 8 heads of 128: 16.9 us, 4.5 TB/s;
-// eight elements a thread 19.9).
+// Sixteen elements a thread, for fewer instructions around them (3 prompts of 4099
+// bf16 tokens, 8 heads of 128: 16.9 us, 4.5 TB/s; eight elements a thread 19.9).
+// What is left is mostly waiting for the rows (an instruction issues in 0.64 of
+// the clocks): a CTA has one tile, and no loads under way behind it.
 #pragma once
 
 #include "q8_common.cuh"

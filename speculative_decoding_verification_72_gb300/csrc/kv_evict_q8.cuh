@@ -26,9 +26,15 @@
 // kv_evict_move_kernel, one warp per destination page (two pages of 16), moves
 // the rows.
 //
-// Measured: 24 prompts of up to 8192 tokens down to 4096, 8 heads of 128: 35 us
-// (17 select, 16 move), bound by latencies in a row (the bytes would take 14);
-// 2 requests of 1090 down to 1024: 11.8 us.
+// Measured: 24 prompts of up to 8192 tokens down to 4096, 8 heads of 128, pages
+// whose scales differ by up to 4: 36 us where an earlier call has already raised
+// the scales of the pages that stay (17 select, 16 move; the bytes would take
+// 14), and 23 us more, all in the move, on a cache as appends leave it: there
+// the rows that stay on a page whose scale rises are rounded again, 139 MB of
+// codes read and written instead of 80 (with those the bytes would take 23). 2
+// requests of 1090 down to 1024: 12 us and 16. Bound by latencies in a row: the
+// selection is one CTA a (request, head), phases with a barrier between; the
+// move waits for source, scale and codes (11 of its warps wait an issue).
 #pragma once
 
 #include "q8_common.cuh"
@@ -308,8 +314,8 @@ __global__ void __launch_bounds__(kEvThreads, 2) kv_evict_select_kernel(const Ev
 // One warp per destination page of a (request, head), or per two pages of 16
 // slots: lane l looks after slot l of each 32. The rows that change are listed
 // in shared memory, and two instructions' worth of them are under way at once
-// (24 prompts of 8192 tokens down to 4096: 34.8 us the call; with four 37.6,
-// with one 37.2, at 8, 12 and 16 CTAs an SM).
+// (24 prompts of 8192 tokens down to 4096, scales settled: 34.8 us the call; with
+// four 37.6, with one 37.2, at 8, 12 and 16 CTAs an SM).
 template <int D>
 __global__ void __launch_bounds__(kMvWarps * 32, 12) kv_evict_move_kernel(const EvictArgs a) {
   constexpr int kLpr = D / 16;          // lanes per row

@@ -91,8 +91,9 @@ bool valid_row_count(int64_t rows, int64_t G, uint64_t inv_g) {
 
 // Rows of a block: all of a kv head's as columns where they are at most 32 (in
 // one or two groups of 16), else blocks of 128 lanes. 32 requests of up to 8192
-// tokens, 8 heads of 128: 16 rows take 82 us in one group, 93 in two, 136 as
-// lanes; 24 rows 96 and 138 us, 32 rows 98 and 140; 64 rows 145 as lanes.
+// tokens, 8 heads of 128, when the rule was set: 16 rows took 82 us in one group,
+// 93 in two, 136 as lanes; 24 rows 96 and 138 us, 32 rows 98 and 140; 64 rows 145
+// as lanes. (Now 16 rows 78, 24 rows 92.)
 int attn_block(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 128; }
 
 constexpr int kAttnGridMost = 320;   // CTAs a workspace is sized for: two an SM of 152, whatever the device
