@@ -547,6 +547,78 @@ sv_status spec_kv_evict_q8(const sv_q8_cache* cache, int32_t B, const int32_t* s
                            int32_t* out_status, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
+ * The 16-bit paged cache: writing it with the position rotation applied on the
+ * way, and the attention of a verify pass or a prompt over it.
+ *
+ * K and V are bf16 or fp16 [num_pages, page_size, Hkv, D] with any element
+ * strides of page, token and head that are multiples of 16 bytes and at least
+ * D (elements of a head are contiguous; heads may come before tokens, K and V
+ * may lie in one tensor; the stride of a dimension of one is not used). Slot p
+ * of request b is row p % page_size of page page_table[b, p / page_size].
+ * page_size is 16, 32, 64 or 128; D is 64 or 128; k and v are 16-byte aligned.
+ * max_pages * page_size is at most 2^31 - 256. In the order [pages, tokens, heads,
+ * elements] and contiguous, spec_kv_compact moves the accepted path's rows.
+ *
+ * New row n of request b has slot seq_base[b] + n and position seq_base[b] +
+ * its depth: its number of ancestors by parents [B, N] (parents[0] = -1,
+ * parents[n] in [0, n), at most SV_MAX_TREE_NODES rows), or n with parents NULL
+ * (a chain or a prompt of any length). A parent outside [0, n) ends the path
+ * there and sets SV_STATUS_BAD_PARENT. Rows from n_nodes[b] (NULL: N)
+ * on are no rows of the request. A page id outside [0, num_pages), a slot
+ * outside the page table, or a row count outside [0, N] sets
+ * SV_STATUS_BAD_PAGE. status pointers may be NULL. */
+typedef struct sv_paged_cache {
+  void* k;
+  void* v;
+  int64_t k_strides[3], v_strides[3];   /* elements: page, token, head */
+  const int32_t* page_table;            /* [B, max_pages] */
+  int32_t num_pages, Hkv, page_size, D, max_pages;
+} sv_paged_cache;
+
+/* Write new keys and values, of the cache's type, rotating keys, and queries
+ * if given: with p the row's position and i < rotary_dims / 2, the pair of
+ * dims (i, i + rotary_dims / 2), or (2 i, 2 i + 1) if interleaved, is turned by
+ * the angle p * inv_freq[i] (inv_freq fp32, on the device); other dims, and
+ * values, are moved as they are. rotary_dims is a multiple of 16, at most D.
+ * q [B, N, Hq, D] goes to out_q (contiguous; q itself if that is); q NULL
+ * takes Hq = 0. Angles are right to 2^-24 of a turn for positions below 2^24
+ * (2^-17 up to 2^31), rotations are fp32 and rounded once. out_len[b] = seq_base[b] +
+ * row count; it is neither seq_base nor n_nodes (SV_ERR_INVALID_ARG: the call
+ * reads them to its end). A request with a bad page, slot or row count has
+ * nothing written (out_len = seq_base), its queries are rotated all the same.
+ * Rows of out_q past the row count, or of a negative seq_base, are 0. Requests
+ * must not share the pages written. 2 Hkv + Hq is at most 16384. */
+sv_status spec_kv_append_rope(const sv_paged_cache* cache, int32_t dtype, const sv_rows* k_new, const sv_rows* v_new,
+                              const sv_rows* q, int32_t B, int32_t N, int32_t Hq, const int32_t* seq_base,
+                              const int32_t* parents, const int32_t* n_nodes, const float* inv_freq, int32_t rotary_dims,
+                              int32_t interleaved, void* out_q, int32_t* out_len, int32_t* out_status, void* stream);
+
+/* Attention of N new rows (queries of the cache's type [B, N, Hq, D], Hq a
+ * multiple of Hkv; head h reads kv head h / (Hq / Hkv)) whose keys and values
+ * are in the cache. Row n sees every slot below seq_base[b], itself, and its
+ * ancestors or, with parents NULL, every earlier row; with window > 0, those
+ * of them whose position is less than `window` below its own (pages that no
+ * row's window reaches are not read). Scores z = sm_scale q.k; with softcap >
+ * 0 they are softcap tanh(z / softcap); with slopes [Hq] fp32 they become z -
+ * slopes[h] * (distance of positions). out [B, N, Hq, D] in the queries' type,
+ * out_lse [B, N, Hq] the natural log of the sum of exponentials (may be NULL).
+ * Rows past n_nodes[b], and rows that see nothing, get output 0 and lse -inf;
+ * slots on a bad page are not seen. Values in slots that a row does not see
+ * never reach it, NaN and infinities among them; values that are not finite
+ * make the outputs of the rows that see them infinite or NaN. Scores, maxima and sums are
+ * fp32; the softmax's terms are rounded to the cache's type where they
+ * multiply V, not in their sum (with Hq / Hkv * N up to 32 that is done in two
+ * terms, to 2^-16 of a bf16 weight and 2^-21 of an f16 one). N * Hq / Hkv is at most 2^26, and B * Hkv *
+ * blocks of 256 rows * max_pages * page_size / 128 below 2^31. A wait inside the
+ * kernels that gave up sets SV_STATUS_TIMEOUT, and the output and lse of the
+ * rows that it may have touched are NaN. */
+size_t spec_attention_workspace_size(int32_t B, int32_t N, int32_t Hq, int32_t Hkv, int32_t D);
+sv_status spec_attention(const sv_rows* q, int32_t dtype, const sv_paged_cache* cache, int32_t B, int32_t N, int32_t Hq,
+                         const int32_t* seq_base, const int32_t* parents, const int32_t* n_nodes, float sm_scale, float softcap,
+                         int32_t window, const float* slopes, void* out, float* out_lse, int32_t* out_status, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
  * Log-probabilities of given tokens, with entropy and top alternatives, for
  * rows of logits (fp32 or bf16): per row, p = softmax(x / T);
  *   out_logprob = ln p(token), 0 where token is -1 (no token);

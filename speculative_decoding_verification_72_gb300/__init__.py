@@ -18,4 +18,5 @@ from .verify import (  # noqa: F401
 from .kv_q8 import (  # noqa: F401
     Q8Cache, q8_cache, spec_attention_q8, spec_attention_weights_q8, spec_kv_append_q8, spec_kv_evict_q8,
 )
+from .paged import PagedCache, paged_cache, spec_attention, spec_kv_append_rope  # noqa: F401
 from .logprobs import spec_token_logprobs, spec_token_logprobs_backward, token_logprobs  # noqa: F401

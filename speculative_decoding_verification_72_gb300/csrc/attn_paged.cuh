@@ -1,0 +1,350 @@
+// Attention of new rows over the 16-bit paged cache: what its kernels share.
+//
+// For row n of request b (slot base_b + n, position pos_n) and head h of group h / G:
+//   z_j = sm q.k_j, under a cap z_j = cap tanh(z_j / cap), with a bias z_j - slope_h (pos_n - pos_j),
+//   o = sum_j softmax(z)_j v_j, lse = ln sum_j exp z_j
+// over the visible slots: every j < base, and j = base + m where m is n itself
+// or an ancestor of n (parents given) or m <= n (a chain or a prompt); with a
+// window, those of them with pos_n - pos_j < window. A row that sees nothing
+// gets o = 0 and lse = -inf.
+//
+// The N G rows of one kv head share its keys and are packed as r = n G + g.
+// Up to 32 are columns of a product with the tokens as its rows
+// (attn_paged_cols.cuh, bound by memory); more are lanes, in blocks of 256
+// (attn_paged_rows.cuh, bound by the tensor cores and the exponentials).
+//
+// Split. A block of rows has the 128-slot tiles from its window's start to its
+// last visible slot. The tiles of all (request, block, kv head) items are one
+// line, cut into equal ranges, one per CTA, so mixed lengths load every CTA
+// alike. A range that holds only part of an item writes a partial (max, sum,
+// unnormalised o) that attn_paged_join_kernel joins, in a fixed order.
+//
+// Non-finite values. A slot's values multiply weights of 0 in rows that do not
+// see it, so a tile that not every row sees whole has infinities and NaN taken
+// out of its V, noted, and put into the output of the rows that do see them.
+#pragma once
+
+#include <cuda.h>
+
+#include "attn_q8.cuh"
+#include "paged_common.cuh"
+#include "tc_common.cuh"
+
+namespace sv {
+
+constexpr int kPgTile = 128;
+
+struct PagedAttnArgs {
+  const uint8_t* q;
+  int64_t sqb, sqn, sqh;       // bytes: request, row, head
+  PagedView c;
+  const int32_t* base;         // [B]
+  const int32_t* n_nodes;      // [B] or nullptr
+  const int32_t* parents;      // [B, N] or nullptr (chain)
+  const float* slopes;         // [Hq] or nullptr
+  void* out;                   // [B, N, Hq, D]
+  float* lse;                  // [B, N, Hq] or nullptr
+  int32_t* status;             // [B] or nullptr
+  int32_t B, N, G, Hq, R, RB;  // R: rows of a block, RB: blocks per kv head
+  uint64_t inv_g;              // ceil(2^32 / G): r / G = r inv_g >> 32 for r G < 2^32
+  float coef;                  // of q.k: sm log2(e), or 2 sm log2(e) / cap
+  float cap;                   // cap log2(e), or 0
+  int32_t window;              // 2^31 - 1 for none
+  float* part;                 // [2 grid][R (D + 2)]
+  int32_t* plan;               // [B RB + 1] tile offsets of the blocks, and their total
+  int4* first;                 // [grid]: the item that a CTA's range begins in: its first tile, tiles, block (of B RB), head
+  uint32_t* failed;            // [grid]: whether a wait of the CTA gave up
+  int32_t grid;
+};
+
+// A request's rows and length, clamped to the page table's capacity (out_status
+// reports what was clamped).
+struct PagedReq {
+  int base, n, len;
+};
+
+__device__ __forceinline__ PagedReq paged_req(const PagedAttnArgs& a, int b) {
+  PagedReq r;
+  const int cap = a.c.max_pages << a.c.page_shift;
+  r.base = a.base[b];
+  r.n = a.n_nodes ? min(max(a.n_nodes[b], 0), a.N) : a.N;
+  if (r.base < 0) r.base = r.n = 0;
+  r.base = min(r.base, cap);
+  r.len = r.n > cap - r.base ? cap : r.base + r.n;
+  return r;
+}
+
+__device__ __forceinline__ int paged_node(const PagedAttnArgs& a, int r) {
+  return static_cast<int>(static_cast<uint64_t>(r) * a.inv_g >> 32);
+}
+
+// What the rows of one block need: slots [first, end), from tile t on.
+struct PagedSpan {
+  int node0, first, end, t, tiles;
+  __device__ __forceinline__ PagedSpan(const PagedAttnArgs& a, const PagedReq& r, int block) {
+    node0 = paged_node(a, block * a.R);
+    const int last = min(paged_node(a, block * a.R + a.R - 1), r.n - 1);
+    end = last < node0 ? 0 : a.parents ? r.len : min(r.len, r.base + last + 1);
+    first = min(max(r.base + (a.parents ? 0 : node0) - a.window + 1, 0), max(end - 1, 0));
+    t = first / kPgTile;
+    tiles = max(1, (end + kPgTile - 1) / kPgTile - t);
+  }
+  // Past every row's window start, as slots: tiles from here on need no mask of it.
+  __device__ __forceinline__ int inside(const PagedAttnArgs& a, const PagedReq& r, int block) const {
+    return r.base + (a.parents ? r.n - 1 : min(paged_node(a, block * a.R + a.R - 1), r.n - 1)) - a.window + 1;
+  }
+};
+
+// A CTA's walk over its range of the line.
+struct PagedCursor {
+  int32_t pos, off;
+  PagedReq rq;
+  int b, block, tiles, h, t0, n, node0, end, inside;   // the piece: tiles t0 .. t0 + n - 1 of item (b, block, h)
+  bool whole, fresh;                                     // whole: the piece is all of its item
+
+  __device__ __forceinline__ void start(const PagedAttnArgs& a, const AttnLine& line, int32_t lo) {
+    pos = lo;
+    off = line.off;
+    b = line.b / a.RB;
+    block = line.b - b * a.RB;
+    n = 0;
+    fresh = true;
+  }
+  // The next piece (called while pos + n < hi); pos is then its first tile.
+  __device__ __forceinline__ void piece(const PagedAttnArgs& a, int32_t hi) {
+    if (fresh) {
+      rq = paged_req(a, b);
+      fresh = false;
+    }
+    PagedSpan s(a, rq, block);
+    while (pos >= (off + s.tiles) * a.c.Hkv) {
+      off += s.tiles;
+      if (++block == a.RB) {
+        block = 0;
+        rq = paged_req(a, ++b);
+      }
+      s = PagedSpan(a, rq, block);
+    }
+    const int rel = pos - off * a.c.Hkv;
+    tiles = s.tiles;
+    h = rel / tiles;
+    const int t = rel - h * tiles;
+    n = min(tiles - t, hi - pos);
+    whole = n == tiles;
+    t0 = s.t + t;
+    node0 = s.node0;
+    end = s.end;
+    inside = s.inside(a, rq, block);
+  }
+  // Of the CTA's first piece.
+  __device__ __forceinline__ int4 item(const PagedAttnArgs& a) const {
+    return make_int4(off * a.c.Hkv + h * tiles, tiles, b * a.RB + block, h);
+  }
+};
+
+// The line for one CTA: every kernel's prologue. [lo, hi) of it is the CTA's.
+template <int kThreads>
+__device__ __forceinline__ void paged_line(const PagedAttnArgs& a, AttnLine* s_line, int32_t* s_warp, int32_t& lo, int32_t& hi) {
+  const int cta = blockIdx.x;
+  const AttnRanges ranges = attn_scan<kThreads>(
+      a.B * a.RB,
+      [&](int e) {
+        const int b = e / a.RB;
+        return PagedSpan(a, paged_req(a, b), e - b * a.RB).tiles;
+      },
+      a.grid, cta, s_line, s_warp, a.c.Hkv, cta == 0 ? a.plan : nullptr);
+  if (cta == 0 && threadIdx.x == 0) a.plan[a.B * a.RB] = s_line->total;
+  lo = cta < ranges.n ? ranges.begin(cta) : 0;
+  hi = cta < ranges.n ? ranges.begin(cta + 1) : 0;
+}
+
+// Pages of a walk through one request, 32 a load: lane l has page 32 g + l of
+// group g, and the next group is on its way.
+struct PagedLook {
+  int group, now, next;
+  __device__ __forceinline__ static int at(const PagedAttnArgs& a, int b, int lp, int end) {
+    return lp << a.c.page_shift < end ? paged_page(a.c, b, lp) : -1;
+  }
+  __device__ __forceinline__ void start(const PagedAttnArgs& a, int b, int lp, int end, int lane) {
+    group = lp >> 5;
+    now = at(a, b, group * 32 + lane, end);
+    next = at(a, b, group * 32 + 32 + lane, end);
+  }
+  // Page lp (the lanes ask for pages of one tile, so of one group).
+  __device__ __forceinline__ int page(const PagedAttnArgs& a, int b, int lp, int end, int lane) {
+    const int g = __shfl_sync(0xffffffffu, lp, 0) >> 5;
+    if (g != group) {
+      group = g;
+      now = next;
+      next = at(a, b, g * 32 + 32 + lane, end);
+    }
+    return __shfl_sync(0xffffffffu, now, lp & 31);
+  }
+};
+
+// Scores in units of log2, before mask and maximum.
+__device__ __forceinline__ float paged_score(const PagedAttnArgs& a, float s) {
+  s *= a.coef;
+  if (a.cap == 0.f) return s;
+  // cap tanh(z / cap) = cap (1 - 2 / (1 + e^(2 z / cap)))
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(s)));
+  return fmaf(-2.f * a.cap, r, a.cap);
+}
+
+// Non-finite 16-bit elements of a 16-byte piece of V as bits: NaN and +inf in
+// the low byte, NaN and -inf in the next.
+template <typename T>
+__device__ __forceinline__ uint32_t nonfinite8(const uint4& w) {
+  constexpr uint32_t e = T::kExpBits == 8 ? 0x7f80u : 0x7c00u;
+  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+  uint32_t r = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t x = v[i] >> (16 * k) & 0xffffu;
+      if ((x & e) != e) continue;
+      const bool nan = (x & 0x7fffu) != e;
+      r |= static_cast<uint32_t>(nan || !(x & 0x8000u)) << (2 * i + k);
+      r |= static_cast<uint32_t>(nan || (x & 0x8000u)) << (8 + 2 * i + k);
+    }
+  return r;
+}
+// Whether any element of the piece is not finite.
+template <typename T>
+__device__ __forceinline__ bool any_nonfinite8(const uint4& w) {
+  constexpr uint32_t e = T::kExpBits == 8 ? 0x7f80u : 0x7c00u, top = T::kExpBits == 8 ? 0x00800080u : 0x04000400u;
+  // an all-ones exponent carries into the sign's place
+  const uint32_t m = e | e << 16;
+  return (((w.x & m) + top) | ((w.y & m) + top) | ((w.z & m) + top) | ((w.w & m) + top)) & 0x80008000u;
+}
+
+// An element of the output and what was taken out of V in its column.
+__device__ __forceinline__ float put_back(float o, bool pos, bool neg) {
+  if (pos) o += INFINITY;
+  if (neg) o -= INFINITY;
+  return o;
+}
+
+// ------------------------------------------------------------------- join
+
+constexpr int kPgJoinThreads = 128;
+constexpr int kPgJoinRows = 16;        // rows a CTA
+constexpr int kPgJoinBatch = 8;
+
+// Joins the pieces of items that several CTAs shared; B more CTAs, before these,
+// check the requests' pages, lengths and trees. A partial is o [R][D] with (max, sum)
+// behind ([R][2]), or, where the lanes that wrote it were rows, o [D][R]: kLanes.
+template <typename T, int D, bool kLanes>
+__global__ void __launch_bounds__(kPgJoinThreads) attn_paged_join_kernel(const PagedAttnArgs a) {
+  const int tid = threadIdx.x;
+  grid_dep_wait();
+  grid_dep_launch();
+  const int groups = a.R / kPgJoinRows;
+  const int total = a.plan[a.B * a.RB] * a.c.Hkv;
+  const AttnRanges ranges(a.grid, total);
+  const int join = static_cast<int>(blockIdx.x) - (a.status ? a.B : 0);
+  if (join < 0) {
+    const int b = blockIdx.x;
+    const PagedReq rq = paged_req(a, b);
+    bool bad_page = a.base[b] < 0 || (a.n_nodes && (a.n_nodes[b] < 0 || a.n_nodes[b] > a.N)) || rq.len - rq.n != a.base[b];
+    for (int j = (rq.n > 0 ? max(rq.base - a.window + 1, 0) >> a.c.page_shift : INT_MAX / 2) + tid;
+         j < (rq.len + (1 << a.c.page_shift) - 1) >> a.c.page_shift; j += kPgJoinThreads)
+      bad_page = bad_page || paged_page(a.c, b, j) < 0;
+    bool tree = false;
+    if (a.parents)
+      for (int n = tid; n < rq.n; n += kPgJoinThreads) tree = tree || bad_parent(a.parents[static_cast<int64_t>(b) * a.N + n], n);
+    const int last = ranges.cta_of(a.plan[(b + 1) * a.RB] * a.c.Hkv - 1);
+    bool late = false;
+    for (int i = ranges.cta_of(a.plan[b * a.RB] * a.c.Hkv) + tid; i <= last; i += kPgJoinThreads) late = late || a.failed[i] != 0;
+    bad_page = __syncthreads_or(bad_page);
+    tree = __syncthreads_or(tree);
+    late = __syncthreads_or(late);
+    if (tid == 0)
+      a.status[b] = (bad_page ? SV_STATUS_BAD_PAGE : 0) | (tree ? SV_STATUS_BAD_PARENT : 0) | (late ? SV_STATUS_TIMEOUT : 0);
+    return;
+  }
+  // One group of CTAs a boundary between ranges; the first boundary within an item joins it.
+  const int at = join / groups + 1;
+  if (at >= ranges.n) return;
+  const int4 item = a.first[at];
+  const int t0 = item.x, e = item.z, h = item.w, c0 = ranges.cta_of(t0), c1 = ranges.cta_of(t0 + item.y - 1);
+  if (ranges.begin(at) == t0 || at != c0 + 1) return;
+  const int in_block = (join - (at - 1) * groups) * kPgJoinRows;
+  const int b = e / a.RB, row0 = (e - b * a.RB) * a.R + in_block;   // of the kv head
+  if (row0 >= a.N * a.G) return;
+  const int slot0 = ranges.begin(c0) == t0 ? 0 : 1;
+  auto partial = [&](int i) { return a.part + static_cast<int64_t>(2 * i + (i == c0 ? slot0 : 0)) * a.R * (D + 2); };
+
+  // A thread has one row and D / 8 of its elements: 8 threads a row.
+  constexpr int kPer = D / 8;
+  __shared__ __align__(16) uint16_t s_o[kPgJoinRows][D + 8];
+  const int r = kLanes ? tid % kPgJoinRows : tid >> 3, d0 = kLanes ? tid / kPgJoinRows * kPer : (tid & 7) * 4;
+  const int row = in_block + r;
+  float m = -INFINITY, l = 0.f, v[kPer];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) v[k] = 0.f;
+  constexpr int kBatch = D == 128 ? kPgJoinBatch / 2 : kPgJoinBatch;
+  for (int i0 = c0; i0 <= c1; i0 += kBatch) {
+    float2 ml[kBatch];
+    float t[kBatch][kPer];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const float* p = partial(min(i0 + k, c1));
+      ml[k] = *reinterpret_cast<const float2*>(p + a.R * D + row * 2);
+      if (kLanes) {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) t[k][j] = p[(d0 + j) * a.R + row];
+      } else {
+#pragma unroll
+        for (int j = 0; j < kPer; j += 4) {
+          const float4 x = *reinterpret_cast<const float4*>(p + row * D + d0 + j * 8);
+          t[k][j] = x.x;
+          t[k][j + 1] = x.y;
+          t[k][j + 2] = x.z;
+          t[k][j + 3] = x.w;
+        }
+      }
+    }
+    float top = m;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) top = i0 + k <= c1 ? fmaxf(top, ml[k].x) : top;
+    const float top0 = top == -INFINITY ? 0.f : top, f0 = ex2(m - top0);
+    l *= f0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) v[j] *= f0;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (i0 + k > c1) break;
+      const float f = ex2(ml[k].x - top0);
+      // Where a piece saw nothing of the row, o is 0 and so is the factor's product.
+      l = fmaf(ml[k].y, f, l);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) v[j] = fmaf(t[k][j], f, v[j]);
+    }
+    m = top;
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int j = 0; j < kPer; j += 2) {
+    const int d = kLanes ? d0 + j : d0 + (j >> 2) * 32 + (j & 3);
+    *reinterpret_cast<uint32_t*>(&s_o[r][d]) = T::pack2(v[j] * inv, v[j + 1] * inv);
+  }
+  const int R = row0 + r;
+  if (a.lse && d0 == 0 && R < a.N * a.G) {
+    const int n = paged_node(a, R);
+    a.lse[(static_cast<int64_t>(b) * a.N + n) * a.Hq + h * a.G + (R - n * a.G)] =
+        l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) + log2f(l)) * kLn2;
+  }
+  __syncthreads();
+  for (int i = tid; i < kPgJoinRows * (D / 8); i += kPgJoinThreads) {
+    const int rr = i / (D / 8), ch = i % (D / 8), RR = row0 + rr;
+    if (RR >= a.N * a.G) break;
+    const int n = paged_node(a, RR);
+    const int64_t at = (static_cast<int64_t>(b) * a.N + n) * a.Hq + h * a.G + (RR - n * a.G);
+    *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + at * D * 2 + ch * 16) = *reinterpret_cast<const uint4*>(&s_o[rr][ch * 8]);
+  }
+}
+
+}  // namespace sv

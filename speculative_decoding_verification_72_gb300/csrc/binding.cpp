@@ -1,5 +1,5 @@
 // Python binding of the verify step's operators (the 8-bit cache, its attention
-// and eviction, token log-probs) over the C ABI of include/spec_verify.h.
+// and eviction, the 16-bit cache and its attention, token log-probs) over the C ABI of include/spec_verify.h.
 //
 // Argument marshalling only. These calls take a few microseconds on the GPU at
 // their smallest, less than the same checks and allocations cost from Python
@@ -223,6 +223,49 @@ std::pair<sv_rows, at::Tensor> rows_of(const at::Tensor& given_t, const char* na
   return {sv_rows{t.data_ptr(), stride(0), stride(1), stride(2)}, t};
 }
 
+struct Paged {
+  sv_paged_cache c;
+  at::Tensor table;
+  at::Device dev{at::kCPU};
+  int64_t H = 0, D = 0;
+  at::ScalarType type = at::kBFloat16;
+  int32_t code = 0;
+};
+
+Paged paged_of(PyObject* o, PyObject* table, int64_t B) {
+  if (!PyTuple_Check(o) || PyTuple_GET_SIZE(o) != 2) refuse("cache must be a PagedCache");
+  const at::Tensor& k = tensor(PyTuple_GET_ITEM(o, 0), "cache.k");
+  const at::Tensor& v = tensor(PyTuple_GET_ITEM(o, 1), "cache.v");
+  if (k.dim() != 4 || !k.is_cuda()) refuse("cache.k must be a CUDA tensor [pages, page size, kv heads, head dim]");
+  if (!same_shape(k.sizes(), v.sizes()) || v.device() != k.device() || v.scalar_type() != k.scalar_type())
+    refuse("cache.v must have cache.k's shape, type and device");
+  Paged r;
+  r.dev = k.device();
+  r.type = k.scalar_type();
+  r.code = dtype_code(k, false, true, "cache.k");
+  const int64_t P = k.size(1);
+  r.H = k.size(2);
+  r.D = k.size(3);
+  if (P != 16 && P != 32 && P != 64 && P != 128) refuse("page size must be 16, 32, 64 or 128, got " + std::to_string(P));
+  if (r.D != 64 && r.D != 128) refuse("head dim must be 64 or 128, got " + std::to_string(r.D));
+  if (k.size(0) < 1 || k.size(0) > INT32_MAX || r.H < 1 || r.H > INT32_MAX) refuse("the cache must have pages and heads");
+  for (const at::Tensor* t : {&k, &v}) {
+    bool well = t->stride(3) == 1 && reinterpret_cast<uintptr_t>(t->data_ptr()) % 16 == 0;
+    for (int64_t d = 0; d < 3; ++d) well = well && (t->size(d) == 1 || (t->stride(d) >= r.D && t->stride(d) % 8 == 0));
+    if (!well)
+      refuse("cache.k and cache.v must have contiguous heads on 16-byte boundaries, and strides of page, token and head that are "
+             "multiples of 16 bytes and no less than a head");
+  }
+  const at::Tensor& t = tensor(table, "page_table");
+  if (t.dim() != 2 || t.size(1) < 1) refuse("page_table must be [B, max_pages]");
+  if (t.size(1) > INT32_MAX) refuse("page_table is too wide");
+  r.table = ints(table, "page_table", {B, t.size(1)}, r.dev);
+  r.c = sv_paged_cache{k.data_ptr(), v.data_ptr(), {k.stride(0), k.stride(1), k.stride(2)}, {v.stride(0), v.stride(1), v.stride(2)},
+                       iptr(r.table), static_cast<int32_t>(k.size(0)), static_cast<int32_t>(r.H), static_cast<int32_t>(P),
+                       static_cast<int32_t>(r.D), static_cast<int32_t>(t.size(1))};
+  return r;
+}
+
 struct Path {
   at::Tensor nodes, n;
   int32_t cols = 0;
@@ -338,6 +381,84 @@ PyObject* kv_evict(PyObject* const* a) {
   const at::Tensor ws = workspace(a[8], spec_kv_evict_q8_workspace_size(i(B), i(c.H), i(keep)), c.dev, stream);
   check(spec_kv_evict_q8(&c.c, i(B), iptr(n), fptr(scores), iptr(positions), i(S), i(keep), i(sinks), iptr(from), fptr(os),
                          iptr(op), iptr(len), iptr(st), ptr(ws), ws.nbytes(), stream));
+  return out.release();
+}
+
+// cache, k_new, v_new, page_table, seq_base, inv_freq, q, parents, n_nodes, interleaved, out
+PyObject* kv_append_rope(PyObject* const* a) {
+  const at::Tensor &k = tensor(a[1], "k_new"), &v = tensor(a[2], "v_new");
+  if (k.dim() != 4 || k.size(1) < 1 || !same_shape(k.sizes(), v.sizes()))
+    refuse("k_new and v_new must be [B, N, kv heads, head dim] of one shape, N at least 1");
+  const int64_t B = k.size(0), N = k.size(1);
+  if (B > INT32_MAX || N > INT32_MAX) refuse("too many rows");
+  const Paged c = paged_of(a[0], a[3], B);
+  const c10::cuda::CUDAGuard guard(c.dev);
+  if (k.scalar_type() != c.type || v.scalar_type() != c.type) refuse("k_new and v_new must have the cache's type");
+  const auto [kr, kt] = rows_of(k, "k_new", c.H, c.D, c.dev);
+  const auto [vr, vt] = rows_of(v, "v_new", c.H, c.D, c.dev);
+  const at::Tensor base = ints(a[4], "seq_base", {B}, c.dev);
+  const at::Tensor& freq = tensor(a[5], "inv_freq");
+  check_dense(freq, "inv_freq", {freq.numel()}, at::kFloat, c.dev);
+  const int64_t rot = 2 * freq.numel();
+  if (rot < 16 || rot > c.D || rot % 16 != 0) refuse("inv_freq must have a multiple of 8 elements, at most half the head dim");
+  const at::Tensor par = given(a[7]) ? ints(a[7], "parents", {B, N}, c.dev) : at::Tensor();
+  const at::Tensor nn = given(a[8]) ? ints(a[8], "n_nodes", {B}, c.dev) : at::Tensor();
+  const int interleaved = PyObject_IsTrue(a[9]);
+  if (interleaved < 0) throw PyFailed{};
+  if (par.defined() && N > SV_MAX_TREE_NODES) refuse("a tree has at most " + std::to_string(SV_MAX_TREE_NODES) + " nodes");
+  Outputs out(a[10], c.dev);
+  sv_rows qr{};
+  at::Tensor q, oq;
+  int64_t Hq = 0;
+  if (given(a[6])) {
+    const at::Tensor& q0 = tensor(a[6], "q");
+    if (q0.dim() != 4 || q0.size(0) != B || q0.size(1) != N || q0.size(2) < 1) refuse("q must be [B, N, heads, head dim] with k_new's B and N");
+    if (q0.scalar_type() != c.type) refuse("q must have the cache's type");
+    Hq = q0.size(2);
+    std::tie(qr, q) = rows_of(q0, "q", Hq, c.D, c.dev);
+    oq = out.get("q", {B, N, Hq, c.D}, c.type);
+  }
+  const at::Tensor len = out.get("out_len", {B}, at::kInt), st = out.get("status", {B}, at::kInt);
+  check(spec_kv_append_rope(&c.c, c.code, &kr, &vr, Hq ? &qr : nullptr, static_cast<int32_t>(B), static_cast<int32_t>(N),
+                            static_cast<int32_t>(std::min<int64_t>(Hq, INT32_MAX)), iptr(base), iptr(par), iptr(nn), fptr(freq),
+                            static_cast<int32_t>(rot), interleaved, ptr(oq), iptr(len), iptr(st),
+                            c10::cuda::getCurrentCUDAStream(c.dev.index()).stream()));
+  return out.release();
+}
+
+// q, cache, page_table, seq_base, parents, n_nodes, sm_scale, softcap, window, slopes, workspace, out
+PyObject* paged_attention(PyObject* const* a) {
+  const at::Tensor& q0 = tensor(a[0], "q");
+  if (q0.dim() != 4 || q0.size(1) < 1) refuse("q must be [B, N, heads, head dim], N at least 1");
+  const int64_t B = q0.size(0), N = q0.size(1), Hq = q0.size(2);
+  if (B > INT32_MAX || N > INT32_MAX || Hq > INT32_MAX) refuse("too many rows");
+  const Paged c = paged_of(a[1], a[2], B);
+  const c10::cuda::CUDAGuard guard(c.dev);
+  if (Hq == 0 || Hq % c.H != 0) refuse("q's heads must be a multiple of the cache's");
+  if (q0.scalar_type() != c.type) refuse("q must have the cache's type");
+  const auto [qr, q] = rows_of(q0, "q", Hq, c.D, c.dev);
+  const at::Tensor base = ints(a[3], "seq_base", {B}, c.dev);
+  const at::Tensor par = given(a[4]) ? ints(a[4], "parents", {B, N}, c.dev) : at::Tensor();
+  const at::Tensor nn = given(a[5]) ? ints(a[5], "n_nodes", {B}, c.dev) : at::Tensor();
+  if (par.defined() && N > SV_MAX_TREE_NODES) refuse("a tree has at most " + std::to_string(SV_MAX_TREE_NODES) + " nodes");
+  const double sm = given(a[6]) ? real(a[6]) : c.D == 64 ? 0.125 : 0.08838834764831845;
+  const double cap = real(a[7]);
+  const int64_t window = integer(a[8]);
+  if (window < 0) refuse("window must not be negative (0: none)");
+  at::Tensor slopes;
+  if (given(a[9])) {
+    slopes = tensor(a[9], "slopes");
+    check_dense(slopes, "slopes", {Hq}, at::kFloat, c.dev);
+  }
+  Outputs out(a[11], c.dev);
+  const at::Tensor o = out.get("out", {B, N, Hq, c.D}, c.type), lse = out.get("lse", {B, N, Hq}, at::kFloat),
+                   st = out.get("status", {B}, at::kInt);
+  void* stream = c10::cuda::getCurrentCUDAStream(c.dev.index()).stream();
+  const auto i = [](int64_t x) { return static_cast<int32_t>(x); };
+  const at::Tensor ws = workspace(a[10], spec_attention_workspace_size(i(B), i(N), i(Hq), i(c.H), i(c.D)), c.dev, stream);
+  check(spec_attention(&qr, c.code, &c.c, i(B), i(N), i(Hq), iptr(base), iptr(par), iptr(nn), static_cast<float>(sm),
+                       static_cast<float>(cap), i(std::min<int64_t>(window, INT32_MAX)), fptr(slopes), ptr(o), fptr(lse), iptr(st),
+                       ptr(ws), ws.nbytes(), stream));
   return out.release();
 }
 
@@ -461,6 +582,8 @@ PyMethodDef g_methods[] = {
     {"attention", fast(guarded<attention, 9>), METH_FASTCALL, nullptr},
     {"attention_weights", fast(guarded<attention_weights, 11>), METH_FASTCALL, nullptr},
     {"kv_evict", fast(guarded<kv_evict, 10>), METH_FASTCALL, nullptr},
+    {"kv_append_rope", fast(guarded<kv_append_rope, 11>), METH_FASTCALL, nullptr},
+    {"paged_attention", fast(guarded<paged_attention, 12>), METH_FASTCALL, nullptr},
     {"token_logprobs", fast(guarded<token_logprobs, 6>), METH_FASTCALL, nullptr},
     {"token_logprobs_backward", fast(guarded<token_logprobs_backward, 7>), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};

@@ -1,6 +1,6 @@
 // Host helpers shared by the C entry points: facts about the current device
 // that are looked up once, launches with programmatic stream serialization,
-// and alignment checks.
+// tensor maps, and checks of arguments.
 #pragma once
 
 #include <atomic>
@@ -8,7 +8,10 @@
 #include <cstring>
 #include <mutex>
 
+#include <cuda.h>
 #include <cuda_runtime.h>
+
+#include "spec_verify.h"
 
 namespace sv {
 
@@ -90,6 +93,30 @@ cudaError_t launch_smem(int grid, int block, size_t smem, size_t most, cudaStrea
     if (cached) SmemSet<Kern>::done.fetch_or(1ull << dev, std::memory_order_release);
   }
   return launch(Kern, grid, block, smem, stream, true, args...);
+}
+
+inline sv_status done(cudaError_t e) { return e == cudaSuccess ? SV_OK : SV_ERR_CUDA; }
+
+inline bool valid_rows(const sv_rows* r, int es) {
+  return r && r->data && aligned(r->data, 16) && r->stride_b * es % 16 == 0 && r->stride_n * es % 16 == 0 &&
+         r->stride_h * es % 16 == 0;
+}
+
+// cuTensorMapEncodeTiled of the loaded driver.
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+inline EncodeTiled encode_tiled() {
+  static std::atomic<void*> found{nullptr};
+  void* f = found.load(std::memory_order_acquire);
+  if (!f) {
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      return nullptr;
+    found.store(f, std::memory_order_release);
+  }
+  return reinterpret_cast<EncodeTiled>(f);
 }
 
 }  // namespace sv

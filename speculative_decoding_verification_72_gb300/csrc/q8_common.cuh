@@ -88,6 +88,9 @@ struct TypeF32 {
 };
 struct TypeBf16 {
   static constexpr int kBytes = 2;
+  static constexpr int kExpBits = 8;
+  static constexpr uint32_t kMma = 1;   // kind::f16's code of the type
+  __device__ static float2 unpack2(uint32_t w) { return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)); }
   __device__ static void unpack8(const uint4& w, float* f) { Elem<2>::unpack(w, f); }
   // max that hands on NaN
   __device__ static uint32_t max2(uint32_t a, uint32_t b) {
@@ -112,6 +115,9 @@ struct TypeBf16 {
 };
 struct TypeF16 {
   static constexpr int kBytes = 2;
+  static constexpr int kExpBits = 5;
+  static constexpr uint32_t kMma = 0;
+  __device__ static float2 unpack2(uint32_t w) { return half2_bits(w); }
   __device__ static uint32_t max2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));

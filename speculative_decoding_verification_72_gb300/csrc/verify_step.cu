@@ -22,8 +22,6 @@ using namespace sv;
 
 constexpr size_t kAlign = 256;
 
-sv_status done(cudaError_t e) { return e == cudaSuccess ? SV_OK : SV_ERR_CUDA; }
-
 bool valid_cache(const sv_q8_cache* c) {
   return c && c->k && c->v && c->k_scale && c->v_scale && c->page_table && aligned(c->k, 16) && aligned(c->v, 16) &&
          aligned(c->k_scale, 4) && aligned(c->v_scale, 4) && aligned(c->page_table, 4) && c->num_pages >= 1 &&
@@ -44,11 +42,6 @@ Q8View view(const sv_q8_cache& c) {
   v.page_shift = c.page_size == 16 ? 4 : c.page_size == 32 ? 5 : c.page_size == 64 ? 6 : 7;
   v.max_pages = c.max_pages;
   return v;
-}
-
-bool valid_rows(const sv_rows* r, int es) {
-  return r && r->data && aligned(r->data, 16) && r->stride_b * es % 16 == 0 && r->stride_n * es % 16 == 0 &&
-         r->stride_h * es % 16 == 0;
 }
 
 int esize(int32_t dtype) { return dtype == SV_F32 ? 4 : dtype == SV_BF16 || dtype == SV_F16 ? 2 : 0; }
@@ -97,23 +90,6 @@ bool valid_row_count(int64_t rows, int64_t G, uint64_t inv_g) {
 int attn_block(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 128; }
 
 constexpr int kAttnGridMost = 320;   // CTAs a workspace is sized for: two an SM of 152, whatever the device
-
-// cuTensorMapEncodeTiled of the loaded driver.
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiled encode_tiled() {
-  static std::atomic<void*> found{nullptr};
-  void* f = found.load(std::memory_order_acquire);
-  if (!f) {
-    cudaDriverEntryPointQueryResult r;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
-        r != cudaDriverEntryPointSuccess)
-      return nullptr;
-    found.store(f, std::memory_order_release);
-  }
-  return reinterpret_cast<EncodeTiled>(f);
-}
 
 // The codes as [pages * heads][page rows][D bytes], read in boxes of a page's
 // head, swizzled for the tensor cores.

@@ -1,0 +1,309 @@
+"""spec_attention over the 16-bit paged cache against the oracle: both kernels, masks, caps, windows, biases."""
+
+import numpy as np
+import pytest
+import torch
+
+import speculative_decoding_verification_72_gb300 as sv
+from oracle import kv_paged as K
+from paged_utils import DEV, check_attention, host_cache, i32, normal, table, to_gpu, tree
+
+pytestmark = pytest.mark.gpu
+
+BF, F16 = torch.bfloat16, torch.float16
+
+
+def run(rng, base, N, H, G, D, P, dtype, parents=None, n_nodes=None, sm=None, cap=0.0, window=0, slopes=None, layout="nhd", tab=None,
+        pages=None, cache=None, q_std=2.0, q=None):
+    B, sm = len(base), D ** -0.5 if sm is None else sm
+    lens = [max(b, 0) + N for b in base]
+    pages = pages or sum(-(-n // P) for n in lens) + 2
+    tab = table(rng, lens, P, pages) if tab is None else tab
+    c = host_cache(rng, pages, P, H, D, dtype) if cache is None else cache
+    hq, gq = normal(rng, (B, N, H * G, D), dtype, q_std) if q is None else q
+    r = sv.spec_attention(gq, to_gpu(c, dtype, layout), i32(tab), i32(base), parents=None if parents is None else i32(parents),
+                          n_nodes=None if n_nodes is None else i32(n_nodes), sm_scale=sm, softcap=cap, window=window,
+                          slopes=None if slopes is None else torch.tensor(slopes, dtype=torch.float32, device=DEV))
+    want = K.attention(hq, c, tab, base, parents, n_nodes, sm, cap, window, slopes)
+    check_attention(r, want, dtype, N * G, cap)
+    return r, want
+
+
+def slopes_of(Hq):
+    return 2.0 ** (-8.0 * np.arange(1, Hq + 1) / Hq)
+
+
+# ------------------------------------------------------- few rows a kv head
+
+@pytest.mark.parametrize("dtype", [BF, F16])
+@pytest.mark.parametrize("D,P", [(128, 16), (64, 32), (64, 128), (128, 64)])
+@pytest.mark.parametrize("N,G", [(1, 1), (1, 4), (3, 5), (6, 4), (1, 32), (16, 2), (32, 1)])
+def test_few_rows(dtype, D, P, N, G):
+    run(np.random.default_rng(N * G + D), [0, 1, 127, 128, 300], N, 2, G, D, P, dtype)
+
+
+@pytest.mark.parametrize("N,G", [(2, 1), (8, 4), (20, 1), (5, 3)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_few_rows_of_trees(N, G, D):
+    rng = np.random.default_rng(N)
+    run(rng, [0, 125, 40, 260], N, 2, G, D, 16, BF, parents=tree(rng, 4, N))
+
+
+# ------------------------------------------------------- many rows a kv head
+
+@pytest.mark.parametrize("dtype", [BF, F16])
+@pytest.mark.parametrize("D,P", [(128, 16), (64, 32), (64, 128), (128, 64)])
+@pytest.mark.parametrize("N,G", [(33, 1), (9, 4), (70, 2), (43, 3), (130, 1)])
+def test_many_rows(dtype, D, P, N, G):
+    run(np.random.default_rng(N * G + D), [0, 1, 127, 300], N, 1, G, D, P, dtype)
+
+
+@pytest.mark.parametrize("N,G", [(64, 4), (33, 1), (200, 2), (20, 7)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_rows_of_trees(N, G, D):
+    rng = np.random.default_rng(N)
+    run(rng, [0, 125, 260], N, 1, G, D, 16, F16 if N == 200 else BF, parents=tree(rng, 3, N, 20 if N == 200 else 5))
+
+
+def test_a_prompt_of_several_blocks():
+    run(np.random.default_rng(8), [0, 77], 300, 1, 2, 64, 32, BF)
+
+
+# ------------------------------------------------------- caps, windows, biases
+
+@pytest.mark.parametrize("N,G", [(1, 4), (6, 5), (20, 4), (140, 2)])
+@pytest.mark.parametrize("cap,window,bias", [(5.0, 0, False), (0.0, 40, False), (0.0, 0, True), (30.0, 130, True), (0.0, 1, False)])
+def test_chain_variants(N, G, cap, window, bias):
+    run(np.random.default_rng(N + window), [0, 90, 300], N, 2, G, 64, 16, BF, cap=cap, window=window,
+        slopes=slopes_of(2 * G) if bias else None, q_std=8.0 if cap else 2.0)
+
+
+@pytest.mark.parametrize("N,G", [(8, 3), (64, 4)])
+@pytest.mark.parametrize("cap,window,bias", [(5.0, 0, False), (0.0, 3, False), (0.0, 0, True), (50.0, 129, True)])
+def test_tree_variants(N, G, cap, window, bias):
+    rng = np.random.default_rng(N + window)
+    run(rng, [0, 126, 300], N, 1, G, 128, 16, F16, parents=tree(rng, 3, N), cap=cap, window=window,
+        slopes=slopes_of(G) if bias else None, q_std=8.0 if cap else 2.0)
+
+
+@pytest.mark.parametrize("N,G", [(2, 4), (20, 4)])
+@pytest.mark.parametrize("sm,cap", [(-0.3, 0.0), (-0.3, 4.0), (0.0, 0.0), (3.0, 0.0), (3.0, 20.0)])
+def test_scales(N, G, sm, cap):
+    run(np.random.default_rng(9), [3, 200], N, 1, G, 64, 16, BF, sm=sm, cap=cap)
+
+
+def test_negative_slopes_and_rising_maxima():
+    """Scores that rise along the line, so that the running maximum does at every tile."""
+    for N, G in ((2, 4), (40, 4)):
+        run(np.random.default_rng(10), [900, 513], N, 1, G, 64, 16, BF, slopes=-np.array([0.1, 0.5, 0.0, 0.25]))
+        run(np.random.default_rng(10), [900, 513], N, 1, G, 64, 16, F16, slopes=np.array([0.1, 0.5, 0.0, 2.0]))
+
+
+# ------------------------------------------------------- pages, counts, trees that are bad
+
+@pytest.mark.parametrize("N,G", [(5, 4), (40, 4)])
+def test_counts_and_missing_pages(N, G):
+    rng = np.random.default_rng(11)
+    base = [100, 40, -1, 17, 0, 150]
+    tab = table(rng, [250] * 6, 16, 120, width=16)
+    tab[0, 2] = -1           # in the prefix
+    tab[3, :] = 4000         # all of them
+    n_nodes = [N, 0, N, N, 1, N + 1]
+    r, want = run(rng, base, N, 2, G, 64, 16, BF, tab=tab, pages=120, n_nodes=n_nodes)
+    assert r["status"].cpu().tolist() == [256, 0, 256, 256, 0, 256]
+    assert (r["out"][1] == 0).all() and (r["out"][3] == 0).all() and (r["out"][4, 1:] == 0).all()
+
+
+@pytest.mark.parametrize("N,G", [(5, 4), (40, 4)])
+def test_a_table_that_is_too_short(N, G):
+    rng = np.random.default_rng(12)
+    r, _ = run(rng, [46, 47, 48, 60], N, 1, G, 64, 16, BF, tab=rng.permutation(12).reshape(4, 3), pages=12)
+    assert (r["status"].cpu() == 256).all()
+
+
+@pytest.mark.parametrize("N,G", [(5, 4), (70, 4)])
+def test_pages_that_no_window_reaches_may_be_gone(N, G):
+    rng = np.random.default_rng(13)
+    tab = table(rng, [600, 600], 16, 90)
+    tab[0, :(500 - 40 + 1) // 16] = -1
+    tab[1, :(300 - 40 + 1) // 16] = 1 << 30
+    r, _ = run(rng, [500, 300], N, 1, G, 64, 16, BF, tab=tab, pages=90, window=40)
+    assert r["status"].cpu().tolist() == [0, 0]
+
+
+@pytest.mark.parametrize("N,G", [(6, 4), (40, 4)])
+def test_bad_parents(N, G):
+    rng = np.random.default_rng(14)
+    par = tree(rng, 4, N)
+    par[0, 4], par[1, 3], par[2, 0] = 5, -1, 2
+    par[3, 5] = -7
+    r, _ = run(rng, [20, 130, 0, 64], N, 1, G, 64, 16, BF, parents=par)
+    assert r["status"].cpu().tolist() == [2, 2, 2, 2]
+
+
+# ------------------------------------------------------- what must not be read
+
+@pytest.mark.parametrize("dtype", [BF, F16])
+@pytest.mark.parametrize("N,G,window", [(6, 4, 0), (6, 4, 50), (40, 4, 0), (40, 4, 50), (1, 2, 7)])
+def test_poison_in_slots_that_are_not_seen(dtype, N, G, window):
+    rng = np.random.default_rng(15)
+    base, P = [0, 37, 100, 250], 16
+    par = tree(rng, 4, N)
+    lens = [b + N for b in base]
+    pages = sum(-(-n // P) for n in lens) + 2
+    tab = table(rng, lens, P, pages)
+    c = host_cache(rng, pages, P, 2, 64, dtype)
+    for b, n in enumerate(lens):   # the last page behind the last row, and pages of no request
+        c["k"][tab[b, (n - 1) // P], n % P or P:], c["v"][tab[b, (n - 1) // P], n % P or P:] = np.nan, np.inf
+    loose = [p for p in range(pages) if p not in tab]
+    c["k"][loose], c["v"][loose] = np.nan, np.nan
+    r, want = run(rng, base, N, 2, G, 64, P, dtype, parents=par, window=window, tab=tab, pages=pages, cache=c)
+    assert np.isfinite(want[0]).all()
+
+
+@pytest.mark.parametrize("N,G", [(6, 4), (40, 4)])
+def test_values_that_are_not_finite_reach_those_who_see_them(N, G):
+    rng = np.random.default_rng(16)
+    base, P = [37, 100], 16
+    par = tree(rng, 2, N)
+    tab = table(rng, [b + N for b in base], P, 30)
+    c = host_cache(rng, 30, P, 1, 64, BF)
+    at = lambda b, p: (tab[b, p // P], p % P, 0)  # noqa: E731
+    c["v"][at(0, base[0] + 3)][5] = np.inf
+    c["v"][at(0, base[0] + 4)][6] = np.nan
+    c["v"][at(0, base[0] + 5)][7] = -np.inf
+    c["v"][at(1, base[1] + 2)][[0, 63]] = np.inf
+    c["v"][at(1, base[1] + 4)][[0, 62]] = -np.inf
+    c["k"][at(1, base[1] + 5)][9] = np.nan
+    r, want = run(rng, base, N, 1, G, 64, P, BF, parents=par, tab=tab, pages=30, cache=c)
+    got = r["out"].double().cpu().numpy()
+    odd = ~np.isfinite(want[0])
+    assert odd.any() and np.array_equal(got[odd], want[0][odd], equal_nan=True)
+
+
+@pytest.mark.parametrize("N,G", [(4, 4), (40, 4)])
+def test_a_query_that_is_not_finite_spoils_its_row_alone(N, G):
+    rng = np.random.default_rng(17)
+    hq, gq = normal(rng, (1, N, G, 64), BF)
+    hq[0, 2, 1, 5], gq[0, 2, 1, 5] = np.nan, float("nan")
+    r, want = run(rng, [150], N, 1, G, 64, 16, BF, q=(hq, gq))
+    got = torch.isnan(r["out"])[0].cpu()
+    assert got[2, 1].all() and int(got.sum()) == 64
+
+
+# ------------------------------------------------------- layouts, streams, graphs
+
+@pytest.mark.parametrize("layout", ["hnd", "joint"])
+@pytest.mark.parametrize("N,G", [(3, 4), (40, 4)])
+def test_layouts(layout, N, G):
+    run(np.random.default_rng(18), [9, 240], N, 3, G, 128, 16, BF, layout=layout)
+
+
+def test_strided_queries():
+    rng = np.random.default_rng(19)
+    for N in (3, 40):
+        hq, gq = normal(rng, (2, N, 4, 64), BF)
+        joint = torch.cat([gq, torch.full_like(gq, float("nan"))], 2)[:, :, :4]
+        odd = torch.empty((2, N, 4, 65), dtype=BF, device=DEV)[..., 1:]
+        odd.copy_(gq)
+        for t in (joint, odd, gq.transpose(0, 1).contiguous().transpose(0, 1)):
+            run(np.random.default_rng(20), [50, 130], N, 1, 4, 64, 16, BF, q=(hq, t))
+
+
+def big(B, N, H, G, D, P, L, dtype, seed):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    W = -(-(L + N) // P)
+    mk = lambda *s: torch.randn(s, generator=g, device=DEV).to(dtype)  # noqa: E731
+    return (mk(B, N, H * G, D), sv.PagedCache(mk(B * W, P, H, D), mk(B * W, P, H, D)),
+            torch.randperm(B * W, generator=g, device=DEV).view(B, W).int())
+
+
+def in_64(q, cache, tab, base, window=0):
+    """Chains in 64 bits with torch: (out, lse, sum p |v|, largest sum |q||k| sm, largest |score|, slots seen)."""
+    B, N, Hq, D = q.shape
+    H = cache.k.shape[2]
+    res = [torch.empty((B, N, Hq, D), dtype=torch.float64) for _ in "oa"] + [torch.empty((B, N, Hq), dtype=torch.float64) for _ in "lszc"]
+    for b in range(B):
+        n = int(base[b]) + N
+        k, v = (t[tab[b].long()].flatten(0, 1)[:n].double() for t in cache)
+        far = (int(base[b]) + torch.arange(N, device=DEV))[:, None] - torch.arange(n, device=DEV)
+        see = (far >= 0) & ((far < window) if window else (far >= 0))
+        for h in range(Hq):
+            kk, vv, qq = k[:, h * H // Hq], v[:, h * H // Hq], q[b, :, h].double()
+            z = (qq @ kk.T * D ** -0.5).masked_fill(~see, -torch.inf)
+            p = torch.softmax(z, -1)
+            for t, x in zip(res, (p @ vv, p @ vv.abs(), torch.logsumexp(z, -1), (qq.abs() @ kk.abs().T * see).amax(-1) * D ** -0.5,
+                                  z.masked_fill(~see, 0).abs().amax(-1), see.sum(-1).double())):
+                t[b, :, h] = x.cpu()
+    o, a, l, s, z, c = (t.numpy() for t in res)
+    return o, l, a, s, z, c
+
+
+@pytest.mark.parametrize("B,N,H,G,D,L,window,dtype", [
+    (1, 1, 1, 4, 128, 70001, 0, BF), (3, 2, 2, 8, 64, 33333, 0, F16), (2, 6, 1, 4, 128, 50000, 4097, BF),
+    (1, 64, 1, 4, 128, 20000, 0, BF), (2, 700, 2, 4, 128, 999, 0, BF), (1, 1500, 1, 8, 64, 0, 0, F16), (1, 1200, 1, 4, 64, 3000, 513, BF)])
+def test_long_lines(B, N, H, G, D, L, window, dtype):
+    q, cache, tab = big(B, N, H, G, D, 16, L, dtype, N + L)
+    base = [max(0, L - 1000 * b) for b in range(B)]
+    r = sv.spec_attention(q, cache, tab, i32(base), window=window)
+    check_attention(r, in_64(q, cache, tab, base, window), dtype, N * G)
+
+
+def test_offsets_past_32_bits():
+    """A cache of more than 2^32 bytes whose last pages are read."""
+    pages = (1 << 32) // (128 * 2 * 128 * 2) + 8
+    k = torch.zeros((pages, 128, 2, 128), dtype=BF, device=DEV)
+    v = torch.zeros_like(k)
+    q, small, tab = big(1, 40, 2, 4, 128, 128, 300, BF, 3)
+    n = small.k.shape[0]
+    k[-n:], v[-n:] = small.k, small.v
+    for rows in (2, 40):
+        a = sv.spec_attention(q[:, :rows], small, tab, i32([300]))
+        b = sv.spec_attention(q[:, :rows], sv.PagedCache(k, v), tab + (pages - n), i32([300]))
+        assert torch.equal(a["out"], b["out"]) and torch.equal(a["lse"], b["lse"])
+
+
+def test_same_again_other_streams_and_graphs():
+    """Bit for bit the same on another stream, with buffers given, and from two graphs whose replays interleave."""
+    base = i32([700, 90, 5000])
+    for N, G in ((3, 4), (40, 4)):
+        q, cache, tab = big(3, N, 2, G, 128, 16, 5000, BF, 1)
+        first = sv.spec_attention(q, cache, tab, base)
+        size = sv.load_library().spec_attention_workspace_size(3, N, 2 * G, 2, 128)
+        out = {n: torch.empty_like(first[n]) for n in first}
+        ws = torch.empty(size, dtype=torch.uint8, device=DEV)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            sv.spec_attention(q, cache, tab, base, workspace=ws, out=out)
+        torch.cuda.current_stream().wait_stream(side)
+        assert all(torch.equal(first[n], out[n]) for n in first)
+        graphs = []
+        for w in (0, 100):
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                graphs.append((g, sv.spec_attention(q, cache, tab, base, window=w), w))
+        sv.spec_attention(q, cache, tab, base)   # a call between, on the kept workspace
+        sides = [torch.cuda.Stream() for _ in graphs]
+        for s, (g, _, _) in zip(sides, graphs):
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for _, got, w in graphs:
+            want = sv.spec_attention(q, cache, tab, base, window=w)
+            assert all(torch.equal(got[n], want[n]) for n in got)
+
+
+def test_requests_that_share_pages_and_many_of_them():
+    q, cache, _ = big(300, 1, 1, 4, 64, 16, 0, BF, 2)
+    tab = torch.arange(4, dtype=torch.int32, device=DEV).repeat(300, 1)
+    base = [(i * 7) % 63 for i in range(300)]
+    r = sv.spec_attention(q, cache, tab, i32(base))
+    check_attention(r, in_64(q, cache, tab, base), BF, 4)
+
+
+def test_no_requests():
+    c = sv.paged_cache(2, 2, 16, 64)
+    e = torch.empty((0, 3, 4, 64), dtype=BF, device=DEV)
+    assert sv.spec_attention(e, c, i32(np.zeros((0, 2))), i32([]))["out"].shape == (0, 3, 4, 64)
