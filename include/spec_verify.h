@@ -608,7 +608,8 @@ sv_status spec_kv_append_rope(const sv_paged_cache* cache, int32_t dtype, const 
  * make the outputs of the rows that see them infinite or NaN. Scores, maxima and sums are
  * fp32; the softmax's terms are rounded to the cache's type where they
  * multiply V, not in their sum (with Hq / Hkv * N up to 32 that is done in two
- * terms, to 2^-16 of a bf16 weight and 2^-21 of an f16 one). N * Hq / Hkv is at most 2^26, and B * Hkv *
+ * terms, to 2^-16 of a bf16 weight and 2^-21 of an f16 one). N * Hq / Hkv is at most 2^26, N + max_pages *
+ * page_size at most 2^31 - 256, and B * Hkv *
  * blocks of 256 rows * max_pages * page_size / 128 below 2^31. A wait inside the
  * kernels that gave up sets SV_STATUS_TIMEOUT, and the output and lse of the
  * rows that it may have touched are NaN. */

@@ -80,11 +80,12 @@ __device__ __forceinline__ int paged_node(const PagedAttnArgs& a, int r) {
 
 // What the rows of one block need: slots [first, end), from tile t on.
 struct PagedSpan {
-  int node0, first, end, t, tiles;
+  int node0, first, end, clear, t, tiles;   // clear: every row of the block sees the slots below it (but for windows)
   __device__ __forceinline__ PagedSpan(const PagedAttnArgs& a, const PagedReq& r, int block) {
     node0 = paged_node(a, block * a.R);
     const int last = min(paged_node(a, block * a.R + a.R - 1), r.n - 1);
     end = last < node0 ? 0 : a.parents ? r.len : min(r.len, r.base + last + 1);
+    clear = a.parents ? r.base : r.base + min(node0 + 1, r.n);
     first = min(max(r.base + (a.parents ? 0 : node0) - a.window + 1, 0), max(end - 1, 0));
     t = first / kPgTile;
     tiles = max(1, (end + kPgTile - 1) / kPgTile - t);
@@ -99,7 +100,7 @@ struct PagedSpan {
 struct PagedCursor {
   int32_t pos, off;
   PagedReq rq;
-  int b, block, tiles, h, t0, n, node0, end, inside;   // the piece: tiles t0 .. t0 + n - 1 of item (b, block, h)
+  int b, block, tiles, h, t0, n, node0, end, clear, inside;   // the piece: tiles t0 .. t0 + n - 1 of item (b, block, h)
   bool whole, fresh;                                     // whole: the piece is all of its item
 
   __device__ __forceinline__ void start(const PagedAttnArgs& a, const AttnLine& line, int32_t lo) {
@@ -134,7 +135,12 @@ struct PagedCursor {
     t0 = s.t + t;
     node0 = s.node0;
     end = s.end;
+    clear = s.clear;
     inside = s.inside(a, rq, block);
+  }
+  // Whether some row of the block does not see all of the tile from tok0 on, of whose pages `there` are there.
+  __device__ __forceinline__ bool special(const PagedAttnArgs& a, int tok0, uint32_t there) const {
+    return tok0 + kPgTile > clear || tok0 < inside || there != (1u << (kPgTile >> a.c.page_shift)) - 1u;
   }
   // Of the CTA's first piece.
   __device__ __forceinline__ int4 item(const PagedAttnArgs& a) const {
@@ -192,32 +198,30 @@ __device__ __forceinline__ float paged_score(const PagedAttnArgs& a, float s) {
   return fmaf(-2.f * a.cap, r, a.cap);
 }
 
-// Non-finite 16-bit elements of a 16-byte piece of V as bits: NaN and +inf in
-// the low byte, NaN and -inf in the next.
+// Whether any 16-bit element of a 16-byte piece of V is not finite: in the sign's
+// places of the result, where an all-ones exponent carries to.
 template <typename T>
 __device__ __forceinline__ uint32_t nonfinite8(const uint4& w) {
-  constexpr uint32_t e = T::kExpBits == 8 ? 0x7f80u : 0x7c00u;
-  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-  uint32_t r = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const uint32_t x = v[i] >> (16 * k) & 0xffffu;
-      if ((x & e) != e) continue;
-      const bool nan = (x & 0x7fffu) != e;
-      r |= static_cast<uint32_t>(nan || !(x & 0x8000u)) << (2 * i + k);
-      r |= static_cast<uint32_t>(nan || (x & 0x8000u)) << (8 + 2 * i + k);
-    }
-  return r;
+  constexpr uint32_t e = T::kExpBits == 8 ? 0x7f807f80u : 0x7c007c00u, one = T::kExpBits == 8 ? 0x00800080u : 0x04000400u;
+  return (((w.x & e) + one) | ((w.y & e) + one) | ((w.z & e) + one) | ((w.w & e) + one)) & 0x80008000u;
 }
-// Whether any element of the piece is not finite.
+
+// Takes the values that are not finite out of a piece of V; what they were, as
+// bits: NaN and +inf in the low byte, NaN and -inf in the next.
 template <typename T>
-__device__ __forceinline__ bool any_nonfinite8(const uint4& w) {
-  constexpr uint32_t e = T::kExpBits == 8 ? 0x7f80u : 0x7c00u, top = T::kExpBits == 8 ? 0x00800080u : 0x04000400u;
-  // an all-ones exponent carries into the sign's place
-  const uint32_t m = e | e << 16;
-  return (((w.x & m) + top) | ((w.y & m) + top) | ((w.z & m) + top) | ((w.w & m) + top)) & 0x80008000u;
+__device__ __forceinline__ uint32_t take_out8(uint4* p) {
+  constexpr uint32_t e = T::kExpBits == 8 ? 0x7f80u : 0x7c00u;
+  uint16_t* v = reinterpret_cast<uint16_t*>(p);
+  uint32_t r = 0;
+#pragma unroll 1
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t x = v[i];
+    if ((x & e) != e) continue;
+    const bool nan = (x & 0x7fffu) != e;
+    r |= (nan || !(x & 0x8000u) ? 1u : 0u) << i | (nan || (x & 0x8000u) ? 1u : 0u) << (8 + i);
+    v[i] = 0;
+  }
+  return r;
 }
 
 // An element of the output and what was taken out of V in its column.

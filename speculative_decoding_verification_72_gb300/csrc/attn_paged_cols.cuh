@@ -74,6 +74,21 @@ __device__ __forceinline__ uint32_t block_off(int rows, int row, int ch) {
   return (ch >> 3) * rows * 128 + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
 }
 
+// What of a token's V row is not finite goes to the rows that see it.
+template <typename T, int D>
+__device__ __noinline__ void note_nonfinite(const uint8_t* vt, int row, uint32_t see, uint32_t* s_inf) {
+  for (int ch = 0; see && ch < D / 8; ++ch) {
+    uint4 w = *reinterpret_cast<const uint4*>(vt + block_off(kPgTile, row, ch));
+    const uint32_t f = take_out8<T>(&w);
+    for (int r = 0; f && r < 16; ++r) {
+      if (!(see >> r & 1)) continue;
+      uint32_t* to = s_inf + r * (D / 16) + (ch >> 2);
+      atomicOr(to, (f & 0xffu) << (ch & 3) * 8);
+      atomicOr(to + D / 32, (f >> 8) << (ch & 3) * 8);
+    }
+  }
+}
+
 // The TMA warp of both kernels: K and V of the CTA's tiles, in turns, into a
 // ring of kStages tiles. s_there has, by tile, which of its pages there are.
 template <int D, int kStages>
@@ -299,8 +314,7 @@ __global__ void __launch_bounds__(PgColLayout<D, MT>::kThreads, 1)
         uint32_t w[16];
         tmem_ld16(t_lane + sb * R + r00, w);
         const uint32_t there = s_there[n & 15];
-        // Whether some row does not see all of the tile: the same for the whole CTA.
-        const bool special = tok0 + kPgTile > rq.base || tok0 < cur.inside || there != (1u << (kPgTile >> a.c.page_shift)) - 1u;
+        const bool special = cur.special(a, tok0, there);   // the same for the whole CTA
         tmem_ld_wait();
         tmem_use(w);
         tc_fence_before();
@@ -336,14 +350,18 @@ __global__ void __launch_bounds__(PgColLayout<D, MT>::kThreads, 1)
           // ---- slow path: masks, maxima, V rows that must not be read
           const bool valid = there >> (row >> a.c.page_shift) & 1 && tok < rq.len;
           uint32_t see = valid ? live : 0u;
-          if (special && see) {
+          if (see && (tok >= rq.base || tok < cur.inside)) {
             const int at = m < 0 ? tok : rq.base + s_depth[m];
+            const uint32_t bit = m < 0 ? 0u : m;
             uint32_t bits = 0;
-#pragma unroll 1
-            for (int r = 0; r < 16; ++r) {
-              bool on = m < 0 || s_anc[r00 + r] >> m & 1;
-              on = on && s_pos[r00 + r] - at < a.window;
-              bits |= static_cast<uint32_t>(on) << r;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint4 anc = reinterpret_cast<const uint4*>(s_anc + r00)[j];
+              const int4 p = reinterpret_cast<const int4*>(s_pos + r00)[j];
+              bits |= ((m < 0 || anc.x >> bit & 1) && p.x - at < a.window ? 1u : 0u) << 4 * j;
+              bits |= ((m < 0 || anc.y >> bit & 1) && p.y - at < a.window ? 2u : 0u) << 4 * j;
+              bits |= ((m < 0 || anc.z >> bit & 1) && p.z - at < a.window ? 4u : 0u) << 4 * j;
+              bits |= ((m < 0 || anc.w >> bit & 1) && p.w - at < a.window ? 8u : 0u) << 4 * j;
             }
             see &= bits;
           }
@@ -358,37 +376,21 @@ __global__ void __launch_bounds__(PgColLayout<D, MT>::kThreads, 1)
             const uint32_t s = 2 * n + 1, st = s % kSt;
             wait_or_fail(full + 8 * st, (s / kSt) & 1, fail);
             uint8_t* vt = smem + st * L::kTileBytes;
-            uint32_t bad = 0;   // 16-byte pieces of the token's V row with values that are not finite
+            uint32_t odd = 0;
             if (valid) {
 #pragma unroll
-              for (int ch = 0; ch < D / 8; ++ch)
-                bad |= static_cast<uint32_t>(any_nonfinite8<T>(*reinterpret_cast<const uint4*>(vt + block_off(kPgTile, row, ch)))) << ch;
-              any_inf = any_inf || bad != 0;
-#pragma unroll 1
-              for (int ch = 0; ch < D / 8; ++ch) {
-                if (!(bad >> ch & 1)) continue;
-                const uint32_t f = nonfinite8<T>(*reinterpret_cast<const uint4*>(vt + block_off(kPgTile, row, ch)));
-                for (int r = 0; r < 16; ++r) {
-                  if (!(see >> r & 1)) continue;
-                  uint32_t* to = &s_inf[(r00 + r) * (D / 16) + (ch >> 2)];
-                  atomicOr(to, (f & 0xffu) << (ch & 3) * 8);
-                  atomicOr(to + D / 32, (f >> 8) << (ch & 3) * 8);
-                }
-              }
+              for (int ch = 0; ch < D / 8; ++ch) odd |= nonfinite8<T>(*reinterpret_cast<const uint4*>(vt + block_off(kPgTile, row, ch)));
+            } else if (grp == 0) {
+#pragma unroll
+              for (int ch = 0; ch < D / 8; ++ch) *reinterpret_cast<uint4*>(vt + block_off(kPgTile, row, ch)) = make_uint4(0, 0, 0, 0);
             }
-            named_barrier_sync(3, kSoft);   // every group has read the row, and its maxima are there
-            if (grp == 0) {
+            if (named_barrier_or(3, kSoft, odd != 0)) {   // rare; maxima are there past it
+              any_inf = true;
+              note_nonfinite<T, D>(vt, row, odd ? see : 0u, s_inf + r00 * (D / 16));
+              named_barrier_sync(3, kSoft);   // every group has read the row
+              if (grp == 0 && odd)
 #pragma unroll 1
-              for (int ch = 0; ch < D / 8; ++ch) {
-                uint16_t* p = reinterpret_cast<uint16_t*>(vt + block_off(kPgTile, row, ch));
-                if (!valid) {
-                  *reinterpret_cast<uint4*>(p) = make_uint4(0, 0, 0, 0);
-                } else if (bad >> ch & 1) {
-                  const uint32_t f = nonfinite8<T>(*reinterpret_cast<const uint4*>(p));
-                  for (int j = 0; j < 8; ++j)
-                    if ((f | f >> 8) >> j & 1) p[j] = 0;
-                }
-              }
+                for (int ch = 0; ch < D / 8; ++ch) take_out8<T>(reinterpret_cast<uint4*>(vt + block_off(kPgTile, row, ch)));
             }
             fence_async_smem();
           } else {
@@ -454,7 +456,6 @@ __global__ void __launch_bounds__(PgColLayout<D, MT>::kThreads, 1)
       }
       // ---- the piece's sums and O^T
       wait_or_fail(p_free, (n - 1) & 1, fail);
-      any_inf = named_barrier_or(bar, 128, any_inf);
       {
         // 16 sums over 32 lanes: halve the rows a lane holds, then the lanes; lane 2 r ends with row r
         float v[16];

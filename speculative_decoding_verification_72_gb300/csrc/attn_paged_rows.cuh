@@ -11,15 +11,16 @@
 // next tile, PV_1, S_1 in turn. S and O of both halves fill all 512 columns of
 // TMEM; one CTA an SM.
 //
-// A thread has one row: it reads all of its 128 scores into registers, so
-// maximum, exponentials and sum are its own. The running maximum is raised only
+// A thread has one row, so maximum, exponentials and sum are its own. It reads
+// its 128 scores 64 at a time: the first for the maximum alone, the second for
+// maximum and exponentials, then the first again; all 128 at once do not fit its
+// registers. The running maximum is raised only
 // when a score exceeds it by 2^8; the warp then rescales its rows of O, which no
 // product touches between S's arrival and P's. P is rounded to 16 bits (half a
 // step of the type: 2^-8 of a bf16 weight, 2^-11 of f16's), its sum is not.
 //
-// A tile that some row does not see whole is masked in TMEM first: the thread
-// turns its row of S into final scores, with -inf where it does not see, and
-// the common path takes them as they are.
+// A tile that some row does not see whole is masked in registers by 128 bits that
+// the thread works out from its row's position and path.
 //
 // Warps 0-3 and 4-7: softmax. 8: TMA. 9: MMA.
 #pragma once
@@ -39,7 +40,7 @@ struct PgRowLayout {
   static constexpr int kOffQ = kStages * kTileBytes;                     // [2 halves][128 rows]
   static constexpr int kOffMisc = kOffQ + 2 * kTileBytes;
   // V's non-finite columns by token (two tiles), by row; parents and depths of the nodes
-  static constexpr int kMiscBytes = 2 * 128 * (D / 16) * 4 + kPgRowBlock * (D / 16) * 4 + SV_MAX_TREE_NODES * 4;
+  static constexpr int kMiscBytes = 2 * 128 * (D / 16) * 4 + kPgRowBlock * (D / 16) * 4 + SV_MAX_TREE_NODES * 4 + kPgTile * 4;
   static constexpr int kBytes = 1024 + kOffMisc + kMiscBytes;
 };
 
@@ -54,6 +55,18 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
       : "r"(addr));
 }
 
+// The bits below bit x of a word.
+__device__ __forceinline__ uint32_t below(int x) { return x <= 0 ? 0u : x >= 32 ? 0xffffffffu : (1u << x) - 1u; }
+
+// What was taken out of the tokens of a tile that a row sees, into the row's flags.
+template <int D>
+__device__ __noinline__ void note_seen(const uint32_t* flags, uint32_t s0, uint32_t s1, uint32_t s2, uint32_t s3, uint32_t* to) {
+  const uint32_t see[4] = {s0, s1, s2, s3};
+  for (int t = 0; t < kPgTile; ++t)
+    if (see[t >> 5] >> (t & 31) & 1)
+      for (int w = 0; w < D / 16; ++w) to[w] |= flags[t * (D / 16) + w];
+}
+
 // kVar: scores are capped or biased.
 template <typename T, int D, bool kVar>
 __global__ void __launch_bounds__(kPgRowThreads, 1)
@@ -64,19 +77,20 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
   __shared__ AttnLine s_line;
   __shared__ int32_t s_warp[kPgRowThreads / 32];
   __shared__ __align__(8) uint64_t s_bar[2 * kSt + 7];
-  __shared__ uint32_t s_tmem, s_fail, s_there[16], s_bad[2];   // s_bad: by tile modulo 2, the last (+ 1) with values taken out
+  __shared__ uint32_t s_tmem, s_fail, s_there[16];
   const uint32_t smem0 = (smem_u32(raw) + 1023u) & ~1023u;
   uint8_t* smem = raw + (smem0 - smem_u32(raw));
   uint32_t* s_tok = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);     // [2][128][2][D / 32] columns with +inf, -inf (NaN: both)
   uint32_t* s_row = s_tok + 2 * 128 * (D / 16);                          // [256][2][D / 32]
   int16_t* s_par = reinterpret_cast<int16_t*>(s_row + kPgRowBlock * (D / 16));   // [nodes]
   int16_t* s_depth = s_par + SV_MAX_TREE_NODES;                          // [nodes]
+  float* s_at = reinterpret_cast<float*>(s_depth + SV_MAX_TREE_NODES);   // [128] positions of a tile's tokens
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t full = smem_u32(s_bar), empty = full + 8 * kSt, s_ready = empty + 8 * kSt, p_ready = s_ready + 16;
   const uint32_t o_done = p_ready + 16, q_ready = o_done + 16;
   if (tid == 0) {
-    s_fail = s_bad[0] = s_bad[1] = 0;
+    s_fail = 0;
     for (int i = 0; i < kSt; ++i) {
       mbar_init(full + 8 * i, 1);
       mbar_init(empty + 8 * i, 1);
@@ -145,8 +159,9 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
-            for (int k = 0; k < kPgTile / 16; ++k)
-              tc_mma_f16_ts(tmem + 256 + g * 128, tmem + g * 128 + k * 8, tc_desc(vt + 2048 * k, kPgTile * 128, 1024, 2), kIdO, i > 0 || k > 0);
+            for (int k = 0; k < kPgTile / 16; ++k)   // P's halves lie where those of S did
+              tc_mma_f16_ts(tmem + 256 + g * 128, tmem + g * 128 + (k & 3) * 8 + (k >> 2) * 64,
+                            tc_desc(vt + 2048 * k, kPgTile * 128, 1024, 2), kIdO, i > 0 || k > 0);
             if (g + 1 == gs) tc_commit(empty + 8 * st);
             // The next S overwrites this P: products of one CTA run in the order they are issued.
             if (i + 1 < cur.n)
@@ -218,6 +233,8 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
       const int pos = rq.base + depth;
       const float slope = kVar && a.slopes && node >= 0 ? a.slopes[cur.h * a.G + Rg - at * a.G] * kLog2e : 0.f;
       const float coef = fabsf(a.coef);
+      const int open = max(pos - a.window + 1, 0);   // the window's first position
+      const int pos0 = rq.base;   // positions relative to it are small enough for fp32
 
       float m_run = 0.f, l = 0.f;   // m_run means something once the row has seen a slot
       bool seen = false;
@@ -227,120 +244,139 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
         wait_or_fail(s_ready + 8 * g, tiles_done & 1, fail);   // and every product before this S is done
         tc_fence_after();
         const uint32_t there = s_there[n & 15];
-        const bool special = tok0 + kPgTile > rq.base || tok0 < cur.inside || there != (1u << (kPgTile >> a.c.page_shift)) - 1u;
+        const bool special = cur.special(a, tok0, there);
+        uint32_t see[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};   // what the row sees of the tile
         if (special) {
-          // ---- V's rows that must not be read, the same for every row
-          {
-            const uint32_t s = 2 * n + 1, st = s % kSt;
-            wait_or_fail(full + 8 * st, (s / kSt) & 1, fail);
-            uint8_t* vt = smem + st * L::kTileBytes;
-            uint32_t* flags = s_tok + ((n & 1) * 128 + row) * (D / 16);
-            const bool valid = there >> (row >> a.c.page_shift) & 1 && tok0 + row < rq.len;
-            const int c0 = gs == 2 ? g * (D / 16) : 0, c1 = gs == 2 ? c0 + D / 16 : D / 8;   // the thread's pieces of token `row`
-#pragma unroll 1
-            for (int w0 = c0; w0 < c1; w0 += 4) {
-              uint32_t up = 0, down = 0;
-              for (int ch = w0; ch < w0 + 4; ++ch) {
-                uint4* p = reinterpret_cast<uint4*>(vt + block_off(kPgTile, row, ch));
-                if (!valid) {
-                  *p = make_uint4(0, 0, 0, 0);
-                } else if (any_nonfinite8<T>(*p)) {
-                  const uint32_t f = nonfinite8<T>(*p);
-                  for (int j = 0; j < 8; ++j)
-                    if ((f | f >> 8) >> j & 1) reinterpret_cast<uint16_t*>(p)[j] = 0;
-                  up |= (f & 0xffu) << (ch & 3) * 8;
-                  down |= (f >> 8) << (ch & 3) * 8;
-                  *const_cast<volatile uint32_t*>(&s_bad[n & 1]) = n + 1;
-                }
-              }
-              flags[w0 >> 2] = up;
-              flags[D / 32 + (w0 >> 2)] = down;
-            }
-            fence_async_smem();
-            named_barrier_sync(1, soft);
-          }
-          // ---- final scores of the thread's row over S, -inf where it does not see
-          const bool bad = *const_cast<volatile uint32_t*>(&s_bad[n & 1]) == n + 1;
-          uint32_t anc[4] = {0, 0, 0, 0};   // tokens of the tile on the row's path
-          if (a.parents)
-            for (int m = node; m >= 0; m = s_par[m]) {
+          if (a.parents) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) see[j] = below(rq.base - tok0 - 32 * j);
+            int far = 0;
+            for (int m = node; m >= 0 && far < a.window; m = s_par[m], ++far) {
               const int c = rq.base + m - tok0;
               if (c < 0) break;   // parents come before
 #pragma unroll
               for (int j = 0; j < 4; ++j)
-                if (c >> 5 == j) anc[j] |= 1u << (c & 31);
+                if (c >> 5 == j) see[j] |= 1u << (c & 31);
             }
-#pragma unroll 1
-          for (int j = 0; j < 8; ++j) {
-            uint32_t s[16];
-            __syncwarp();
-            tmem_ld16(t_s + j * 16, s);
-            uint32_t path = 0;
+          }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) path = j >> 1 == k ? anc[k] : path;
-            path >>= (j & 1) * 16;
-            const bool page = there >> (j * 16 >> a.c.page_shift) & 1;
-            tmem_ld_wait();
-            tmem_use(s);
+          for (int j = 0; j < 4; ++j) {
+            const int c = tok0 + 32 * j;
+            if (!a.parents) see[j] = below(rq.base + node + 1 - c);
+            const uint32_t prefix = a.parents ? below(rq.base - c) : 0xffffffffu;   // slots whose positions are their places
+            see[j] &= below(rq.len - c) & ~(prefix & below(open - c));
+            if (!(there >> (32 * j >> a.c.page_shift) & 1)) see[j] &= 0xffff0000u;
+            if (!(there >> ((32 * j + 16) >> a.c.page_shift) & 1)) see[j] &= 0x0000ffffu;
+            if (node < 0) see[j] = 0;
+          }
+          // ---- V's rows that must not be read, the same for every row
+          const uint32_t s = 2 * n + 1, st = s % kSt;
+          wait_or_fail(full + 8 * st, (s / kSt) & 1, fail);
+          uint8_t* vt = smem + st * L::kTileBytes;
+          const bool valid = there >> (row >> a.c.page_shift) & 1 && tok0 + row < rq.len;
+          uint32_t odd = 0;
+#pragma unroll
+          for (int ch = 0; ch < D / 8; ++ch) {
+            if (gs == 2 && ch / (D / 16) != g) continue;   // the thread's pieces of token `row`
+            uint4* p = reinterpret_cast<uint4*>(vt + block_off(kPgTile, row, ch));
+            if (valid)
+              odd |= nonfinite8<T>(*p);
+            else
+              *p = make_uint4(0, 0, 0, 0);
+          }
+          if (named_barrier_or(1, soft, odd != 0)) {   // rare
+            uint32_t* flags = s_tok + (n & 1) * 128 * (D / 16);
+            for (int ch = gs == 2 ? g * (D / 16) : 0; ch < (gs == 2 ? (g + 1) * (D / 16) : D / 8); ++ch) {
+              const uint32_t f = valid ? take_out8<T>(reinterpret_cast<uint4*>(vt + block_off(kPgTile, row, ch))) : 0u;
+              uint8_t* to = reinterpret_cast<uint8_t*>(flags + row * (D / 16)) + ch;
+              to[0] = static_cast<uint8_t>(f);
+              to[D / 8] = static_cast<uint8_t>(f >> 8);
+            }
+            named_barrier_sync(1, soft);
+            note_seen<D>(flags, see[0], see[1], see[2], see[3], s_row + (g * 128 + row) * (D / 16));
+          }
+          fence_async_smem();
+          if (kVar && a.slopes && a.parents) {
+            named_barrier_sync(1, soft);   // every row has read the last such tile's positions
+            const int m = tok0 + row - rq.base;
+            if (g == 0) s_at[row] = static_cast<float>(m >= 0 && m < rq.n ? rq.base + s_depth[m] - pos0 : tok0 + row - pos0);
+            named_barrier_sync(1, soft);
+          }
+          __syncwarp();
+        }
+        // ---- 64 scores, in units of log2
+        const float c = kVar ? 1.f : coef;
+        auto scores = [&](uint32_t (&w)[64], int half) {
+          tmem_ld32(t_s + half * 64, w);
+          tmem_ld32(t_s + half * 64 + 32, w + 32);
+          tmem_ld_wait();
+          tmem_use(w);
+          if (kVar) {
+            if (a.cap != 0.f) {
+#pragma unroll
+              for (int j = 0; j < 64; ++j) {
+                float r;
+                asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(__uint_as_float(w[j]) * coef)));
+                w[j] = __float_as_uint(fmaf(-2.f * a.cap, r, a.cap));
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < 64; ++j) w[j] = __float_as_uint(__uint_as_float(w[j]) * coef);
+            }
+            if (a.slopes) {
+              if (special && a.parents) {
+                const float off = static_cast<float>(pos0 - pos);
+#pragma unroll
+                for (int j = 0; j < 64; j += 4) {
+                  const float4 at4 = *reinterpret_cast<const float4*>(s_at + half * 64 + j);
+                  w[j] = __float_as_uint(fmaf(slope, at4.x + off, __uint_as_float(w[j])));
+                  w[j + 1] = __float_as_uint(fmaf(slope, at4.y + off, __uint_as_float(w[j + 1])));
+                  w[j + 2] = __float_as_uint(fmaf(slope, at4.z + off, __uint_as_float(w[j + 2])));
+                  w[j + 3] = __float_as_uint(fmaf(slope, at4.w + off, __uint_as_float(w[j + 3])));
+                }
+              } else {
+                const float off = static_cast<float>(tok0 + half * 64 - pos);
+#pragma unroll
+                for (int j = 0; j < 64; ++j) w[j] = __float_as_uint(fmaf(slope, off + static_cast<float>(j), __uint_as_float(w[j])));
+              }
+            }
+          }
+          if (special) {
+#pragma unroll
+            for (int j = 0; j < 64; ++j) w[j] = see[half * 2 + (j >> 5)] >> (j & 31) & 1 ? w[j] : 0xff800000u;
+          }
+        };
+        auto largest = [](const uint32_t (&w)[64]) {
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int j = 0; j < 64; j += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mx[k] = fmaxf(fmaxf(mx[k], __uint_as_float(w[j + 2 * k])), __uint_as_float(w[j + 2 * k + 1]));
+          return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        };
+        // ---- exponentials, their sum, P over the scores
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        auto weights = [&](const uint32_t (&w)[64], int half) {
+          const float2 c2 = make_float2(c, c), m2 = make_float2(-m_run, -m_run);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            uint32_t h[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
-              const int tok = tok0 + j * 16 + k, m = tok - rq.base;
-              bool on = page && node >= 0 && tok < rq.len;
-              int from = tok;
-              if (m >= 0 && on) {
-                on = a.parents ? path >> k & 1 : m <= node;
-                if (a.parents) from = rq.base + s_depth[m];
-              }
-              on = on && pos - from < a.window;
-              float x = __uint_as_float(s[k]) * coef;
-              if (kVar) {
-                if (a.cap != 0.f) {
-                  float r;
-                  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(x)));
-                  x = fmaf(-2.f * a.cap, r, a.cap);
-                }
-                x = fmaf(slope, static_cast<float>(from - pos), x);
-              }
-              s[k] = on ? __float_as_uint(x) : 0xff800000u;
-              if (bad && on) {
-                const uint32_t* f = s_tok + ((n & 1) * 128 + j * 16 + k) * (D / 16);
-                for (int w = 0; w < D / 16; ++w) s_row[(g * 128 + row) * (D / 16) + w] |= f[w];
-              }
+              const float2 x = __ffma2_rn(make_float2(__uint_as_float(w[32 * j + 2 * k]), __uint_as_float(w[32 * j + 2 * k + 1])), c2, m2);
+              const float2 p = make_float2(ex2(x.x), ex2(x.y));
+              sum[k & 1] = __fadd2_rn(sum[k & 1], p);
+              h[k] = T::pack2(p.x, p.y);
             }
-            __syncwarp();
-            tmem_st16(t_s + j * 16, s);
+            tmem_st16(t_s + half * 64 + j * 16, h);
           }
-          tmem_st_wait();
-        }
-        // ---- scores into registers, in units of log2
-        uint32_t w[128];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) tmem_ld32(t_s + j * 32, w + 32 * j);
-        tmem_ld_wait();
-        tmem_use(w);
-        float c = special ? 1.f : coef;
-        if (kVar && !special) {
-          c = 1.f;
-          const float far = static_cast<float>(tok0 - pos);
-#pragma unroll
-          for (int j = 0; j < 128; ++j) {
-            float x = __uint_as_float(w[j]) * coef;
-            if (a.cap != 0.f) {
-              float r;
-              asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(x)));
-              x = fmaf(-2.f * a.cap, r, a.cap);
-            }
-            w[j] = __float_as_uint(fmaf(slope, far + static_cast<float>(j), x));
-          }
-        }
-        // ---- maximum
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int j = 0; j < 128; j += 8)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mx[k] = fmaxf(fmaxf(mx[k], __uint_as_float(w[j + 2 * k])), __uint_as_float(w[j + 2 * k + 1]));
-        const float most = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        };
+        uint32_t w[64];
+        scores(w, 0);
+        float most = largest(w);
+        scores(w, 1);
+        most = fmaxf(most, largest(w));
         const float top = most == -INFINITY ? -INFINITY : fmaf(most, c, -m_run);
         const bool raise = seen ? top > kPgSlack + kPgLift<T> : top > -INFINITY;
         if (__any_sync(0xffffffffu, raise)) {
@@ -361,21 +397,9 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
             }
           }
         }
-        // ---- exponentials, their sum, P
-        const float2 c2 = make_float2(c, c), m2 = make_float2(-m_run, -m_run);
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t h[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const float2 x = __ffma2_rn(make_float2(__uint_as_float(w[32 * j + 2 * k]), __uint_as_float(w[32 * j + 2 * k + 1])), c2, m2);
-            const float2 p = make_float2(ex2(x.x), ex2(x.y));
-            sum[k & 1] = __fadd2_rn(sum[k & 1], p);
-            h[k] = T::pack2(p.x, p.y);
-          }
-          tmem_st16(t_s + j * 16, h);
-        }
+        weights(w, 1);
+        scores(w, 0);
+        weights(w, 0);
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         tmem_st_wait();
         tc_fence_before();

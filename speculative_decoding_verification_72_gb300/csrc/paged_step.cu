@@ -200,6 +200,7 @@ sv_status spec_attention(const sv_rows* q, int32_t dtype, const sv_paged_cache* 
   a.coef = static_cast<float>(softcap > 0.f ? 2.0 * scale / softcap : scale);
   a.cap = static_cast<float>(softcap * 1.4426950408889634);
   if (!std::isfinite(a.coef) || !std::isfinite(a.cap)) return SV_ERR_INVALID_ARG;
+  if (std::fabs(a.coef) < 1e-30f) a.coef = 1e-30f;   // 0 times a masked -inf would be NaN
   a.q = static_cast<const uint8_t*>(q->data);
   a.sqb = q->stride_b * 2;
   a.sqn = q->stride_n * 2;
@@ -226,7 +227,7 @@ sv_status spec_attention(const sv_rows* q, int32_t dtype, const sv_paged_cache* 
   a.plan = reinterpret_cast<int32_t*>(ws + p.off_plan);
   const int64_t items = B * p.RB * cache->Hkv;
   const int64_t tiles = (static_cast<int64_t>(cache->max_pages) * cache->page_size + kPgTile - 1) / kPgTile;
-  if (items > INT32_MAX / tiles) return SV_ERR_INVALID_ARG;
+  if (items > INT32_MAX / tiles || static_cast<int64_t>(cache->max_pages) * cache->page_size + N > INT32_MAX - 255) return SV_ERR_INVALID_ARG;
   a.grid = static_cast<int32_t>(std::min<int64_t>({sm_count(), kPagedGridMost, items * tiles}));
   CUtensorMap k, v;
   if (!page_map(*cache, a.c, 0, &k) || !page_map(*cache, a.c, 1, &v)) return SV_ERR_CUDA;
