@@ -5,24 +5,28 @@
 // and V; for each half g
 //   S_g [128 rows, 128 tokens] = q_g K^T,   O_g [128 rows, D] += P_g V,
 // K and V as TMA brings them (V transposed by the descriptor), P_g in the type
-// of V over the columns of S_g in TMEM. Per tile and half the products take
-// 8 D clocks and the 128 x 128 exponentials 1024 (16 a clock), so one half's
-// softmax runs under the other's products: the MMA warp issues PV_0, S_0 of the
-// next tile, PV_1, S_1 in turn. S and O of both halves fill all 512 columns of
-// TMEM; one CTA an SM.
+// of V over the columns of S_g in TMEM. Per tile the products of a half take
+// 8 D clocks and its 128 x 128 exponentials 512 (32 a clock). S and O of both
+// halves fill all 512 columns of TMEM, so within a half S, softmax and P V
+// follow each other and one half's softmax runs under the other's products; one
+// CTA an SM.
 //
-// A thread has one row, so maximum, exponentials and sum are its own. It reads
-// its 128 scores 64 at a time: the first for the maximum alone, the second for
-// maximum and exponentials, then the first again; all 128 at once do not fit its
-// registers. The running maximum is raised only
-// when a score exceeds it by 2^8; the warp then rescales its rows of O, which no
-// product touches between S's arrival and P's. P is rounded to 16 bits (half a
-// step of the type: 2^-8 of a bf16 weight, 2^-11 of f16's), its sum is not.
+// A thread has one row, so maximum, exponentials and sum are its own. It takes
+// 64 tokens at a time: P of the first 64 is multiplied while those of the others
+// are worked out. The exponentials do not wait for the maximum: they go by the
+// running maximum, and are done again in the rare case that a score exceeds it
+// by more than 2^8 (or is the row's first). The warp then rescales its rows of O.
+// P is rounded to 16 bits (half a step of the type: 2^-8 of a bf16 weight, 2^-11
+// of f16's), its sum is not.
 //
 // A tile that some row does not see whole is masked in registers by 128 bits that
-// the thread works out from its row's position and path.
+// the thread works out from its row's position and path; what must not be read of
+// its V is taken out by a warp of its own, as soon as the tile is there.
 //
-// Warps 0-3 and 4-7: softmax. 8: TMA. 9: MMA.
+// The rows of the next piece's q are loaded while the last products run, and
+// take their place once the output has left it.
+//
+// Warps 0-3 and 4-7: softmax. 8: TMA. 9 and 10: MMA of the halves. 11: V.
 #pragma once
 
 #include "attn_paged_cols.cuh"
@@ -30,17 +34,18 @@
 
 namespace sv {
 
-constexpr int kPgRowThreads = 320;
+constexpr int kPgRowThreads = 384;
 constexpr int kPgRowBlock = 256;
 
 template <int D>
 struct PgRowLayout {
   static constexpr int kTileBytes = kPgTile * D * 2;
   static constexpr int kStages = 128 * 1024 / kTileBytes;
+  static constexpr int kDepth = kStages / 2;                             // V tiles in the ring
   static constexpr int kOffQ = kStages * kTileBytes;                     // [2 halves][128 rows]
   static constexpr int kOffMisc = kOffQ + 2 * kTileBytes;
-  // V's non-finite columns by token (two tiles), by row; parents and depths of the nodes
-  static constexpr int kMiscBytes = 2 * 128 * (D / 16) * 4 + kPgRowBlock * (D / 16) * 4 + SV_MAX_TREE_NODES * 4 + kPgTile * 4;
+  // V's non-finite columns by token and by row; parents and depths of the nodes; positions of a tile's tokens by half
+  static constexpr int kMiscBytes = (kDepth * 128 + kPgRowBlock) * (D / 16) * 4 + SV_MAX_TREE_NODES * 4 + 2 * kPgTile * 4;
   static constexpr int kBytes = 1024 + kOffMisc + kMiscBytes;
 };
 
@@ -72,35 +77,38 @@ template <typename T, int D, bool kVar>
 __global__ void __launch_bounds__(kPgRowThreads, 1)
     attn_paged_rows_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, const PagedAttnArgs a) {
   using L = PgRowLayout<D>;
-  constexpr int kSt = L::kStages;
+  constexpr int kSt = L::kStages, kDepth = L::kDepth;
   extern __shared__ uint8_t raw[];
   __shared__ AttnLine s_line;
   __shared__ int32_t s_warp[kPgRowThreads / 32];
-  __shared__ __align__(8) uint64_t s_bar[2 * kSt + 7];
-  __shared__ uint32_t s_tmem, s_fail, s_there[16];
+  __shared__ __align__(8) uint64_t s_bar[2 * kSt + kDepth + 12];
+  __shared__ uint32_t s_tmem, s_fail, s_there[16], s_odd[kDepth];   // s_odd: whether values were taken out of a tile's V
   const uint32_t smem0 = (smem_u32(raw) + 1023u) & ~1023u;
   uint8_t* smem = raw + (smem0 - smem_u32(raw));
-  uint32_t* s_tok = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);     // [2][128][2][D / 32] columns with +inf, -inf (NaN: both)
-  uint32_t* s_row = s_tok + 2 * 128 * (D / 16);                          // [256][2][D / 32]
-  int16_t* s_par = reinterpret_cast<int16_t*>(s_row + kPgRowBlock * (D / 16));   // [nodes]
+  uint32_t* s_tok = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);     // [kDepth][128][2][D / 32] columns with +inf, -inf (NaN: both)
+  uint32_t* s_row = s_tok + kDepth * 128 * (D / 16);                     // [256][2][D / 32]
+  float* s_at = reinterpret_cast<float*>(s_row + kPgRowBlock * (D / 16));   // [2][128] positions of a tile's tokens
+  int16_t* s_par = reinterpret_cast<int16_t*>(s_at + 2 * kPgTile);       // [nodes]
   int16_t* s_depth = s_par + SV_MAX_TREE_NODES;                          // [nodes]
-  float* s_at = reinterpret_cast<float*>(s_depth + SV_MAX_TREE_NODES);   // [128] positions of a tile's tokens
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t full = smem_u32(s_bar), empty = full + 8 * kSt, s_ready = empty + 8 * kSt, p_ready = s_ready + 16;
-  const uint32_t o_done = p_ready + 16, q_ready = o_done + 16;
+  const uint32_t full = smem_u32(s_bar), empty = full + 8 * kSt, v_fit = empty + 8 * kSt, s_ready = v_fit + 8 * kDepth;
+  const uint32_t p_ready = s_ready + 16, first_done = p_ready + 32, o_done = first_done + 16, q_ready = o_done + 16;
   if (tid == 0) {
     s_fail = 0;
     for (int i = 0; i < kSt; ++i) {
       mbar_init(full + 8 * i, 1);
-      mbar_init(empty + 8 * i, 1);
+      mbar_init(empty + 8 * i, 2);
     }
+    for (int i = 0; i < kDepth; ++i) mbar_init(v_fit + 8 * i, 32);
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_ready + 8 * i, 1);
-      mbar_init(p_ready + 8 * i, 128);
+      mbar_init(p_ready + 16 * i, 128);       // tokens 0 .. 63 of a tile, of half i
+      mbar_init(p_ready + 16 * i + 8, 128);   // tokens 64 .. 127
+      mbar_init(first_done + 8 * i, 1);
       mbar_init(o_done + 8 * i, 1);
+      mbar_init(q_ready + 8 * i, 128);
     }
-    mbar_init(q_ready, 256);
     fence_barrier_init();
   }
   if (warp == 9) tmem_alloc(smem_u32(&s_tmem), 512);
@@ -127,48 +135,104 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
 
   if (warp == 8) {
     paged_load<D, kSt>(a, &k_map, &v_map, cur, hi, smem0, full, empty, s_there, fail);
-  } else if (warp == 9) {
+  } else if (warp == 11) {
+    // -------------------------------------------- V's rows that must not be read
+    bool ok = true;
+    for (; ok && cur.pos < hi; cur.pos += cur.n) {
+      cur.piece(a, hi);
+      for (int i = 0; i < cur.n && ok; ++i, ++n) {
+        const int tok0 = (cur.t0 + i) * kPgTile;
+        const uint32_t s = 2 * n + 1, st = s % kSt;
+        ok = wait_or_fail(full + 8 * st, (s / kSt) & 1, fail);
+        if (!ok) break;
+        const uint32_t there = s_there[n & 15];
+        const bool special = cur.special(a, tok0, there);
+        uint8_t* vt = smem + st * L::kTileBytes;
+        uint32_t odd = 0;
+#pragma unroll 1
+        for (int row = lane; special && row < kPgTile; row += 32) {
+          const bool valid = there >> (row >> a.c.page_shift) & 1 && tok0 + row < cur.rq.len;
+#pragma unroll
+          for (int ch = 0; ch < D / 8; ++ch) {
+            uint4* p = reinterpret_cast<uint4*>(vt + block_off(kPgTile, row, ch));
+            if (valid)
+              odd |= nonfinite8<T>(*p);
+            else
+              *p = make_uint4(0, 0, 0, 0);
+          }
+        }
+        odd = __any_sync(0xffffffffu, odd != 0);
+        uint32_t* flags = s_tok + (n % kDepth) * 128 * (D / 16);
+        for (int row = lane; odd && row < kPgTile; row += 32) {
+          const bool valid = there >> (row >> a.c.page_shift) & 1 && tok0 + row < cur.rq.len;
+          for (int ch = 0; ch < D / 8; ++ch) {
+            const uint32_t f = valid ? take_out8<T>(reinterpret_cast<uint4*>(vt + block_off(kPgTile, row, ch))) : 0u;
+            uint8_t* to = reinterpret_cast<uint8_t*>(flags + row * (D / 16)) + ch;
+            to[0] = static_cast<uint8_t>(f);
+            to[D / 8] = static_cast<uint8_t>(f >> 8);
+          }
+        }
+        if (lane == 0) s_odd[n % kDepth] = odd;
+        fence_async_smem();
+        mbar_arrive(v_fit + 8 * (n % kDepth));
+      }
+    }
+  } else if (warp >= 9) {
     // ------------------------------------------------------------------ MMA
+    const int g = warp - 9;
     if (lane == 0) {
       constexpr uint32_t kIdS = tc_idesc(T::kMma, false, false, 128, 128), kIdO = tc_idesc(T::kMma, false, true, 128, D);
+      const uint32_t t_s = tmem + g * 128, t_o = tmem + 256 + g * 128, qt = smem0 + L::kOffQ + g * L::kTileBytes;
       bool ok = true;
-      uint32_t pieces = 0, done[2] = {0, 0};   // done: tiles of each half whose P has been awaited
-      auto scores = [&](uint32_t m, int g, bool last) {
+      uint32_t pieces = 0, mine = 0;   // of this half; mine: tiles
+      auto scores = [&](uint32_t m) {
         const uint32_t s = 2 * m, st = s % kSt;
-        if (g == 0) ok = ok && wait_or_fail(full + 8 * st, (s / kSt) & 1, fail);
+        ok = ok && wait_or_fail(full + 8 * st, (s / kSt) & 1, fail);
         if (!ok) return;
         tc_fence_after();
-        const uint32_t qt = smem0 + L::kOffQ + g * L::kTileBytes, kt = smem0 + st * L::kTileBytes;
+        const uint32_t kt = smem0 + st * L::kTileBytes;
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          tc_mma_f16(tmem + g * 128, tc_desc(qt + (k >> 2) * (kPgTile * 128) + (k & 3) * 32, 16, 1024, 2),
-                     tc_desc(kt + (k >> 2) * (kPgTile * 128) + (k & 3) * 32, 16, 1024, 2), kIdS, k > 0);
+        for (int j = 0; j < D / 16; ++j)
+          tc_mma_f16(t_s, tc_desc(qt + (j >> 2) * (kPgTile * 128) + (j & 3) * 32, 16, 1024, 2),
+                     tc_desc(kt + (j >> 2) * (kPgTile * 128) + (j & 3) * 32, 16, 1024, 2), kIdS, j > 0);
         tc_commit(s_ready + 8 * g);
-        if (last) tc_commit(empty + 8 * st);
+        tc_commit(empty + 8 * st);
       };
       for (; ok && cur.pos < hi; cur.pos += cur.n) {
         cur.piece(a, hi);
-        const int gs = halves(cur.block);
-        ok = wait_or_fail(q_ready, pieces++ & 1, fail);
-        for (int g = 0; g < gs && ok; ++g) scores(n, g, g + 1 == gs);
+        if (g >= halves(cur.block)) {   // keeps in step with the ring: a wait must not be a round of it ahead
+          for (int i = 0; i < cur.n && ok; ++i, ++n) {
+            const uint32_t s = 2 * n;
+            ok = wait_or_fail(full + 8 * (s % kSt), (s / kSt) & 1, fail);
+            if (ok) mbar_arrive(empty + 8 * (s % kSt));
+            ok = ok && wait_or_fail(v_fit + 8 * (n % kDepth), (n / kDepth) & 1, fail);
+            if (ok) mbar_arrive(empty + 8 * ((s + 1) % kSt));
+          }
+          continue;
+        }
+        ok = wait_or_fail(q_ready + 8 * g, pieces++ & 1, fail);
+        if (ok) scores(n);
         for (int i = 0; i < cur.n && ok; ++i, ++n) {
-          const uint32_t s = 2 * n + 1, st = s % kSt, vt = smem0 + st * L::kTileBytes;
-          for (int g = 0; g < gs && ok; ++g) {
-            if (g == 0) ok = wait_or_fail(full + 8 * st, (s / kSt) & 1, fail);
-            ok = ok && wait_or_fail(p_ready + 8 * g, done[g]++ & 1, fail);
+          const uint32_t st = (2 * n + 1) % kSt, vt = smem0 + st * L::kTileBytes;
+          ok = wait_or_fail(v_fit + 8 * (n % kDepth), (n / kDepth) & 1, fail);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            ok = ok && wait_or_fail(p_ready + 16 * g + 8 * u, mine & 1, fail);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
-            for (int k = 0; k < kPgTile / 16; ++k)   // P's halves lie where those of S did
-              tc_mma_f16_ts(tmem + 256 + g * 128, tmem + g * 128 + (k & 3) * 8 + (k >> 2) * 64,
-                            tc_desc(vt + 2048 * k, kPgTile * 128, 1024, 2), kIdO, i > 0 || k > 0);
-            if (g + 1 == gs) tc_commit(empty + 8 * st);
-            // The next S overwrites this P: products of one CTA run in the order they are issued.
-            if (i + 1 < cur.n)
-              scores(n + 1, g, g + 1 == gs);
-            else
-              tc_commit(o_done + 8 * g);
+            for (int j = 4 * u; j < 4 * u + 4; ++j)   // P's halves lie where those of S did
+              tc_mma_f16_ts(t_o, t_s + (j & 3) * 8 + u * 64, tc_desc(vt + 2048 * j, kPgTile * 128, 1024, 2), kIdO, i > 0 || j > 0);
+            if (u == 0) tc_commit(first_done + 8 * g);
           }
+          if (!ok) break;
+          ++mine;
+          tc_commit(empty + 8 * st);
+          // The next S overwrites this P: products that one thread issues run in order.
+          if (i + 1 < cur.n)
+            scores(n + 1);
+          else
+            tc_commit(o_done + 8 * g);
         }
       }
     }
@@ -179,46 +243,55 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
     const uint32_t t_lane = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t t_s = t_lane + g * 128, t_o = t_lane + 256 + g * 128;
     uint8_t* qt = smem + L::kOffQ + g * L::kTileBytes;
-    uint32_t tiles_done = 0, pieces = 0;   // of this half
+    uint32_t* flags = s_row + (g * 128 + row) * (D / 16);
+    uint32_t mine = 0, pieces = 0;   // tiles and pieces of this half
+    constexpr int kLpr = D / 8, kRpp = 128 / kLpr;   // lanes a row of q or of the output, rows a pass of the half's threads
+    const int ch = row % kLpr, r_0 = row / kLpr;
+    // q's rows of a piece, D / 8 lanes a row: into registers, and to their place.
+    auto q_load = [&](const PagedCursor& c, uint4 (&w)[kLpr]) {
+      const uint8_t* q = a.q + c.b * a.sqb + static_cast<int64_t>(c.h) * a.G * a.sqh + ch * 16;
+      const int first = c.block * kPgRowBlock + g * 128 + r_0;
+#pragma unroll
+      for (int j = 0; j < kLpr; ++j) {
+        const int Rg = first + j * kRpp, node = paged_node(a, Rg);
+        w[j] = make_uint4(0, 0, 0, 0);
+        if (Rg < rows_total && node < c.rq.n) w[j] = *reinterpret_cast<const uint4*>(q + node * a.sqn + (Rg - node * a.G) * a.sqh);
+      }
+    };
+    auto q_store = [&](const uint4 (&w)[kLpr]) {
+      const uint32_t flip = a.coef < 0.f ? 0x80008000u : 0u;   // scores grow with S
+#pragma unroll
+      for (int j = 0; j < kLpr; ++j)
+        *reinterpret_cast<uint4*>(qt + block_off(128, r_0 + j * kRpp, ch)) = make_uint4(w[j].x ^ flip, w[j].y ^ flip, w[j].z ^ flip, w[j].w ^ flip);
+      fence_async_smem();
+      mbar_arrive(q_ready + 8 * g);
+    };
+    const float coef = fabsf(a.coef);
+    if (cur.pos < hi) {
+      cur.piece(a, hi);
+      if (tid == 0) a.first[blockIdx.x] = cur.item(a);
+      if (g < halves(cur.block)) {
+        uint4 w[kLpr];
+        q_load(cur, w);
+        q_store(w);
+      }
+    }
+    bool first = true;
     // A wait that gives up ends no loop here: these warps meet at barriers, so all
     // run on to the end (every later wait then returns at once), without meaning:
     // the rows of every piece that ends after it are NaN.
-    for (; cur.pos < hi; cur.pos += cur.n) {
-      cur.piece(a, hi);
-      if (cur.pos == lo && tid == 0) a.first[blockIdx.x] = cur.item(a);
+    while (cur.pos < hi) {
       const PagedReq rq = cur.rq;
       const int gs = halves(cur.block), soft = 128 * gs;
+      const bool active = g < gs;
       const int row0 = cur.block * kPgRowBlock + g * 128;
-      if (g >= gs) {
-        n += cur.n;
-        named_barrier_sync(4, kRowSoft);
-        continue;
-      }
-      // ---- q, D / 8 lanes a row
-      const uint8_t* q = a.q + cur.b * a.sqb + static_cast<int64_t>(cur.h) * a.G * a.sqh;
-#pragma unroll 4
-      for (int i = row; i < 128 * (D / 8); i += 128) {
-        const int r = i / (D / 8), ch = i % (D / 8), Rg = row0 + r, node = paged_node(a, Rg);
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (Rg < rows_total && node < rq.n) w = *reinterpret_cast<const uint4*>(q + node * a.sqn + (Rg - node * a.G) * a.sqh + ch * 16);
-        if (a.coef < 0.f) {   // scores grow with S
-          w.x ^= 0x80008000u;
-          w.y ^= 0x80008000u;
-          w.z ^= 0x80008000u;
-          w.w ^= 0x80008000u;
-        }
-        *reinterpret_cast<uint4*>(qt + block_off(128, r, ch)) = w;
-      }
-      fence_async_smem();
-      mbar_arrive(q_ready);
-      if (gs == 1) mbar_arrive(q_ready);   // for the other half's thread
       // ---- the thread's row, the request's tree
       const int Rg = row0 + row, at = paged_node(a, Rg);
       const int node = Rg < rows_total && at < rq.n ? at : -1;
       int depth = max(node, 0);
 #pragma unroll
-      for (int j = 0; j < D / 16; ++j) s_row[(g * 128 + row) * (D / 16) + j] = 0;
-      if (a.parents) {
+      for (int j = 0; j < D / 16; ++j) flags[j] = 0;
+      if (a.parents && active) {
         const int32_t* par = a.parents + static_cast<int64_t>(cur.b) * a.N;
         for (int i = tid; i < rq.n; i += soft) s_par[i] = static_cast<int16_t>(tree_up(par, i));
         named_barrier_sync(1, soft);
@@ -231,19 +304,19 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
         depth = s_depth[max(node, 0)];
       }
       const int pos = rq.base + depth;
-      const float slope = kVar && a.slopes && node >= 0 ? a.slopes[cur.h * a.G + Rg - at * a.G] * kLog2e : 0.f;
-      const float coef = fabsf(a.coef);
       const int open = max(pos - a.window + 1, 0);   // the window's first position
-      const int pos0 = rq.base;   // positions relative to it are small enough for fp32
+      const int pos0 = rq.base;                      // positions relative to it are small enough for fp32
+      const float slope = kVar && a.slopes && node >= 0 ? a.slopes[cur.h * a.G + Rg - at * a.G] * kLog2e : 0.f;
 
       float m_run = 0.f, l = 0.f;   // m_run means something once the row has seen a slot
       bool seen = false;
 #pragma unroll 1
-      for (int i = 0; i < cur.n; ++i, ++n, ++tiles_done) {
+      for (int i = 0; i < (active ? cur.n : 0); ++i, ++mine) {
+        const uint32_t tile = n + i;
         const int tok0 = (cur.t0 + i) * kPgTile;
-        wait_or_fail(s_ready + 8 * g, tiles_done & 1, fail);   // and every product before this S is done
+        wait_or_fail(s_ready + 8 * g, mine & 1, fail);   // and every product before this S is done
         tc_fence_after();
-        const uint32_t there = s_there[n & 15];
+        const uint32_t there = s_there[tile & 15];
         const bool special = cur.special(a, tok0, there);
         uint32_t see[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};   // what the row sees of the tile
         if (special) {
@@ -269,46 +342,21 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
             if (!(there >> ((32 * j + 16) >> a.c.page_shift) & 1)) see[j] &= 0x0000ffffu;
             if (node < 0) see[j] = 0;
           }
-          // ---- V's rows that must not be read, the same for every row
-          const uint32_t s = 2 * n + 1, st = s % kSt;
-          wait_or_fail(full + 8 * st, (s / kSt) & 1, fail);
-          uint8_t* vt = smem + st * L::kTileBytes;
-          const bool valid = there >> (row >> a.c.page_shift) & 1 && tok0 + row < rq.len;
-          uint32_t odd = 0;
-#pragma unroll
-          for (int ch = 0; ch < D / 8; ++ch) {
-            if (gs == 2 && ch / (D / 16) != g) continue;   // the thread's pieces of token `row`
-            uint4* p = reinterpret_cast<uint4*>(vt + block_off(kPgTile, row, ch));
-            if (valid)
-              odd |= nonfinite8<T>(*p);
-            else
-              *p = make_uint4(0, 0, 0, 0);
-          }
-          if (named_barrier_or(1, soft, odd != 0)) {   // rare
-            uint32_t* flags = s_tok + (n & 1) * 128 * (D / 16);
-            for (int ch = gs == 2 ? g * (D / 16) : 0; ch < (gs == 2 ? (g + 1) * (D / 16) : D / 8); ++ch) {
-              const uint32_t f = valid ? take_out8<T>(reinterpret_cast<uint4*>(vt + block_off(kPgTile, row, ch))) : 0u;
-              uint8_t* to = reinterpret_cast<uint8_t*>(flags + row * (D / 16)) + ch;
-              to[0] = static_cast<uint8_t>(f);
-              to[D / 8] = static_cast<uint8_t>(f >> 8);
-            }
-            named_barrier_sync(1, soft);
-            note_seen<D>(flags, see[0], see[1], see[2], see[3], s_row + (g * 128 + row) * (D / 16));
-          }
-          fence_async_smem();
           if (kVar && a.slopes && a.parents) {
-            named_barrier_sync(1, soft);   // every row has read the last such tile's positions
             const int m = tok0 + row - rq.base;
-            if (g == 0) s_at[row] = static_cast<float>(m >= 0 && m < rq.n ? rq.base + s_depth[m] - pos0 : tok0 + row - pos0);
-            named_barrier_sync(1, soft);
+            named_barrier_sync(2 + g, 128);   // every row has read the last such tile's positions
+            s_at[g * 128 + row] = static_cast<float>(m >= 0 && m < rq.n ? rq.base + s_depth[m] - pos0 : tok0 + row - pos0);
+            named_barrier_sync(2 + g, 128);
           }
           __syncwarp();
         }
-        // ---- 64 scores, in units of log2
         const float c = kVar ? 1.f : coef;
-        auto scores = [&](uint32_t (&w)[64], int half) {
-          tmem_ld32(t_s + half * 64, w);
-          tmem_ld32(t_s + half * 64 + 32, w + 32);
+#pragma unroll 1
+        for (int u = 0; u < 2; ++u) {
+          // ---- 64 scores, in units of log2
+          uint32_t w[64];
+          tmem_ld32(t_s + u * 64, w);
+          tmem_ld32(t_s + u * 64 + 32, w + 32);
           tmem_ld_wait();
           tmem_use(w);
           if (kVar) {
@@ -326,135 +374,154 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
             if (a.slopes) {
               if (special && a.parents) {
                 const float off = static_cast<float>(pos0 - pos);
+                const float* at_u = s_at + g * 128 + u * 64;
 #pragma unroll
                 for (int j = 0; j < 64; j += 4) {
-                  const float4 at4 = *reinterpret_cast<const float4*>(s_at + half * 64 + j);
+                  const float4 at4 = *reinterpret_cast<const float4*>(at_u + j);
                   w[j] = __float_as_uint(fmaf(slope, at4.x + off, __uint_as_float(w[j])));
                   w[j + 1] = __float_as_uint(fmaf(slope, at4.y + off, __uint_as_float(w[j + 1])));
                   w[j + 2] = __float_as_uint(fmaf(slope, at4.z + off, __uint_as_float(w[j + 2])));
                   w[j + 3] = __float_as_uint(fmaf(slope, at4.w + off, __uint_as_float(w[j + 3])));
                 }
               } else {
-                const float off = static_cast<float>(tok0 + half * 64 - pos);
+                const float off = static_cast<float>(tok0 + u * 64 - pos);
 #pragma unroll
                 for (int j = 0; j < 64; ++j) w[j] = __float_as_uint(fmaf(slope, off + static_cast<float>(j), __uint_as_float(w[j])));
               }
             }
           }
           if (special) {
+            const uint32_t see0 = u ? see[2] : see[0], see1 = u ? see[3] : see[1];
 #pragma unroll
-            for (int j = 0; j < 64; ++j) w[j] = see[half * 2 + (j >> 5)] >> (j & 31) & 1 ? w[j] : 0xff800000u;
+            for (int j = 0; j < 64; ++j) w[j] = (j < 32 ? see0 : see1) >> (j & 31) & 1 ? w[j] : 0xff800000u;
           }
-        };
-        auto largest = [](const uint32_t (&w)[64]) {
+          // ---- weights by the running maximum, their sum; the scores' maximum
+          uint32_t h[32];
+          float2 sum[2];
+          auto weights = [&] {
+            const float2 c2 = make_float2(c, c), m2 = make_float2(-m_run, -m_run);
+            sum[0] = sum[1] = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const float2 x = __ffma2_rn(make_float2(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1])), c2, m2);
+              const float2 p = make_float2(ex2(x.x), ex2(x.y));
+              sum[j & 1] = __fadd2_rn(sum[j & 1], p);
+              h[j] = T::pack2(p.x, p.y);
+            }
+          };
+          weights();
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int j = 0; j < 64; j += 8)
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mx[k] = fmaxf(fmaxf(mx[k], __uint_as_float(w[j + 2 * k])), __uint_as_float(w[j + 2 * k + 1]));
-          return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        };
-        // ---- exponentials, their sum, P over the scores
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        auto weights = [&](const uint32_t (&w)[64], int half) {
-          const float2 c2 = make_float2(c, c), m2 = make_float2(-m_run, -m_run);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            uint32_t h[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const float2 x = __ffma2_rn(make_float2(__uint_as_float(w[32 * j + 2 * k]), __uint_as_float(w[32 * j + 2 * k + 1])), c2, m2);
-              const float2 p = make_float2(ex2(x.x), ex2(x.y));
-              sum[k & 1] = __fadd2_rn(sum[k & 1], p);
-              h[k] = T::pack2(p.x, p.y);
-            }
-            tmem_st16(t_s + half * 64 + j * 16, h);
-          }
-        };
-        uint32_t w[64];
-        scores(w, 0);
-        float most = largest(w);
-        scores(w, 1);
-        most = fmaxf(most, largest(w));
-        const float top = most == -INFINITY ? -INFINITY : fmaf(most, c, -m_run);
-        const bool raise = seen ? top > kPgSlack + kPgLift<T> : top > -INFINITY;
-        if (__any_sync(0xffffffffu, raise)) {
-          const float f = raise && seen ? ex2(kPgLift<T> - top) : 1.f;
-          if (raise) m_run += top - kPgLift<T>;
-          seen = seen || raise;
-          l *= f;
-          if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+            for (int e = 0; e < 4; ++e)
+              mx[e] = fmaxf(fmaxf(mx[e], __uint_as_float(w[j + 2 * e])), __uint_as_float(w[j + 2 * e + 1]));
+          const float most = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          const float top = most == -INFINITY ? -INFINITY : fmaf(most, c, -m_run);
+          const bool raise = seen ? top > kPgSlack + kPgLift<T> : top > -INFINITY;
+          if (__any_sync(0xffffffffu, raise)) {
+            const float f = raise && seen ? ex2(kPgLift<T> - top) : 1.f;
+            if (raise) m_run += top - kPgLift<T>;
+            seen = seen || raise;
+            l *= f;
+            if (i + u > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+              if (u == 1) {   // the first tokens' products are the last that touch O
+                wait_or_fail(first_done + 8 * g, mine & 1, fail);
+                tc_fence_after();
+              }
 #pragma unroll 1
-            for (int j = 0; j < D / 16; ++j) {
-              uint32_t o[16];
-              tmem_ld16(t_o + j * 16, o);
-              tmem_ld_wait();
-              tmem_use(o);
+              for (int j = 0; j < D / 16; ++j) {
+                uint32_t o[16];
+                tmem_ld16(t_o + j * 16, o);
+                tmem_ld_wait();
+                tmem_use(o);
 #pragma unroll
-              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-              tmem_st16(t_o + j * 16, o);
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st16(t_o + j * 16, o);
+              }
             }
+            weights();
+          }
+          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          tmem_st16(t_s + u * 64, h);
+          tmem_st16(t_s + u * 64 + 16, h + 16);
+          if (special && u == 1) {   // what was taken out of V, before the tile is given up
+            wait_or_fail(v_fit + 8 * (tile % kDepth), (tile / kDepth) & 1, fail);
+            if (const_cast<volatile uint32_t*>(s_odd)[tile % kDepth])
+              note_seen<D>(s_tok + (tile % kDepth) * 128 * (D / 16), see[0], see[1], see[2], see[3], flags);
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(p_ready + 16 * g + 8 * u);
+        }
+      }
+      n += cur.n;
+      // ---- the piece's rows, under whose last products the next piece's are loaded
+      PagedCursor next = cur;
+      next.pos += cur.n;
+      const bool more = next.pos < hi;
+      uint4 w[kLpr];
+      if (more) {
+        next.piece(a, hi);
+        if (g < halves(next.block)) q_load(next, w);
+      }
+      if (active) {
+        wait_or_fail(o_done + 8 * g, pieces++ & 1, fail);
+        tc_fence_after();
+        if (*fail) l = __int_as_float(0x7fc00000);
+        if (node < 0) l = 0.f;
+        const float f = l == 0.f ? 0.f : cur.whole ? 1.f / l : 1.f;
+        float* part = a.part + static_cast<int64_t>(2 * blockIdx.x + (first ? 0 : 1)) * kPgRowBlock * (D + 2);
+#pragma unroll 1
+        for (int j = 0; j < D / 32; ++j) {
+          uint32_t o[32];
+          tmem_ld32(t_o + j * 32, o);
+          tmem_ld_wait();
+          tmem_use(o);
+          const uint32_t up = flags[j], down = flags[D / 32 + j];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(f == 0.f ? 0.f : __uint_as_float(o[e]) * f);
+          if (__any_sync(0xffffffffu, (up | down) != 0 && f != 0.f)) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (f != 0.f) o[e] = __float_as_uint(put_back(__uint_as_float(o[e]), up >> e & 1, down >> e & 1));
+          }
+          if (cur.whole) {   // the rows of q are done with: their place takes the output's
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t y[4];
+#pragma unroll
+              for (int x = 0; x < 4; ++x) y[x] = T::pack2(__uint_as_float(o[8 * e + 2 * x]), __uint_as_float(o[8 * e + 2 * x + 1]));
+              *reinterpret_cast<uint4*>(qt + block_off(128, row, j * 4 + e)) = make_uint4(y[0], y[1], y[2], y[3]);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) part[(j * 32 + e) * kPgRowBlock + g * 128 + row] = __uint_as_float(o[e]);
           }
         }
-        weights(w, 1);
-        scores(w, 0);
-        weights(w, 0);
-        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-        tmem_st_wait();
+        if (!cur.whole)
+          *reinterpret_cast<float2*>(part + kPgRowBlock * D + (g * 128 + row) * 2) = make_float2(l == 0.f ? -INFINITY : m_run, l);
+        else if (a.lse && Rg < rows_total)
+          a.lse[(static_cast<int64_t>(cur.b) * a.N + at) * a.Hq + cur.h * a.G + (Rg - at * a.G)] = l == 0.f ? -INFINITY : (m_run + log2f(l)) * kLn2;
         tc_fence_before();
-        mbar_arrive(p_ready + 8 * g);
-      }
-      // ---- the piece's rows
-      wait_or_fail(o_done + 8 * g, pieces++ & 1, fail);
-      tc_fence_after();
-      if (*fail) l = __int_as_float(0x7fc00000);
-      if (node < 0) l = 0.f;
-      const float f = l == 0.f ? 0.f : cur.whole ? 1.f / l : 1.f;
-      float* part = a.part + static_cast<int64_t>(2 * blockIdx.x + (cur.pos == lo ? 0 : 1)) * kPgRowBlock * (D + 2);
-#pragma unroll 1
-      for (int j = 0; j < D / 32; ++j) {
-        uint32_t o[32];
-        tmem_ld32(t_o + j * 32, o);
-        tmem_ld_wait();
-        tmem_use(o);
-        const uint32_t up = s_row[(g * 128 + row) * (D / 16) + j], down = s_row[(g * 128 + row) * (D / 16) + D / 32 + j];
+        if (cur.whole) {
+          named_barrier_sync(2 + g, 128);
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          float y = f == 0.f ? 0.f : __uint_as_float(o[k]) * f;
-          if (up | down) y = f == 0.f ? 0.f : put_back(y, up >> k & 1, down >> k & 1);
-          o[k] = __float_as_uint(y);
-        }
-        if (cur.whole) {   // the rows of q are done with: their place takes the output's
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t y[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = T::pack2(__uint_as_float(o[8 * k + 2 * e]), __uint_as_float(o[8 * k + 2 * e + 1]));
-            *reinterpret_cast<uint4*>(qt + block_off(128, row, j * 4 + k)) = make_uint4(y[0], y[1], y[2], y[3]);
+          for (int j = 0; j < kLpr; ++j) {
+            const int r = r_0 + j * kRpp, RR = row0 + r;
+            if (RR < rows_total) {
+              const int nn = paged_node(a, RR);
+              const int64_t to = (static_cast<int64_t>(cur.b) * a.N + nn) * a.Hq + cur.h * a.G + (RR - nn * a.G);
+              *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + to * D * 2 + ch * 16) = *reinterpret_cast<const uint4*>(qt + block_off(128, r, ch));
+            }
           }
-        } else {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) part[(j * 32 + k) * kPgRowBlock + g * 128 + row] = __uint_as_float(o[k]);
+          named_barrier_sync(2 + g, 128);   // before q's rows come
         }
       }
-      if (!cur.whole)
-        *reinterpret_cast<float2*>(part + kPgRowBlock * D + (g * 128 + row) * 2) = make_float2(l == 0.f ? -INFINITY : m_run, l);
-      else if (a.lse && Rg < rows_total)
-        a.lse[(static_cast<int64_t>(cur.b) * a.N + at) * a.Hq + cur.h * a.G + (Rg - at * a.G)] = l == 0.f ? -INFINITY : (m_run + log2f(l)) * kLn2;
-      tc_fence_before();
-      named_barrier_sync(2 + g, 128);
-      if (cur.whole) {
-#pragma unroll 4
-        for (int i = row; i < 128 * (D / 8); i += 128) {
-          const int r = i / (D / 8), ch = i % (D / 8), RR = row0 + r;
-          if (RR >= rows_total) break;
-          const int nn = paged_node(a, RR);
-          const int64_t to = (static_cast<int64_t>(cur.b) * a.N + nn) * a.Hq + cur.h * a.G + (RR - nn * a.G);
-          *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + to * D * 2 + ch * 16) = *reinterpret_cast<const uint4*>(qt + block_off(128, r, ch));
-        }
-      }
-      named_barrier_sync(4, kRowSoft);   // the tree and the rows' places are free for the next piece
+      if (more && g < halves(next.block)) q_store(w);
+      first = false;
+      cur = next;
+      if (a.parents) named_barrier_sync(4, kRowSoft);   // the tree's place is free for the next piece
     }
   }
   __syncthreads();
