@@ -13,11 +13,12 @@
 //
 // A thread has one row, so maximum, exponentials and sum are its own. It takes
 // 64 tokens at a time: P of the first 64 is multiplied while those of the others
-// are worked out. The exponentials do not wait for the maximum: they go by the
-// running maximum, and are done again in the rare case that a score exceeds it
-// by more than 2^8 (or is the row's first). The warp then rescales its rows of O.
-// P is rounded to 16 bits (half a step of the type: 2^-8 of a bf16 weight, 2^-11
-// of f16's), its sum is not.
+// are worked out. The exponentials go by a running maximum, and no maximum of the
+// new scores is taken: their sum, which is needed anyway, shows whether one is
+// too large. In that rare case, and until the row has seen a slot, the maximum is
+// taken, the warp's rows of O are rescaled and the weights done again. P is rounded to 16
+// bits (half a step of the type: 2^-8 of a bf16 weight, 2^-11 of f16's), its sum
+// is not.
 //
 // A tile that some row does not see whole is masked in registers by 128 bits that
 // the thread works out from its row's position and path; what must not be read of
@@ -26,7 +27,8 @@
 // The rows of the next piece's q are loaded while the last products run, and
 // take their place once the output has left it.
 //
-// Warps 0-3 and 4-7: softmax. 8: TMA. 9 and 10: MMA of the halves. 11: V.
+// Warps 0-3 and 4-7: softmax of the halves. 8: TMA. 9: MMA, which takes the
+// halves by turns, so that they fall out of step. 10: V. 11 makes up the last four.
 #pragma once
 
 #include "attn_paged_cols.cuh"
@@ -35,6 +37,7 @@
 namespace sv {
 
 constexpr int kPgRowThreads = 384;
+constexpr int kPgRowSoft = 256;       // softmax threads
 constexpr int kPgRowBlock = 256;
 
 template <int D>
@@ -63,24 +66,40 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
 // The bits below bit x of a word.
 __device__ __forceinline__ uint32_t below(int x) { return x <= 0 ? 0u : x >= 32 ? 0xffffffffu : (1u << x) - 1u; }
 
+// What 64 weights of a row may add up to by its running maximum, before that is raised: none is above it, and f16 holds it.
+constexpr float kPgMost = 32768.f;
+
 // What was taken out of the tokens of a tile that a row sees, into the row's flags.
 template <int D>
-__device__ __noinline__ void note_seen(const uint32_t* flags, uint32_t s0, uint32_t s1, uint32_t s2, uint32_t s3, uint32_t* to) {
+__device__ __noinline__ void note_seen(const uint32_t* from, uint32_t s0, uint32_t s1, uint32_t s2, uint32_t s3, uint32_t* to) {
   const uint32_t see[4] = {s0, s1, s2, s3};
   for (int t = 0; t < kPgTile; ++t)
     if (see[t >> 5] >> (t & 31) & 1)
-      for (int w = 0; w < D / 16; ++w) to[w] |= flags[t * (D / 16) + w];
+      for (int w = 0; w < D / 16; ++w) to[w] |= from[t * (D / 16) + w];
+}
+
+// A warp's cursor in shared memory, moved on to its next piece: the softmax warps have no registers for theirs.
+__device__ __noinline__ void next_piece(const PagedAttnArgs& a, const PagedCursor* from, PagedCursor* to, int32_t hi) {
+  if ((threadIdx.x & 31) == 0) {
+    PagedCursor c = *from;
+    c.pos += c.n;
+    if (c.pos < hi) c.piece(a, hi);
+    *to = c;
+  }
+  __syncwarp();
 }
 
 // kVar: scores are capped or biased.
 template <typename T, int D, bool kVar>
 __global__ void __launch_bounds__(kPgRowThreads, 1)
-    attn_paged_rows_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, const PagedAttnArgs a) {
+    attn_paged_rows_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                           const __grid_constant__ PagedAttnArgs a) {
   using L = PgRowLayout<D>;
   constexpr int kSt = L::kStages, kDepth = L::kDepth;
   extern __shared__ uint8_t raw[];
   __shared__ AttnLine s_line;
   __shared__ int32_t s_warp[kPgRowThreads / 32];
+  __shared__ PagedCursor s_cur[kPgRowSoft / 32][2];
   __shared__ __align__(8) uint64_t s_bar[2 * kSt + kDepth + 12];
   __shared__ uint32_t s_tmem, s_fail, s_there[16], s_odd[kDepth];   // s_odd: whether values were taken out of a tile's V
   const uint32_t smem0 = (smem_u32(raw) + 1023u) & ~1023u;
@@ -98,7 +117,7 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
     s_fail = 0;
     for (int i = 0; i < kSt; ++i) {
       mbar_init(full + 8 * i, 1);
-      mbar_init(empty + 8 * i, 2);
+      mbar_init(empty + 8 * i, 1);
     }
     for (int i = 0; i < kDepth; ++i) mbar_init(v_fit + 8 * i, 32);
     for (int i = 0; i < 2; ++i) {
@@ -135,7 +154,7 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
 
   if (warp == 8) {
     paged_load<D, kSt>(a, &k_map, &v_map, cur, hi, smem0, full, empty, s_there, fail);
-  } else if (warp == 11) {
+  } else if (warp == 10) {
     // -------------------------------------------- V's rows that must not be read
     bool ok = true;
     for (; ok && cur.pos < hi; cur.pos += cur.n) {
@@ -177,111 +196,113 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
         mbar_arrive(v_fit + 8 * (n % kDepth));
       }
     }
-  } else if (warp >= 9) {
+  } else if (warp == 9) {
     // ------------------------------------------------------------------ MMA
-    const int g = warp - 9;
     if (lane == 0) {
       constexpr uint32_t kIdS = tc_idesc(T::kMma, false, false, 128, 128), kIdO = tc_idesc(T::kMma, false, true, 128, D);
-      const uint32_t t_s = tmem + g * 128, t_o = tmem + 256 + g * 128, qt = smem0 + L::kOffQ + g * L::kTileBytes;
       bool ok = true;
-      uint32_t pieces = 0, mine = 0;   // of this half; mine: tiles
-      auto scores = [&](uint32_t m) {
-        const uint32_t s = 2 * m, st = s % kSt;
-        ok = ok && wait_or_fail(full + 8 * st, (s / kSt) & 1, fail);
-        if (!ok) return;
-        tc_fence_after();
-        const uint32_t kt = smem0 + st * L::kTileBytes;
+      uint32_t pieces[2] = {0, 0}, mine[2] = {0, 0};   // by half; mine: tiles
+      auto scores = [&](uint32_t m, int g, bool last) {
+        const uint32_t st = 2 * m % kSt;
+        const uint32_t qt = smem0 + L::kOffQ + g * L::kTileBytes, kt = smem0 + st * L::kTileBytes;
 #pragma unroll
         for (int j = 0; j < D / 16; ++j)
-          tc_mma_f16(t_s, tc_desc(qt + (j >> 2) * (kPgTile * 128) + (j & 3) * 32, 16, 1024, 2),
+          tc_mma_f16(tmem + g * 128, tc_desc(qt + (j >> 2) * (kPgTile * 128) + (j & 3) * 32, 16, 1024, 2),
                      tc_desc(kt + (j >> 2) * (kPgTile * 128) + (j & 3) * 32, 16, 1024, 2), kIdS, j > 0);
         tc_commit(s_ready + 8 * g);
-        tc_commit(empty + 8 * st);
+        if (last) tc_commit(empty + 8 * st);
       };
+      auto k_there = [&](uint32_t m) { ok = ok && wait_or_fail(full + 8 * (2 * m % kSt), (2 * m / kSt) & 1, fail); };
       for (; ok && cur.pos < hi; cur.pos += cur.n) {
         cur.piece(a, hi);
-        if (g >= halves(cur.block)) {   // keeps in step with the ring: a wait must not be a round of it ahead
-          for (int i = 0; i < cur.n && ok; ++i, ++n) {
-            const uint32_t s = 2 * n;
-            ok = wait_or_fail(full + 8 * (s % kSt), (s / kSt) & 1, fail);
-            if (ok) mbar_arrive(empty + 8 * (s % kSt));
-            ok = ok && wait_or_fail(v_fit + 8 * (n % kDepth), (n / kDepth) & 1, fail);
-            if (ok) mbar_arrive(empty + 8 * ((s + 1) % kSt));
-          }
-          continue;
+        const int gs = halves(cur.block);
+        k_there(n);
+        for (int g = 0; g < gs && ok; ++g) {
+          ok = wait_or_fail(q_ready + 8 * g, pieces[g]++ & 1, fail);
+          if (!ok) break;
+          tc_fence_after();
+          scores(n, g, g + 1 == gs);
         }
-        ok = wait_or_fail(q_ready + 8 * g, pieces++ & 1, fail);
-        if (ok) scores(n);
         for (int i = 0; i < cur.n && ok; ++i, ++n) {
           const uint32_t st = (2 * n + 1) % kSt, vt = smem0 + st * L::kTileBytes;
+          const bool more = i + 1 < cur.n;
           ok = wait_or_fail(v_fit + 8 * (n % kDepth), (n / kDepth) & 1, fail);
+          if (more) k_there(n + 1);
+          for (int g = 0; g < gs && ok; ++g) {
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            ok = ok && wait_or_fail(p_ready + 16 * g + 8 * u, mine & 1, fail);
+            for (int u = 0; u < 2; ++u) {
+              ok = ok && wait_or_fail(p_ready + 16 * g + 8 * u, mine[g] & 1, fail);
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll
+              for (int j = 4 * u; j < 4 * u + 4; ++j)   // P's halves lie where those of S did
+                tc_mma_f16_ts(tmem + 256 + g * 128, tmem + g * 128 + (j & 3) * 8 + u * 64, tc_desc(vt + 2048 * j, kPgTile * 128, 1024, 2),
+                              kIdO, i > 0 || j > 0);
+              if (u == 0) tc_commit(first_done + 8 * g);
+            }
             if (!ok) break;
-            tc_fence_after();
-#pragma unroll
-            for (int j = 4 * u; j < 4 * u + 4; ++j)   // P's halves lie where those of S did
-              tc_mma_f16_ts(t_o, t_s + (j & 3) * 8 + u * 64, tc_desc(vt + 2048 * j, kPgTile * 128, 1024, 2), kIdO, i > 0 || j > 0);
-            if (u == 0) tc_commit(first_done + 8 * g);
+            ++mine[g];
+            // The next S overwrites this P: products that one thread issues run in order.
+            if (more)
+              scores(n + 1, g, g + 1 == gs);
+            else
+              tc_commit(o_done + 8 * g);
+            if (g + 1 == gs) tc_commit(empty + 8 * st);
           }
-          if (!ok) break;
-          ++mine;
-          tc_commit(empty + 8 * st);
-          // The next S overwrites this P: products that one thread issues run in order.
-          if (i + 1 < cur.n)
-            scores(n + 1);
-          else
-            tc_commit(o_done + 8 * g);
         }
       }
     }
     __syncwarp();
-  } else {
+  } else if (warp < 8) {
     // -------------------------------------------------------------- softmax
     const int g = warp >> 2, row = tid & 127;   // the thread's half, its row of it
+    const int bar = 2 + g;                       // of the half's threads
     const uint32_t t_lane = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t t_s = t_lane + g * 128, t_o = t_lane + 256 + g * 128;
     uint8_t* qt = smem + L::kOffQ + g * L::kTileBytes;
     uint32_t* flags = s_row + (g * 128 + row) * (D / 16);
     uint32_t mine = 0, pieces = 0;   // tiles and pieces of this half
-    constexpr int kLpr = D / 8, kRpp = 128 / kLpr;   // lanes a row of q or of the output, rows a pass of the half's threads
+    constexpr int kLpr = D / 8, kRpp = 128 / kLpr, kPasses = kLpr;   // lanes a row of q or of the output, rows a pass, passes
     const int ch = row % kLpr, r_0 = row / kLpr;
     // q's rows of a piece, D / 8 lanes a row: into registers, and to their place.
-    auto q_load = [&](const PagedCursor& c, uint4 (&w)[kLpr]) {
+    auto q_load = [&](const PagedCursor& c, uint4 (&w)[kPasses]) {
       const uint8_t* q = a.q + c.b * a.sqb + static_cast<int64_t>(c.h) * a.G * a.sqh + ch * 16;
       const int first = c.block * kPgRowBlock + g * 128 + r_0;
 #pragma unroll
-      for (int j = 0; j < kLpr; ++j) {
+      for (int j = 0; j < kPasses; ++j) {
         const int Rg = first + j * kRpp, node = paged_node(a, Rg);
         w[j] = make_uint4(0, 0, 0, 0);
         if (Rg < rows_total && node < c.rq.n) w[j] = *reinterpret_cast<const uint4*>(q + node * a.sqn + (Rg - node * a.G) * a.sqh);
       }
     };
-    auto q_store = [&](const uint4 (&w)[kLpr]) {
+    auto q_store = [&](const uint4 (&w)[kPasses]) {
       const uint32_t flip = a.coef < 0.f ? 0x80008000u : 0u;   // scores grow with S
 #pragma unroll
-      for (int j = 0; j < kLpr; ++j)
+      for (int j = 0; j < kPasses; ++j)
         *reinterpret_cast<uint4*>(qt + block_off(128, r_0 + j * kRpp, ch)) = make_uint4(w[j].x ^ flip, w[j].y ^ flip, w[j].z ^ flip, w[j].w ^ flip);
       fence_async_smem();
       mbar_arrive(q_ready + 8 * g);
     };
     const float coef = fabsf(a.coef);
-    if (cur.pos < hi) {
-      cur.piece(a, hi);
-      if (tid == 0) a.first[blockIdx.x] = cur.item(a);
-      if (g < halves(cur.block)) {
-        uint4 w[kLpr];
-        q_load(cur, w);
+    PagedCursor* place = s_cur[warp];
+    if (lane == 0) place[1] = cur;
+    __syncwarp();
+    next_piece(a, place + 1, place, hi);
+    if (place->pos < hi) {
+      if (tid == 0) a.first[blockIdx.x] = place->item(a);
+      if (g < halves(place->block)) {
+        uint4 w[kPasses];
+        q_load(*place, w);
         q_store(w);
       }
     }
-    bool first = true;
+    uint32_t count = 0;   // pieces
     // A wait that gives up ends no loop here: these warps meet at barriers, so all
     // run on to the end (every later wait then returns at once), without meaning:
     // the rows of every piece that ends after it are NaN.
-    while (cur.pos < hi) {
-      const PagedReq rq = cur.rq;
+    for (; place[count & 1].pos < hi; ++count) {
+      const PagedCursor& cur = place[count & 1];
+      const PagedReq& rq = cur.rq;
       const int gs = halves(cur.block), soft = 128 * gs;
       const bool active = g < gs;
       const int row0 = cur.block * kPgRowBlock + g * 128;
@@ -305,123 +326,125 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
       }
       const int pos = rq.base + depth;
       const int open = max(pos - a.window + 1, 0);   // the window's first position
-      const int pos0 = rq.base;                      // positions relative to it are small enough for fp32
       const float slope = kVar && a.slopes && node >= 0 ? a.slopes[cur.h * a.G + Rg - at * a.G] * kLog2e : 0.f;
 
+      const int tiles = active ? cur.n : 0, t0 = cur.t0;
       float m_run = 0.f, l = 0.f;   // m_run means something once the row has seen a slot
-      bool seen = false;
+      bool seen = node < 0;           // (what no row needs may be anything)
 #pragma unroll 1
-      for (int i = 0; i < (active ? cur.n : 0); ++i, ++mine) {
+      for (int i = 0; i < tiles; ++i, ++mine) {
         const uint32_t tile = n + i;
-        const int tok0 = (cur.t0 + i) * kPgTile;
+        const int tok0 = (t0 + i) * kPgTile;
         wait_or_fail(s_ready + 8 * g, mine & 1, fail);   // and every product before this S is done
         tc_fence_after();
         const uint32_t there = s_there[tile & 15];
         const bool special = cur.special(a, tok0, there);
         uint32_t see[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};   // what the row sees of the tile
         if (special) {
+          uint32_t path[4] = {0, 0, 0, 0};   // tokens on the row's way up
           if (a.parents) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) see[j] = below(rq.base - tok0 - 32 * j);
             int far = 0;
             for (int m = node; m >= 0 && far < a.window; m = s_par[m], ++far) {
               const int c = rq.base + m - tok0;
               if (c < 0) break;   // parents come before
 #pragma unroll
               for (int j = 0; j < 4; ++j)
-                if (c >> 5 == j) see[j] |= 1u << (c & 31);
+                if (c >> 5 == j) path[j] |= 1u << (c & 31);
             }
           }
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int c = tok0 + 32 * j;
-            if (!a.parents) see[j] = below(rq.base + node + 1 - c);
-            const uint32_t prefix = a.parents ? below(rq.base - c) : 0xffffffffu;   // slots whose positions are their places
-            see[j] &= below(rq.len - c) & ~(prefix & below(open - c));
+            see[j] = a.parents ? (below(rq.base - c) & ~below(open - c)) | path[j] : below(rq.base + node + 1 - c) & ~below(open - c);
+            see[j] &= below(rq.len - c);
             if (!(there >> (32 * j >> a.c.page_shift) & 1)) see[j] &= 0xffff0000u;
             if (!(there >> ((32 * j + 16) >> a.c.page_shift) & 1)) see[j] &= 0x0000ffffu;
             if (node < 0) see[j] = 0;
           }
-          if (kVar && a.slopes && a.parents) {
+          if (kVar && a.slopes && a.parents) {   // positions of the tile's tokens, relative to base: small enough for fp32
             const int m = tok0 + row - rq.base;
-            named_barrier_sync(2 + g, 128);   // every row has read the last such tile's positions
-            s_at[g * 128 + row] = static_cast<float>(m >= 0 && m < rq.n ? rq.base + s_depth[m] - pos0 : tok0 + row - pos0);
-            named_barrier_sync(2 + g, 128);
+            named_barrier_sync(bar, 128);   // every row has read the last such tile's
+            s_at[g * 128 + row] = static_cast<float>(m >= 0 && m < rq.n ? s_depth[m] : m);
+            named_barrier_sync(bar, 128);
           }
           __syncwarp();
         }
         const float c = kVar ? 1.f : coef;
 #pragma unroll 1
         for (int u = 0; u < 2; ++u) {
-          // ---- 64 scores, in units of log2
-          uint32_t w[64];
-          tmem_ld32(t_s + u * 64, w);
-          tmem_ld32(t_s + u * 64 + 32, w + 32);
-          tmem_ld_wait();
-          tmem_use(w);
-          if (kVar) {
-            if (a.cap != 0.f) {
+          const uint32_t see0 = u ? see[2] : see[0], see1 = u ? see[3] : see[1];
+          // N scores from token `at_t` of the tile on, in units of log2 but for the factor c; -inf where the row does not see.
+          auto scores = [&]<int kN>(uint32_t (&x)[kN], int at_t) {
 #pragma unroll
-              for (int j = 0; j < 64; ++j) {
-                float r;
-                asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(__uint_as_float(w[j]) * coef)));
-                w[j] = __float_as_uint(fmaf(-2.f * a.cap, r, a.cap));
-              }
-            } else {
+            for (int j = 0; j < kN; j += 16) tmem_ld16(t_s + at_t + j, x + j);
+            tmem_ld_wait();
+            tmem_use(x);
+            if (kVar) {
+              if (a.cap != 0.f) {
 #pragma unroll
-              for (int j = 0; j < 64; ++j) w[j] = __float_as_uint(__uint_as_float(w[j]) * coef);
-            }
-            if (a.slopes) {
-              if (special && a.parents) {
-                const float off = static_cast<float>(pos0 - pos);
-                const float* at_u = s_at + g * 128 + u * 64;
-#pragma unroll
-                for (int j = 0; j < 64; j += 4) {
-                  const float4 at4 = *reinterpret_cast<const float4*>(at_u + j);
-                  w[j] = __float_as_uint(fmaf(slope, at4.x + off, __uint_as_float(w[j])));
-                  w[j + 1] = __float_as_uint(fmaf(slope, at4.y + off, __uint_as_float(w[j + 1])));
-                  w[j + 2] = __float_as_uint(fmaf(slope, at4.z + off, __uint_as_float(w[j + 2])));
-                  w[j + 3] = __float_as_uint(fmaf(slope, at4.w + off, __uint_as_float(w[j + 3])));
+                for (int j = 0; j < kN; ++j) {
+                  float r;
+                  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(__uint_as_float(x[j]) * coef)));
+                  x[j] = __float_as_uint(fmaf(-2.f * a.cap, r, a.cap));
                 }
               } else {
-                const float off = static_cast<float>(tok0 + u * 64 - pos);
 #pragma unroll
-                for (int j = 0; j < 64; ++j) w[j] = __float_as_uint(fmaf(slope, off + static_cast<float>(j), __uint_as_float(w[j])));
+                for (int j = 0; j < kN; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * coef);
+              }
+              if (a.slopes) {
+                if (special && a.parents) {
+                  const float off = static_cast<float>(-depth);
+#pragma unroll
+                  for (int j = 0; j < kN; ++j)
+                    x[j] = __float_as_uint(fmaf(slope, s_at[g * 128 + at_t + j] + off, __uint_as_float(x[j])));
+                } else {
+                  const float off = static_cast<float>(tok0 + at_t - pos);
+#pragma unroll
+                  for (int j = 0; j < kN; ++j) x[j] = __float_as_uint(fmaf(slope, off + static_cast<float>(j), __uint_as_float(x[j])));
+                }
               }
             }
-          }
-          if (special) {
-            const uint32_t see0 = u ? see[2] : see[0], see1 = u ? see[3] : see[1];
+            if (special) {
+              const uint64_t on = (static_cast<uint64_t>(see1) << 32 | see0) >> (at_t & 63);
 #pragma unroll
-            for (int j = 0; j < 64; ++j) w[j] = (j < 32 ? see0 : see1) >> (j & 31) & 1 ? w[j] : 0xff800000u;
-          }
-          // ---- weights by the running maximum, their sum; the scores' maximum
-          uint32_t h[32];
-          float2 sum[2];
-          auto weights = [&] {
-            const float2 c2 = make_float2(c, c), m2 = make_float2(-m_run, -m_run);
-            sum[0] = sum[1] = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const float2 x = __ffma2_rn(make_float2(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1])), c2, m2);
-              const float2 p = make_float2(ex2(x.x), ex2(x.y));
-              sum[j & 1] = __fadd2_rn(sum[j & 1], p);
-              h[j] = T::pack2(p.x, p.y);
+              for (int j = 0; j < kN; ++j) x[j] = on >> j & 1 ? x[j] : 0xff800000u;
             }
           };
-          weights();
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          uint32_t h[32];
+          float total;
+          for (;;) {
+            // ---- weights by the running maximum, their sum
+            uint32_t w[64];
+            scores(w, u * 64);
+            const float2 c2 = make_float2(c, c), m2 = make_float2(-m_run, -m_run);
+            float2 sum[4];
 #pragma unroll
-          for (int j = 0; j < 64; j += 8)
+            for (int j = 0; j < 4; ++j) sum[j] = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              mx[e] = fmaxf(fmaxf(mx[e], __uint_as_float(w[j + 2 * e])), __uint_as_float(w[j + 2 * e + 1]));
-          const float most = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          const float top = most == -INFINITY ? -INFINITY : fmaf(most, c, -m_run);
-          const bool raise = seen ? top > kPgSlack + kPgLift<T> : top > -INFINITY;
-          if (__any_sync(0xffffffffu, raise)) {
+            for (int j = 0; j < 32; ++j) {
+              const float2 y = __ffma2_rn(make_float2(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1])), c2, m2);
+              const float2 p = make_float2(ex2(y.x), ex2(y.y));
+              sum[j & 3] = __fadd2_rn(sum[j & 3], p);
+              h[j] = T::pack2(p.x, p.y);
+            }
+            sum[0] = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
+            total = sum[0].x + sum[0].y;
+            // The sum bounds each weight: no maximum is needed to see that none is too large.
+            if (!__any_sync(0xffffffffu, !seen || total > kPgMost)) break;
+            // ---- rare: the scores' maximum, and the row by it
+            float most = -INFINITY;
+#pragma unroll 1
+            for (int j = 0; j < 64; j += 16) {
+              uint32_t x[16];
+              scores(x, u * 64 + j);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) most = fmaxf(most, __uint_as_float(x[e]));
+            }
+            const float top = most == -INFINITY ? -INFINITY : fmaf(most, c, -m_run);
+            const bool raise = seen ? total > kPgMost && top > kPgLift<T> : top > -INFINITY;
             const float f = raise && seen ? ex2(kPgLift<T> - top) : 1.f;
             if (raise) m_run += top - kPgLift<T>;
+            const bool settled = __all_sync(0xffffffffu, !raise);   // nothing has changed: what is still unseen has no weight, NaN stays
             seen = seen || raise;
             l *= f;
             if (i + u > 0 && __any_sync(0xffffffffu, f != 1.f)) {
@@ -440,9 +463,9 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
                 tmem_st16(t_o + j * 16, o);
               }
             }
-            weights();
+            if (settled) break;
           }
-          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          l += total;
           tmem_st16(t_s + u * 64, h);
           tmem_st16(t_s + u * 64 + 16, h + 16);
           if (special && u == 1) {   // what was taken out of V, before the tile is given up
@@ -457,28 +480,26 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
       }
       n += cur.n;
       // ---- the piece's rows, under whose last products the next piece's are loaded
-      PagedCursor next = cur;
-      next.pos += cur.n;
+      const PagedCursor& next = place[~count & 1];
+      next_piece(a, &cur, place + (~count & 1), hi);
       const bool more = next.pos < hi;
-      uint4 w[kLpr];
-      if (more) {
-        next.piece(a, hi);
-        if (g < halves(next.block)) q_load(next, w);
-      }
+      uint4 w[kPasses];
+      if (more && g < halves(next.block)) q_load(next, w);
       if (active) {
         wait_or_fail(o_done + 8 * g, pieces++ & 1, fail);
         tc_fence_after();
         if (*fail) l = __int_as_float(0x7fc00000);
         if (node < 0) l = 0.f;
         const float f = l == 0.f ? 0.f : cur.whole ? 1.f / l : 1.f;
-        float* part = a.part + static_cast<int64_t>(2 * blockIdx.x + (first ? 0 : 1)) * kPgRowBlock * (D + 2);
+        float* part = a.part + static_cast<int64_t>(2 * blockIdx.x + (count == 0 ? 0 : 1)) * kPgRowBlock * (D + 2);
 #pragma unroll 1
         for (int j = 0; j < D / 32; ++j) {
+          const int d0 = j * 32;
           uint32_t o[32];
           tmem_ld32(t_o + j * 32, o);
           tmem_ld_wait();
           tmem_use(o);
-          const uint32_t up = flags[j], down = flags[D / 32 + j];
+          const uint32_t up = flags[d0 / 32], down = flags[D / 32 + d0 / 32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(f == 0.f ? 0.f : __uint_as_float(o[e]) * f);
           if (__any_sync(0xffffffffu, (up | down) != 0 && f != 0.f)) {
@@ -492,11 +513,11 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
               uint32_t y[4];
 #pragma unroll
               for (int x = 0; x < 4; ++x) y[x] = T::pack2(__uint_as_float(o[8 * e + 2 * x]), __uint_as_float(o[8 * e + 2 * x + 1]));
-              *reinterpret_cast<uint4*>(qt + block_off(128, row, j * 4 + e)) = make_uint4(y[0], y[1], y[2], y[3]);
+              *reinterpret_cast<uint4*>(qt + block_off(128, row, d0 / 8 + e)) = make_uint4(y[0], y[1], y[2], y[3]);
             }
           } else {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) part[(j * 32 + e) * kPgRowBlock + g * 128 + row] = __uint_as_float(o[e]);
+            for (int e = 0; e < 32; ++e) part[(d0 + e) * kPgRowBlock + g * 128 + row] = __uint_as_float(o[e]);
           }
         }
         if (!cur.whole)
@@ -504,10 +525,10 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
         else if (a.lse && Rg < rows_total)
           a.lse[(static_cast<int64_t>(cur.b) * a.N + at) * a.Hq + cur.h * a.G + (Rg - at * a.G)] = l == 0.f ? -INFINITY : (m_run + log2f(l)) * kLn2;
         tc_fence_before();
+        named_barrier_sync(bar, 128);   // O has been read, the output is in place
         if (cur.whole) {
-          named_barrier_sync(2 + g, 128);
 #pragma unroll
-          for (int j = 0; j < kLpr; ++j) {
+          for (int j = 0; j < kPasses; ++j) {
             const int r = r_0 + j * kRpp, RR = row0 + r;
             if (RR < rows_total) {
               const int nn = paged_node(a, RR);
@@ -515,13 +536,12 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
               *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + to * D * 2 + ch * 16) = *reinterpret_cast<const uint4*>(qt + block_off(128, r, ch));
             }
           }
-          named_barrier_sync(2 + g, 128);   // before q's rows come
+          // The thread that puts a piece of q in place is the one that read the output there.
         }
       }
       if (more && g < halves(next.block)) q_store(w);
-      first = false;
-      cur = next;
-      if (a.parents) named_barrier_sync(4, kRowSoft);   // the tree's place is free for the next piece
+      __syncwarp();   // every lane is done with this piece's cursor
+      if (a.parents) named_barrier_sync(4, kPgRowSoft);   // the tree's place is free for the next piece
     }
   }
   __syncthreads();
