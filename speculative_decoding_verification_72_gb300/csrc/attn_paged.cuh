@@ -14,10 +14,11 @@
 // (attn_paged_rows.cuh, bound by the tensor cores and the exponentials).
 //
 // Split. A block of rows has the 128-slot tiles from its window's start to its
-// last visible slot. The tiles of all (request, block, kv head) items are one
+// last visible slot. The tiles of all (request, block, kv head) items, each with
+// `extra` places before its first for what its beginning and end cost, are one
 // line, cut into equal ranges, one per CTA, so mixed lengths load every CTA
-// alike. A range that holds only part of an item writes a partial (max, sum,
-// unnormalised o) that attn_paged_join_kernel joins, in a fixed order.
+// alike. A range that holds only part of an item's tiles writes a partial (max,
+// sum, unnormalised o) that attn_paged_join_kernel joins, in a fixed order.
 //
 // Non-finite values. A slot's values multiply weights of 0 in rows that do not
 // see it, so a tile that not every row sees whole has infinities and NaN taken
@@ -51,10 +52,10 @@ struct PagedAttnArgs {
   float cap;                   // cap log2(e), or 0
   int32_t window;              // 2^31 - 1 for none
   float* part;                 // [2 grid][R (D + 2)]
-  int32_t* plan;               // [B RB + 1] tile offsets of the blocks, and their total
-  int4* first;                 // [grid]: the item that a CTA's range begins in: its first tile, tiles, block (of B RB), head
+  int32_t* plan;               // [B RB + 1] places before the blocks, and in all, for one kv head
+  int4* first;                 // [grid]: the first item a CTA has tiles of: place of its first tile, tiles, block (of B RB), head
   uint32_t* failed;            // [grid]: whether a wait of the CTA gave up
-  int32_t grid;
+  int32_t grid, extra;
 };
 
 // A request's rows and length, clamped to the page table's capacity (out_status
@@ -101,7 +102,7 @@ struct PagedCursor {
   int32_t pos, off;
   PagedReq rq;
   int b, block, tiles, h, t0, n, node0, end, clear, inside;   // the piece: tiles t0 .. t0 + n - 1 of item (b, block, h)
-  bool whole, fresh;                                     // whole: the piece is all of its item
+  bool whole, fresh;                                          // whole: the piece is all of its item
 
   __device__ __forceinline__ void start(const PagedAttnArgs& a, const AttnLine& line, int32_t lo) {
     pos = lo;
@@ -111,25 +112,24 @@ struct PagedCursor {
     n = 0;
     fresh = true;
   }
-  // The next piece (called while pos + n < hi); pos is then its first tile.
+  // The next piece that has tiles, from place pos on; pos is then the place of its first tile, or at least hi if there is none.
   __device__ __forceinline__ void piece(const PagedAttnArgs& a, int32_t hi) {
-    if (fresh) {
-      rq = paged_req(a, b);
-      fresh = false;
-    }
+    if (fresh) rq = paged_req(a, b);
+    fresh = false;
     PagedSpan s(a, rq, block);
-    while (pos >= (off + s.tiles) * a.c.Hkv) {
-      off += s.tiles;
+    while (pos >= (off + s.tiles + a.extra) * a.c.Hkv) {
+      off += s.tiles + a.extra;
       if (++block == a.RB) {
         block = 0;
         rq = paged_req(a, ++b);
       }
       s = PagedSpan(a, rq, block);
     }
-    const int rel = pos - off * a.c.Hkv;
     tiles = s.tiles;
-    h = rel / tiles;
-    const int t = rel - h * tiles;
+    const int rel = pos - off * a.c.Hkv, places = tiles + a.extra;
+    h = rel / places;
+    const int t = max(rel - h * places - a.extra, 0);
+    pos = off * a.c.Hkv + h * places + a.extra + t;
     n = min(tiles - t, hi - pos);
     whole = n == tiles;
     t0 = s.t + t;
@@ -144,7 +144,7 @@ struct PagedCursor {
   }
   // Of the CTA's first piece.
   __device__ __forceinline__ int4 item(const PagedAttnArgs& a) const {
-    return make_int4(off * a.c.Hkv + h * tiles, tiles, b * a.RB + block, h);
+    return make_int4(off * a.c.Hkv + h * (tiles + a.extra) + a.extra, tiles, b * a.RB + block, h);
   }
 };
 
@@ -156,12 +156,13 @@ __device__ __forceinline__ void paged_line(const PagedAttnArgs& a, AttnLine* s_l
       a.B * a.RB,
       [&](int e) {
         const int b = e / a.RB;
-        return PagedSpan(a, paged_req(a, b), e - b * a.RB).tiles;
+        return PagedSpan(a, paged_req(a, b), e - b * a.RB).tiles + a.extra;
       },
       a.grid, cta, s_line, s_warp, a.c.Hkv, cta == 0 ? a.plan : nullptr);
   if (cta == 0 && threadIdx.x == 0) a.plan[a.B * a.RB] = s_line->total;
   lo = cta < ranges.n ? ranges.begin(cta) : 0;
   hi = cta < ranges.n ? ranges.begin(cta + 1) : 0;
+  if (threadIdx.x == 0) a.first[cta] = make_int4(INT_MAX, 0, 0, 0);   // unless it has a piece
 }
 
 // Pages of a walk through one request, 32 a load: lane l has page 32 g + l of
@@ -273,12 +274,13 @@ __global__ void __launch_bounds__(kPgJoinThreads) attn_paged_join_kernel(const P
   const int at = join / groups + 1;
   if (at >= ranges.n) return;
   const int4 item = a.first[at];
+  if (ranges.begin(at) <= item.x) return;   // the CTA begins with its item, or has none
   const int t0 = item.x, e = item.z, h = item.w, c0 = ranges.cta_of(t0), c1 = ranges.cta_of(t0 + item.y - 1);
-  if (ranges.begin(at) == t0 || at != c0 + 1) return;
+  if (at != c0 + 1) return;
   const int in_block = (join - (at - 1) * groups) * kPgJoinRows;
   const int b = e / a.RB, row0 = (e - b * a.RB) * a.R + in_block;   // of the kv head
   if (row0 >= a.N * a.G) return;
-  const int slot0 = ranges.begin(c0) == t0 ? 0 : 1;
+  const int slot0 = ranges.begin(c0) >= t0 - a.extra ? 0 : 1;   // of what came before the item it has the last tile
   auto partial = [&](int i) { return a.part + static_cast<int64_t>(2 * i + (i == c0 ? slot0 : 0)) * a.R * (D + 2); };
 
   // A thread has one row and D / 8 of its elements: 8 threads a row.

@@ -14,7 +14,7 @@
 // Lane = token in S^T, so a thread has one token's scores for 16 rows, sums over
 // tokens stay in its registers until the end, and P is two 16-byte stores a
 // term. The running maximum is raised only when a score exceeds it by 2^8 (a
-// vote per tile), which takes the slow path: maxima across the CTA and a
+// vote per tile), which takes the slow path: maxima across its warps and a
 // rescale of O^T in TMEM. So does every tile until each row has seen a slot,
 // and every tile that some row does not see whole: masks, and V's rows that are
 // no slots of the request (0 * NaN would reach every row) and non-finite values.
@@ -103,8 +103,9 @@ __device__ __forceinline__ void paged_load(const PagedAttnArgs& a, const CUtenso
   const uint32_t dst0 = ring + half * kPgTile * 128 + mine * box;
   uint32_t n = 0;
   PagedLook look;
-  for (; cur.pos < hi; cur.pos += cur.n) {
-    cur.piece(a, hi);
+  for (;; cur.pos += cur.n) {
+    if (cur.pos < hi) cur.piece(a, hi);
+    if (cur.pos >= hi) break;
     look.start(a, cur.b, cur.t0 << shift, cur.end, lane);
     for (int i = 0; i < cur.n; ++i, ++n) {
       const int page = look.page(a, cur.b, ((cur.t0 + i) << shift) + mine, cur.end, lane);
@@ -201,36 +202,40 @@ __global__ void __launch_bounds__(PgColLayout<D, MT>::kThreads, 1)
     paged_load<D, kSt>(a, &k_map, &v_map, cur, hi, smem0, full, empty, s_there, fail);
   } else if (warp == 4 * MT + 1) {
     // ------------------------------------------------------------------ MMA
-    if (lane == 0) {
-      constexpr uint32_t kIdS = tc_idesc(T::kMma, false, false, 128, R), kIdO = tc_idesc(T::kMma, true, true, 128, L::kNo);
-      bool ok = true;
-      uint32_t pieces = 0;
-      auto scores = [&](uint32_t m) {
-        const uint32_t s = 2 * m, st = s % kSt, sb = m & 1;
-        ok = ok && wait_or_fail(full + 8 * st, (s / kSt) & 1, fail);
-        if (m >= 2) ok = ok && wait_or_fail(s_free + 8 * sb, ((m >> 1) - 1) & 1, fail);
-        if (!ok) return;
-        tc_fence_after();
-        const uint32_t kt = smem0 + st * L::kTileBytes;
+    constexpr uint32_t kIdS = tc_idesc(T::kMma, false, false, 128, R), kIdO = tc_idesc(T::kMma, true, true, 128, L::kNo);
+    bool ok = true;
+    uint32_t pieces = 0;
+    auto scores = [&](uint32_t m) {
+      const uint32_t s = 2 * m, st = s % kSt, sb = m & 1;
+      ok = ok && warp_wait_or_fail(full + 8 * st, (s / kSt) & 1, fail);
+      if (m >= 2) ok = ok && warp_wait_or_fail(s_free + 8 * sb, ((m >> 1) - 1) & 1, fail);
+      if (!ok) return;
+      tc_fence_after();
+      const uint32_t kt = smem0 + st * L::kTileBytes;
+      if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
           tc_mma_f16(tmem + sb * R, tc_desc(kt + (k >> 2) * (kPgTile * 128) + (k & 3) * 32, 16, 1024, 2),
                      tc_desc(smem0 + L::kOffQ + (k >> 2) * (R * 128) + (k & 3) * 32, 16, 1024, 2), kIdS, k > 0);
         tc_commit(empty + 8 * st);
         tc_commit(s_ready + 8 * sb);
-      };
-      for (; ok && cur.pos < hi; cur.pos += cur.n) {
-        cur.piece(a, hi);
-        ok = wait_or_fail(q_ready, pieces++ & 1, fail);
+      }
+      __syncwarp();
+    };
+    for (; ok; cur.pos += cur.n) {
+      if (cur.pos < hi) cur.piece(a, hi);
+      if (cur.pos >= hi) break;
+      ok = warp_wait_or_fail(q_ready, pieces++ & 1, fail);
+      if (!ok) break;
+      scores(n);
+      for (int i = 0; i < cur.n && ok; ++i, ++n) {
+        if (i + 1 < cur.n) scores(n + 1);
+        const uint32_t s = 2 * n + 1, st = s % kSt;
+        ok = ok && warp_wait_or_fail(full + 8 * st, (s / kSt) & 1, fail) && warp_wait_or_fail(p_ready, n & 1, fail);
         if (!ok) break;
-        scores(n);
-        for (int i = 0; i < cur.n && ok; ++i, ++n) {
-          if (i + 1 < cur.n) scores(n + 1);
-          const uint32_t s = 2 * n + 1, st = s % kSt;
-          ok = ok && wait_or_fail(full + 8 * st, (s / kSt) & 1, fail) && wait_or_fail(p_ready, n & 1, fail);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t vt = smem0 + st * L::kTileBytes;
+        tc_fence_after();
+        const uint32_t vt = smem0 + st * L::kTileBytes;
+        if (elect_one()) {
           // 64-wide heads are half of the product's 128 rows; a block stride of 0 gives the other half the same rows.
 #pragma unroll
           for (int k = 0; k < kPgTile / 16; ++k)
@@ -239,9 +244,9 @@ __global__ void __launch_bounds__(PgColLayout<D, MT>::kThreads, 1)
           tc_commit(empty + 8 * st);
           tc_commit(p_free);
         }
+        __syncwarp();
       }
     }
-    __syncwarp();
   } else {
     // -------------------------------------------------------------- softmax
     const int grp = warp >> 2, row = tid & 127, r00 = grp * 16;   // the thread's rows r00 .. r00 + 15, token `row` of a tile
@@ -257,9 +262,10 @@ __global__ void __launch_bounds__(PgColLayout<D, MT>::kThreads, 1)
     // A wait that gives up ends no loop here: these warps meet at barriers, so all
     // run on to the end (every later wait then returns at once), without meaning:
     // the rows of every piece that ends after it are NaN.
-    for (; cur.pos < hi; cur.pos += cur.n) {
-      cur.piece(a, hi);
-      if (cur.pos == lo && tid == 0) a.first[blockIdx.x] = cur.item(a);
+    for (bool first = true;; cur.pos += cur.n, first = false) {
+      if (cur.pos < hi) cur.piece(a, hi);
+      if (cur.pos >= hi) break;
+      if (first && tid == 0) a.first[blockIdx.x] = cur.item(a);
       const PagedReq rq = cur.rq;
       const int row0 = cur.block * R;
       // ---- the rows: q, positions, what they see of the nodes
@@ -346,7 +352,7 @@ __global__ void __launch_bounds__(PgColLayout<D, MT>::kThreads, 1)
           x[2 * j + 1] = __fadd2_rn(x[2 * j + 1], make_float2(-mm.z, -mm.w));
           top = fmaxf(fmaxf(fmaxf(top, x[2 * j].x), x[2 * j].y), fmaxf(x[2 * j + 1].x, x[2 * j + 1].y));
         }
-        if (named_barrier_or(bar, 128, top > kPgSlack + kPgLift<T> || special || *unseen)) {
+        if (named_barrier_or(3, kSoft, top > kPgSlack + kPgLift<T> || special || *unseen)) {   // of one mind, whatever `special` read
           // ---- slow path: masks, maxima, V rows that must not be read
           const bool valid = there >> (row >> a.c.page_shift) & 1 && tok < rq.len;
           uint32_t see = valid ? live : 0u;
@@ -372,7 +378,7 @@ __global__ void __launch_bounds__(PgColLayout<D, MT>::kThreads, 1)
             const float mx = warp_max(v);
             if (lane == 0) max_w[r] = mx;
           }
-          if (special) {
+          if (named_barrier_or(3, kSoft, special)) {
             const uint32_t s = 2 * n + 1, st = s % kSt;
             wait_or_fail(full + 8 * st, (s / kSt) & 1, fail);
             uint8_t* vt = smem + st * L::kTileBytes;
@@ -384,7 +390,7 @@ __global__ void __launch_bounds__(PgColLayout<D, MT>::kThreads, 1)
 #pragma unroll
               for (int ch = 0; ch < D / 8; ++ch) *reinterpret_cast<uint4*>(vt + block_off(kPgTile, row, ch)) = make_uint4(0, 0, 0, 0);
             }
-            if (named_barrier_or(3, kSoft, odd != 0)) {   // rare; maxima are there past it
+            if (named_barrier_or(3, kSoft, odd != 0)) {   // rare
               any_inf = true;
               note_nonfinite<T, D>(vt, row, odd ? see : 0u, s_inf + r00 * (D / 16));
               named_barrier_sync(3, kSoft);   // every group has read the row
@@ -393,8 +399,6 @@ __global__ void __launch_bounds__(PgColLayout<D, MT>::kThreads, 1)
                 for (int ch = 0; ch < D / 8; ++ch) take_out8<T>(reinterpret_cast<uint4*>(vt + block_off(kPgTile, row, ch)));
             }
             fence_async_smem();
-          } else {
-            named_barrier_sync(bar, 128);
           }
           // one thread per row: by how much its maximum rises; a row's first maximum may lie anywhere
           if (row < 16) {
@@ -477,7 +481,7 @@ __global__ void __launch_bounds__(PgColLayout<D, MT>::kThreads, 1)
         if (!(lane & 1)) max_w[lane >> 1] = v[0];
       }
       named_barrier_sync(bar, 128);
-      float* part = a.part + static_cast<int64_t>(2 * blockIdx.x + (cur.pos == lo ? 0 : 1)) * R * (D + 2);
+      float* part = a.part + static_cast<int64_t>(2 * blockIdx.x + (first ? 0 : 1)) * R * (D + 2);
       if (row < 16) {
         const int r = r00 + row, Rg = row0 + r, node = paged_node(a, Rg);
         const float sum = s_node[r] < 0 ? 0.f

@@ -22,13 +22,13 @@
 //
 // A tile that some row does not see whole is masked in registers by 128 bits that
 // the thread works out from its row's position and path; what must not be read of
-// its V is taken out by a warp of its own, as soon as the tile is there.
+// its V is taken out by two warps of their own, as soon as the tile is there.
 //
 // The rows of the next piece's q are loaded while the last products run, and
 // take their place once the output has left it.
 //
 // Warps 0-3 and 4-7: softmax of the halves. 8: TMA. 9: MMA, which takes the
-// halves by turns, so that they fall out of step. 10: V. 11 makes up the last four.
+// halves by turns, so that they fall out of step. 10 and 11: V.
 #pragma once
 
 #include "attn_paged_cols.cuh"
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
       mbar_init(full + 8 * i, 1);
       mbar_init(empty + 8 * i, 1);
     }
-    for (int i = 0; i < kDepth; ++i) mbar_init(v_fit + 8 * i, 32);
+    for (int i = 0; i < kDepth; ++i) mbar_init(v_fit + 8 * i, 64);
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_ready + 8 * i, 1);
       mbar_init(p_ready + 16 * i, 128);       // tokens 0 .. 63 of a tile, of half i
@@ -154,22 +154,22 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
 
   if (warp == 8) {
     paged_load<D, kSt>(a, &k_map, &v_map, cur, hi, smem0, full, empty, s_there, fail);
-  } else if (warp == 10) {
+  } else if (warp >= 10) {
     // -------------------------------------------- V's rows that must not be read
-    bool ok = true;
-    for (; ok && cur.pos < hi; cur.pos += cur.n) {
-      cur.piece(a, hi);
-      for (int i = 0; i < cur.n && ok; ++i, ++n) {
+    // A wait that gives up ends no loop here either: two warps meet at a barrier.
+    for (;; cur.pos += cur.n) {
+      if (cur.pos < hi) cur.piece(a, hi);
+      if (cur.pos >= hi) break;
+      for (int i = 0; i < cur.n; ++i, ++n) {
         const int tok0 = (cur.t0 + i) * kPgTile;
         const uint32_t s = 2 * n + 1, st = s % kSt;
-        ok = wait_or_fail(full + 8 * st, (s / kSt) & 1, fail);
-        if (!ok) break;
+        wait_or_fail(full + 8 * st, (s / kSt) & 1, fail);
         const uint32_t there = s_there[n & 15];
         const bool special = cur.special(a, tok0, there);
         uint8_t* vt = smem + st * L::kTileBytes;
         uint32_t odd = 0;
 #pragma unroll 1
-        for (int row = lane; special && row < kPgTile; row += 32) {
+        for (int row = tid - 320; special && row < kPgTile; row += 64) {
           const bool valid = there >> (row >> a.c.page_shift) & 1 && tok0 + row < cur.rq.len;
 #pragma unroll
           for (int ch = 0; ch < D / 8; ++ch) {
@@ -180,9 +180,9 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
               *p = make_uint4(0, 0, 0, 0);
           }
         }
-        odd = __any_sync(0xffffffffu, odd != 0);
+        odd = named_barrier_or(5, 64, odd != 0);
         uint32_t* flags = s_tok + (n % kDepth) * 128 * (D / 16);
-        for (int row = lane; odd && row < kPgTile; row += 32) {
+        for (int row = tid - 320; odd && row < kPgTile; row += 64) {
           const bool valid = there >> (row >> a.c.page_shift) & 1 && tok0 + row < cur.rq.len;
           for (int ch = 0; ch < D / 8; ++ch) {
             const uint32_t f = valid ? take_out8<T>(reinterpret_cast<uint4*>(vt + block_off(kPgTile, row, ch))) : 0u;
@@ -191,68 +191,75 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
             to[D / 8] = static_cast<uint8_t>(f >> 8);
           }
         }
-        if (lane == 0) s_odd[n % kDepth] = odd;
+        if (tid == 320) s_odd[n % kDepth] = odd;
         fence_async_smem();
         mbar_arrive(v_fit + 8 * (n % kDepth));
       }
     }
   } else if (warp == 9) {
     // ------------------------------------------------------------------ MMA
-    if (lane == 0) {
-      constexpr uint32_t kIdS = tc_idesc(T::kMma, false, false, 128, 128), kIdO = tc_idesc(T::kMma, false, true, 128, D);
-      bool ok = true;
-      uint32_t pieces[2] = {0, 0}, mine[2] = {0, 0};   // by half; mine: tiles
-      auto scores = [&](uint32_t m, int g, bool last) {
-        const uint32_t st = 2 * m % kSt;
-        const uint32_t qt = smem0 + L::kOffQ + g * L::kTileBytes, kt = smem0 + st * L::kTileBytes;
+    constexpr uint32_t kIdS = tc_idesc(T::kMma, false, false, 128, 128), kIdO = tc_idesc(T::kMma, false, true, 128, D);
+    bool ok = true;
+    uint32_t pieces[2] = {0, 0}, mine[2] = {0, 0};   // by half; mine: tiles
+    auto scores = [&](uint32_t m, int g, bool last) {
+      const uint32_t st = 2 * m % kSt;
+      const uint32_t qt = smem0 + L::kOffQ + g * L::kTileBytes, kt = smem0 + st * L::kTileBytes;
+      if (elect_one()) {
 #pragma unroll
         for (int j = 0; j < D / 16; ++j)
           tc_mma_f16(tmem + g * 128, tc_desc(qt + (j >> 2) * (kPgTile * 128) + (j & 3) * 32, 16, 1024, 2),
                      tc_desc(kt + (j >> 2) * (kPgTile * 128) + (j & 3) * 32, 16, 1024, 2), kIdS, j > 0);
         tc_commit(s_ready + 8 * g);
         if (last) tc_commit(empty + 8 * st);
-      };
-      auto k_there = [&](uint32_t m) { ok = ok && wait_or_fail(full + 8 * (2 * m % kSt), (2 * m / kSt) & 1, fail); };
-      for (; ok && cur.pos < hi; cur.pos += cur.n) {
-        cur.piece(a, hi);
-        const int gs = halves(cur.block);
-        k_there(n);
-        for (int g = 0; g < gs && ok; ++g) {
-          ok = wait_or_fail(q_ready + 8 * g, pieces[g]++ & 1, fail);
-          if (!ok) break;
-          tc_fence_after();
-          scores(n, g, g + 1 == gs);
-        }
-        for (int i = 0; i < cur.n && ok; ++i, ++n) {
-          const uint32_t st = (2 * n + 1) % kSt, vt = smem0 + st * L::kTileBytes;
-          const bool more = i + 1 < cur.n;
-          ok = wait_or_fail(v_fit + 8 * (n % kDepth), (n / kDepth) & 1, fail);
-          if (more) k_there(n + 1);
-          for (int g = 0; g < gs && ok; ++g) {
+      }
+      __syncwarp();
+    };
+    auto k_there = [&](uint32_t m) { ok = ok && warp_wait_or_fail(full + 8 * (2 * m % kSt), (2 * m / kSt) & 1, fail); };
+    for (; ok; cur.pos += cur.n) {
+      if (cur.pos < hi) cur.piece(a, hi);
+      if (cur.pos >= hi) break;
+      const int gs = halves(cur.block);
+      k_there(n);
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              ok = ok && wait_or_fail(p_ready + 16 * g + 8 * u, mine[g] & 1, fail);
-              if (!ok) break;
-              tc_fence_after();
+      for (int g = 0; g < 2; ++g) {
+        if (g == gs || !ok) break;
+        ok = warp_wait_or_fail(q_ready + 8 * g, pieces[g]++ & 1, fail);
+        if (!ok) break;
+        tc_fence_after();
+        scores(n, g, g + 1 == gs);
+      }
+      for (int i = 0; i < cur.n && ok; ++i, ++n) {
+        const uint32_t st = (2 * n + 1) % kSt, vt = smem0 + st * L::kTileBytes;
+        const bool more = i + 1 < cur.n;
+        ok = warp_wait_or_fail(v_fit + 8 * (n % kDepth), (n / kDepth) & 1, fail);
+        if (more) k_there(n + 1);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          if (g == gs || !ok) break;
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            ok = ok && warp_wait_or_fail(p_ready + 16 * g + 8 * u, mine[g] & 1, fail);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
               for (int j = 4 * u; j < 4 * u + 4; ++j)   // P's halves lie where those of S did
                 tc_mma_f16_ts(tmem + 256 + g * 128, tmem + g * 128 + (j & 3) * 8 + u * 64, tc_desc(vt + 2048 * j, kPgTile * 128, 1024, 2),
                               kIdO, i > 0 || j > 0);
               if (u == 0) tc_commit(first_done + 8 * g);
+              if (u == 1 && !more) tc_commit(o_done + 8 * g);
             }
-            if (!ok) break;
-            ++mine[g];
-            // The next S overwrites this P: products that one thread issues run in order.
-            if (more)
-              scores(n + 1, g, g + 1 == gs);
-            else
-              tc_commit(o_done + 8 * g);
-            if (g + 1 == gs) tc_commit(empty + 8 * st);
+            __syncwarp();
           }
+          if (!ok) break;
+          ++mine[g];
+          // The next S overwrites this P: products that one thread issues run in order.
+          if (more) scores(n + 1, g, g + 1 == gs);
         }
+        if (ok && elect_one()) tc_commit(empty + 8 * st);
+        __syncwarp();
       }
     }
-    __syncwarp();
   } else if (warp < 8) {
     // -------------------------------------------------------------- softmax
     const int g = warp >> 2, row = tid & 127;   // the thread's half, its row of it
@@ -361,13 +368,13 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
             if (!(there >> ((32 * j + 16) >> a.c.page_shift) & 1)) see[j] &= 0x0000ffffu;
             if (node < 0) see[j] = 0;
           }
-          if (kVar && a.slopes && a.parents) {   // positions of the tile's tokens, relative to base: small enough for fp32
-            const int m = tok0 + row - rq.base;
-            named_barrier_sync(bar, 128);   // every row has read the last such tile's
-            s_at[g * 128 + row] = static_cast<float>(m >= 0 && m < rq.n ? s_depth[m] : m);
-            named_barrier_sync(bar, 128);
-          }
           __syncwarp();
+        }
+        if (kVar && a.slopes && a.parents) {   // positions of the tile's tokens, relative to base: small enough for fp32
+          const int m = tok0 + row - rq.base;
+          named_barrier_sync(bar, 128);   // every row has read the last tile's
+          s_at[g * 128 + row] = static_cast<float>(m >= 0 && m < rq.n ? s_depth[m] : m);
+          named_barrier_sync(bar, 128);
         }
         const float c = kVar ? 1.f : coef;
 #pragma unroll 1
@@ -392,7 +399,7 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
                 for (int j = 0; j < kN; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * coef);
               }
               if (a.slopes) {
-                if (special && a.parents) {
+                if (a.parents) {
                   const float off = static_cast<float>(-depth);
 #pragma unroll
                   for (int j = 0; j < kN; ++j)

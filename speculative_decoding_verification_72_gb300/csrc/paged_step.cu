@@ -69,6 +69,9 @@ bool page_map(const sv_paged_cache& c, const PagedView& v, int kv, CUtensorMap* 
 // one or two groups of 16), else blocks of 256 lanes.
 int paged_block(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : kPgRowBlock; }
 
+// What an item's beginning and end cost, in tiles.
+constexpr int kPagedColExtra = 1, kPagedRowExtra = 2;
+
 constexpr int kPagedGridMost = 160;   // CTAs a workspace is sized for: one an SM, whatever the device
 constexpr int64_t kPagedMostRows = int64_t{1} << 26;   // rows of a kv head; their node is exact up to 2^32 / G
 
@@ -227,7 +230,8 @@ sv_status spec_attention(const sv_rows* q, int32_t dtype, const sv_paged_cache* 
   a.plan = reinterpret_cast<int32_t*>(ws + p.off_plan);
   const int64_t items = B * p.RB * cache->Hkv;
   const int64_t tiles = (static_cast<int64_t>(cache->max_pages) * cache->page_size + kPgTile - 1) / kPgTile;
-  if (items > INT32_MAX / tiles || static_cast<int64_t>(cache->max_pages) * cache->page_size + N > INT32_MAX - 255) return SV_ERR_INVALID_ARG;
+  a.extra = p.block == kPgRowBlock ? kPagedRowExtra : kPagedColExtra;
+  if (items > INT32_MAX / (tiles + a.extra) || static_cast<int64_t>(cache->max_pages) * cache->page_size + N > INT32_MAX - 255) return SV_ERR_INVALID_ARG;
   a.grid = static_cast<int32_t>(std::min<int64_t>({sm_count(), kPagedGridMost, items * tiles}));
   CUtensorMap k, v;
   if (!page_map(*cache, a.c, 0, &k) || !page_map(*cache, a.c, 1, &v)) return SV_ERR_CUDA;

@@ -47,6 +47,15 @@ __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence:
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// One lane of a converged warp. What it guards is known to run in one thread, so
+// the operands of tcgen05 instructions stay in uniform registers; under lane == 0
+// each of them is moved there first (about 65 clocks a product).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // ------------------------------------------------------------------- TMEM
 
 // Warp-collective; cols a power of two >= 32. The address lands at smem word `slot`.
@@ -146,6 +155,11 @@ static __device__ __noinline__ bool wait_or_fail_slow(uint32_t bar, uint32_t par
 
 __device__ __forceinline__ bool wait_or_fail(uint32_t bar, uint32_t parity, volatile uint32_t* fail) {
   return mbar_try_wait_for(bar, parity, kWaitSleepNs) || wait_or_fail_slow(bar, parity, fail);
+}
+
+// The same for a whole warp, which goes on converged and of one mind.
+__device__ __forceinline__ bool warp_wait_or_fail(uint32_t bar, uint32_t parity, volatile uint32_t* fail) {
+  return __all_sync(0xffffffffu, wait_or_fail(bar, parity, fail));
 }
 
 }  // namespace sv
