@@ -117,6 +117,7 @@ struct PagedCursor {
     if (fresh) rq = paged_req(a, b);
     fresh = false;
     PagedSpan s(a, rq, block);
+#pragma unroll 1
     while (pos >= (off + s.tiles + a.extra) * a.c.Hkv) {
       off += s.tiles + a.extra;
       if (++block == a.RB) {
@@ -147,6 +148,20 @@ struct PagedCursor {
     return make_int4(off * a.c.Hkv + h * (tiles + a.extra) + a.extra, tiles, b * a.RB + block, h);
   }
 };
+
+// A warp's cursor, in shared memory, moved on to its next piece (`to` may be
+// `from`). One copy of the code for all roles, which run at once and share the
+// instruction cache.
+__device__ __noinline__ void next_piece(const PagedAttnArgs& a, const PagedCursor* from, PagedCursor* to, int32_t hi) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) {
+    PagedCursor c = *from;
+    c.pos += c.n;
+    if (c.pos < hi) c.piece(a, hi);
+    *to = c;
+  }
+  __syncwarp();
+}
 
 // The line for one CTA: every kernel's prologue. [lo, hi) of it is the CTA's.
 template <int kThreads>
@@ -254,14 +269,17 @@ __global__ void __launch_bounds__(kPgJoinThreads) attn_paged_join_kernel(const P
     const int b = blockIdx.x;
     const PagedReq rq = paged_req(a, b);
     bool bad_page = a.base[b] < 0 || (a.n_nodes && (a.n_nodes[b] < 0 || a.n_nodes[b] > a.N)) || rq.len - rq.n != a.base[b];
+#pragma unroll 1
     for (int j = (rq.n > 0 ? max(rq.base - a.window + 1, 0) >> a.c.page_shift : INT_MAX / 2) + tid;
          j < (rq.len + (1 << a.c.page_shift) - 1) >> a.c.page_shift; j += kPgJoinThreads)
       bad_page = bad_page || paged_page(a.c, b, j) < 0;
     bool tree = false;
     if (a.parents)
+#pragma unroll 1
       for (int n = tid; n < rq.n; n += kPgJoinThreads) tree = tree || bad_parent(a.parents[static_cast<int64_t>(b) * a.N + n], n);
     const int last = ranges.cta_of(a.plan[(b + 1) * a.RB] * a.c.Hkv - 1);
     bool late = false;
+#pragma unroll 1
     for (int i = ranges.cta_of(a.plan[b * a.RB] * a.c.Hkv) + tid; i <= last; i += kPgJoinThreads) late = late || a.failed[i] != 0;
     bad_page = __syncthreads_or(bad_page);
     tree = __syncthreads_or(tree);
@@ -292,6 +310,7 @@ __global__ void __launch_bounds__(kPgJoinThreads) attn_paged_join_kernel(const P
 #pragma unroll
   for (int k = 0; k < kPer; ++k) v[k] = 0.f;
   constexpr int kBatch = D == 128 ? kPgJoinBatch / 2 : kPgJoinBatch;
+#pragma unroll 1
   for (int i0 = c0; i0 <= c1; i0 += kBatch) {
     float2 ml[kBatch];
     float t[kBatch][kPer];
@@ -344,6 +363,7 @@ __global__ void __launch_bounds__(kPgJoinThreads) attn_paged_join_kernel(const P
         l == 0.f ? -INFINITY : ((m == -INFINITY ? 0.f : m) + log2f(l)) * kLn2;
   }
   __syncthreads();
+#pragma unroll 1
   for (int i = tid; i < kPgJoinRows * (D / 8); i += kPgJoinThreads) {
     const int rr = i / (D / 8), ch = i % (D / 8), RR = row0 + rr;
     if (RR >= a.N * a.G) break;

@@ -77,9 +77,11 @@ __device__ __forceinline__ uint32_t block_off(int rows, int row, int ch) {
 // What of a token's V row is not finite goes to the rows that see it.
 template <typename T, int D>
 __device__ __noinline__ void note_nonfinite(const uint8_t* vt, int row, uint32_t see, uint32_t* s_inf) {
+#pragma unroll 1
   for (int ch = 0; see && ch < D / 8; ++ch) {
     uint4 w = *reinterpret_cast<const uint4*>(vt + block_off(kPgTile, row, ch));
     const uint32_t f = take_out8<T>(&w);
+#pragma unroll 1
     for (int r = 0; f && r < 16; ++r) {
       if (!(see >> r & 1)) continue;
       uint32_t* to = s_inf + r * (D / 16) + (ch >> 2);
@@ -92,7 +94,7 @@ __device__ __noinline__ void note_nonfinite(const uint8_t* vt, int row, uint32_t
 // The TMA warp of both kernels: K and V of the CTA's tiles, in turns, into a
 // ring of kStages tiles. s_there has, by tile, which of its pages there are.
 template <int D, int kStages>
-__device__ __forceinline__ void paged_load(const PagedAttnArgs& a, const CUtensorMap* k_map, const CUtensorMap* v_map, PagedCursor cur,
+__device__ __forceinline__ void paged_load(const PagedAttnArgs& a, const CUtensorMap* k_map, const CUtensorMap* v_map, PagedCursor* place,
                                            int32_t hi, uint32_t ring, uint32_t full, uint32_t empty, uint32_t* s_there,
                                            volatile uint32_t* fail) {
   constexpr int kTileBytes = kPgTile * D * 2;
@@ -103,10 +105,11 @@ __device__ __forceinline__ void paged_load(const PagedAttnArgs& a, const CUtenso
   const uint32_t dst0 = ring + half * kPgTile * 128 + mine * box;
   uint32_t n = 0;
   PagedLook look;
-  for (;; cur.pos += cur.n) {
-    if (cur.pos < hi) cur.piece(a, hi);
-    if (cur.pos >= hi) break;
+  const PagedCursor& cur = *place;
+#pragma unroll 1
+  for (; cur.pos < hi; next_piece(a, place, place, hi)) {
     look.start(a, cur.b, cur.t0 << shift, cur.end, lane);
+#pragma unroll 1
     for (int i = 0; i < cur.n; ++i, ++n) {
       const int page = look.page(a, cur.b, ((cur.t0 + i) << shift) + mine, cur.end, lane);
       const uint32_t there = __ballot_sync(0xffffffffu, page >= 0) & ((1u << ppt) - 1u);
@@ -132,18 +135,21 @@ __device__ __forceinline__ void paged_load(const PagedAttnArgs& a, const CUtenso
 // Leaves time for copies and products in flight after a wait gave up.
 __device__ __forceinline__ void settle_after_failure() {
   const uint64_t t = global_timer_ns();
+#pragma unroll 1
   for (int i = 0; i < (1 << 20) && global_timer_ns() - t < 2000000; ++i) {
   }
 }
 
 template <typename T, int D, int MT>
 __global__ void __launch_bounds__(PgColLayout<D, MT>::kThreads, 1)
-    attn_paged_cols_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, const PagedAttnArgs a) {
+    attn_paged_cols_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                           const __grid_constant__ PagedAttnArgs a) {
   using L = PgColLayout<D, MT>;
   constexpr int R = L::R, kSt = L::kStages, kSoft = 128 * MT;
   extern __shared__ uint8_t raw[];
   __shared__ AttnLine s_line;
   __shared__ int32_t s_warp[L::kThreads / 32];
+  __shared__ PagedCursor s_cur[L::kThreads / 32];
   __shared__ __align__(8) uint64_t s_bar[2 * kSt + 7];
   __shared__ uint32_t s_tmem, s_fail, s_there[16];
   const uint32_t smem0 = (smem_u32(raw) + 1023u) & ~1023u;
@@ -166,10 +172,12 @@ __global__ void __launch_bounds__(PgColLayout<D, MT>::kThreads, 1)
   const uint32_t p_ready = s_free + 16, p_free = p_ready + 8, q_ready = p_free + 8;
   if (tid == 0) {
     s_fail = 0;
+#pragma unroll 1
     for (int i = 0; i < kSt; ++i) {
       mbar_init(full + 8 * i, 1);
       mbar_init(empty + 8 * i, 1);
     }
+#pragma unroll 1
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_ready + 8 * i, 1);
       mbar_init(s_free + 8 * i, 4 * MT);
@@ -193,13 +201,15 @@ __global__ void __launch_bounds__(PgColLayout<D, MT>::kThreads, 1)
   grid_dep_launch();
   int32_t lo, hi;
   paged_line<L::kThreads>(a, &s_line, s_warp, lo, hi);
-  PagedCursor cur;   // every role walks the same pieces; n counts tiles across them
-  cur.start(a, s_line, lo);
+  PagedCursor* place = s_cur + warp;   // every role walks the same pieces; n counts tiles across them
+  const PagedCursor& cur = *place;
+  if (lane == 0) place->start(a, s_line, lo);
+  next_piece(a, place, place, hi);
   uint32_t n = 0;
   volatile uint32_t* fail = &s_fail;
 
   if (warp == 4 * MT) {
-    paged_load<D, kSt>(a, &k_map, &v_map, cur, hi, smem0, full, empty, s_there, fail);
+    paged_load<D, kSt>(a, &k_map, &v_map, place, hi, smem0, full, empty, s_there, fail);
   } else if (warp == 4 * MT + 1) {
     // ------------------------------------------------------------------ MMA
     constexpr uint32_t kIdS = tc_idesc(T::kMma, false, false, 128, R), kIdO = tc_idesc(T::kMma, true, true, 128, L::kNo);
@@ -222,12 +232,12 @@ __global__ void __launch_bounds__(PgColLayout<D, MT>::kThreads, 1)
       }
       __syncwarp();
     };
-    for (; ok; cur.pos += cur.n) {
-      if (cur.pos < hi) cur.piece(a, hi);
-      if (cur.pos >= hi) break;
+#pragma unroll 1
+    for (; ok && cur.pos < hi; next_piece(a, place, place, hi)) {
       ok = warp_wait_or_fail(q_ready, pieces++ & 1, fail);
       if (!ok) break;
       scores(n);
+#pragma unroll 1
       for (int i = 0; i < cur.n && ok; ++i, ++n) {
         if (i + 1 < cur.n) scores(n + 1);
         const uint32_t s = 2 * n + 1, st = s % kSt;
@@ -262,14 +272,14 @@ __global__ void __launch_bounds__(PgColLayout<D, MT>::kThreads, 1)
     // A wait that gives up ends no loop here: these warps meet at barriers, so all
     // run on to the end (every later wait then returns at once), without meaning:
     // the rows of every piece that ends after it are NaN.
-    for (bool first = true;; cur.pos += cur.n, first = false) {
-      if (cur.pos < hi) cur.piece(a, hi);
-      if (cur.pos >= hi) break;
+#pragma unroll 1
+    for (bool first = true; cur.pos < hi; next_piece(a, place, place, hi), first = false) {
       if (first && tid == 0) a.first[blockIdx.x] = cur.item(a);
       const PagedReq rq = cur.rq;
       const int row0 = cur.block * R;
       // ---- the rows: q, positions, what they see of the nodes
       const uint8_t* q = a.q + cur.b * a.sqb + static_cast<int64_t>(cur.h) * a.G * a.sqh;
+#pragma unroll 1
       for (int i = tid; i < R * (D / 8); i += kSoft) {
         const int r = i / (D / 8), ch = i % (D / 8), Rg = row0 + r, node = paged_node(a, Rg);
         uint4 w = make_uint4(0, 0, 0, 0);
@@ -285,6 +295,7 @@ __global__ void __launch_bounds__(PgColLayout<D, MT>::kThreads, 1)
         if (a.parents && node >= 0) {
           const int32_t* par = a.parents + static_cast<int64_t>(cur.b) * a.N;
           depth = -1;
+#pragma unroll 1
           for (int m = node; m >= 0; m = tree_up(par, m)) {
             anc |= 1u << m;   // up to 32 rows have up to 32 nodes
             ++depth;
@@ -300,6 +311,7 @@ __global__ void __launch_bounds__(PgColLayout<D, MT>::kThreads, 1)
         s_m[tid] = 0.f;
         s_seen[tid] = 0;
       }
+#pragma unroll 1
       for (int i = tid; i < R * (D / 16); i += kSoft) s_inf[i] = 0;
       if (row == 0) *unseen = 1;
       fence_async_smem();

@@ -11,24 +11,27 @@
 // follow each other and one half's softmax runs under the other's products; one
 // CTA an SM.
 //
-// A thread has one row, so maximum, exponentials and sum are its own. It takes
-// 64 tokens at a time: P of the first 64 is multiplied while those of the others
-// are worked out. The exponentials go by a running maximum, and no maximum of the
-// new scores is taken: their sum, which is needed anyway, shows whether one is
-// too large. In that rare case, and until the row has seen a slot, the maximum is
-// taken, the warp's rows of O are rescaled and the weights done again. P is rounded to 16
-// bits (half a step of the type: 2^-8 of a bf16 weight, 2^-11 of f16's), its sum
-// is not.
+// A thread has one row, so maximum, exponentials and sum are its own. It reads its
+// scores twice, for the maximum and for the exponentials, which it writes over
+// what it has read; P of the first 64 tokens is multiplied while those of the
+// others are worked out. The running maximum is raised only when a score exceeds
+// it by 2^8; the warp then rescales its rows of O. P is rounded to 16 bits (half a
+// step of the type: 2^-8 of a bf16 weight, 2^-11 of f16's), its sum is not.
 //
-// A tile that some row does not see whole is masked in registers by 128 bits that
-// the thread works out from its row's position and path; what must not be read of
-// its V is taken out by two warps of their own, as soon as the tile is there.
+// Capped or biased scores, and those of a tile that some row does not see whole,
+// are made final in TMEM on the first reading: -inf where the row's 128 bits say
+// so, which the thread works out from its position and path. What must not be read
+// of such a tile's V is taken out by two warps of their own as soon as it is there;
+// they also bring the next piece's q once the last scores of this one are done.
 //
-// The rows of the next piece's q are loaded while the last products run, and
-// take their place once the output has left it.
+// The roles run different code at once, and all of it has to stay in the
+// instruction cache: loops are rolled, and what is rare is out of line. With the
+// 128 columns unrolled and read once (held in registers, no maximum where the
+// weights' sum showed that none was too large) a tile took fewer instructions
+// and more time: prompts 425 us against 419 before, capped trees 337 against 218.
 //
 // Warps 0-3 and 4-7: softmax of the halves. 8: TMA. 9: MMA, which takes the
-// halves by turns, so that they fall out of step. 10 and 11: V.
+// halves by turns, so that they fall out of step. 10 and 11: V and q.
 #pragma once
 
 #include "attn_paged_cols.cuh"
@@ -66,30 +69,23 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
 // The bits below bit x of a word.
 __device__ __forceinline__ uint32_t below(int x) { return x <= 0 ? 0u : x >= 32 ? 0xffffffffu : (1u << x) - 1u; }
 
-// What 64 weights of a row may add up to by its running maximum, before that is raised: none is above it, and f16 holds it.
-constexpr float kPgMost = 32768.f;
-
 // What was taken out of the tokens of a tile that a row sees, into the row's flags.
 template <int D>
 __device__ __noinline__ void note_seen(const uint32_t* from, uint32_t s0, uint32_t s1, uint32_t s2, uint32_t s3, uint32_t* to) {
   const uint32_t see[4] = {s0, s1, s2, s3};
+#pragma unroll 1
   for (int t = 0; t < kPgTile; ++t)
     if (see[t >> 5] >> (t & 31) & 1)
+#pragma unroll 1
       for (int w = 0; w < D / 16; ++w) to[w] |= from[t * (D / 16) + w];
 }
 
-// A warp's cursor in shared memory, moved on to its next piece: the softmax warps have no registers for theirs.
-__device__ __noinline__ void next_piece(const PagedAttnArgs& a, const PagedCursor* from, PagedCursor* to, int32_t hi) {
-  if ((threadIdx.x & 31) == 0) {
-    PagedCursor c = *from;
-    c.pos += c.n;
-    if (c.pos < hi) c.piece(a, hi);
-    *to = c;
-  }
-  __syncwarp();
+// 16 bytes from global to shared memory, or zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 
-// kVar: scores are capped or biased.
+// kVar: scores are capped or biased, or their factor is negative.
 template <typename T, int D, bool kVar>
 __global__ void __launch_bounds__(kPgRowThreads, 1)
     attn_paged_rows_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
@@ -99,8 +95,8 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
   extern __shared__ uint8_t raw[];
   __shared__ AttnLine s_line;
   __shared__ int32_t s_warp[kPgRowThreads / 32];
-  __shared__ PagedCursor s_cur[kPgRowSoft / 32][2];
-  __shared__ __align__(8) uint64_t s_bar[2 * kSt + kDepth + 12];
+  __shared__ PagedCursor s_cur[kPgRowThreads / 32][2];
+  __shared__ __align__(8) uint64_t s_bar[2 * kSt + kDepth + 14];
   __shared__ uint32_t s_tmem, s_fail, s_there[16], s_odd[kDepth];   // s_odd: whether values were taken out of a tile's V
   const uint32_t smem0 = (smem_u32(raw) + 1023u) & ~1023u;
   uint8_t* smem = raw + (smem0 - smem_u32(raw));
@@ -112,21 +108,25 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t full = smem_u32(s_bar), empty = full + 8 * kSt, v_fit = empty + 8 * kSt, s_ready = v_fit + 8 * kDepth;
-  const uint32_t p_ready = s_ready + 16, first_done = p_ready + 32, o_done = first_done + 16, q_ready = o_done + 16;
+  const uint32_t p_ready = s_ready + 16, first_done = p_ready + 32, o_done = first_done + 16, q_ready = o_done + 16, q_free = q_ready + 16;
   if (tid == 0) {
     s_fail = 0;
+#pragma unroll 1
     for (int i = 0; i < kSt; ++i) {
       mbar_init(full + 8 * i, 1);
       mbar_init(empty + 8 * i, 1);
     }
+#pragma unroll 1
     for (int i = 0; i < kDepth; ++i) mbar_init(v_fit + 8 * i, 64);
+#pragma unroll 1
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_ready + 8 * i, 1);
       mbar_init(p_ready + 16 * i, 128);       // tokens 0 .. 63 of a tile, of half i
       mbar_init(p_ready + 16 * i + 8, 128);   // tokens 64 .. 127
       mbar_init(first_done + 8 * i, 1);
       mbar_init(o_done + 8 * i, 1);
-      mbar_init(q_ready + 8 * i, 128);
+      mbar_init(q_ready + 8 * i, 64);
+      mbar_init(q_free + 8 * i, 1);
     }
     fence_barrier_init();
   }
@@ -144,8 +144,10 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
   grid_dep_launch();
   int32_t lo, hi;
   paged_line<kPgRowThreads>(a, &s_line, s_warp, lo, hi);
-  PagedCursor cur;   // every role walks the same pieces; n counts tiles across them
-  cur.start(a, s_line, lo);
+  PagedCursor* place = s_cur[warp];   // every role walks the same pieces; n counts tiles across them
+  PagedCursor& cur = place[0];
+  if (lane == 0) cur.start(a, s_line, lo);
+  next_piece(a, place, place, hi);
   uint32_t n = 0;
   volatile uint32_t* fail = &s_fail;
   const int rows_total = a.N * a.G;
@@ -153,13 +155,34 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
   auto halves = [&](int block) { return rows_total - block * kPgRowBlock > 128 ? 2 : 1; };
 
   if (warp == 8) {
-    paged_load<D, kSt>(a, &k_map, &v_map, cur, hi, smem0, full, empty, s_there, fail);
+    paged_load<D, kSt>(a, &k_map, &v_map, &cur, hi, smem0, full, empty, s_there, fail);
   } else if (warp >= 10) {
     // -------------------------------------------- V's rows that must not be read
     // A wait that gives up ends no loop here either: two warps meet at a barrier.
-    for (;; cur.pos += cur.n) {
-      if (cur.pos < hi) cur.piece(a, hi);
-      if (cur.pos >= hi) break;
+    uint32_t pieces[2] = {0, 0};   // by half
+#pragma unroll 1
+    for (; cur.pos < hi; next_piece(a, &cur, &cur, hi)) {
+      // ---- q's rows, D / 8 threads a row
+      const int gs = halves(cur.block);
+      constexpr int kLpr = D / 8;
+      const int ch = (tid - 320) % kLpr;
+      const uint8_t* q = a.q + cur.b * a.sqb + static_cast<int64_t>(cur.h) * a.G * a.sqh + ch * 16;
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        if (g == gs) break;
+        if (pieces[g]++ > 0) wait_or_fail(q_free + 8 * g, pieces[g] & 1, fail);   // of the piece before
+#pragma unroll 4
+        for (int r = (tid - 320) / kLpr; r < 128; r += 64 / kLpr) {
+          const int Rg = cur.block * kPgRowBlock + g * 128 + r, node = paged_node(a, Rg);
+          const bool there = Rg < rows_total && node < cur.rq.n;
+          copy16(smem0 + L::kOffQ + g * L::kTileBytes + block_off(128, r, ch), there ? q + node * a.sqn + (Rg - node * a.G) * a.sqh : a.q, there);
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      fence_async_smem();
+      mbar_arrive(q_ready);
+      if (gs == 2) mbar_arrive(q_ready + 8);
+#pragma unroll 1
       for (int i = 0; i < cur.n; ++i, ++n) {
         const int tok0 = (cur.t0 + i) * kPgTile;
         const uint32_t s = 2 * n + 1, st = s % kSt;
@@ -182,8 +205,10 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
         }
         odd = named_barrier_or(5, 64, odd != 0);
         uint32_t* flags = s_tok + (n % kDepth) * 128 * (D / 16);
+#pragma unroll 1
         for (int row = tid - 320; odd && row < kPgTile; row += 64) {
           const bool valid = there >> (row >> a.c.page_shift) & 1 && tok0 + row < cur.rq.len;
+#pragma unroll 1
           for (int ch = 0; ch < D / 8; ++ch) {
             const uint32_t f = valid ? take_out8<T>(reinterpret_cast<uint4*>(vt + block_off(kPgTile, row, ch))) : 0u;
             uint8_t* to = reinterpret_cast<uint8_t*>(flags + row * (D / 16)) + ch;
@@ -201,7 +226,7 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
     constexpr uint32_t kIdS = tc_idesc(T::kMma, false, false, 128, 128), kIdO = tc_idesc(T::kMma, false, true, 128, D);
     bool ok = true;
     uint32_t pieces[2] = {0, 0}, mine[2] = {0, 0};   // by half; mine: tiles
-    auto scores = [&](uint32_t m, int g, bool last) {
+    auto scores = [&](uint32_t m, int g, bool last, bool end) {
       const uint32_t st = 2 * m % kSt;
       const uint32_t qt = smem0 + L::kOffQ + g * L::kTileBytes, kt = smem0 + st * L::kTileBytes;
       if (elect_one()) {
@@ -211,13 +236,13 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
                      tc_desc(kt + (j >> 2) * (kPgTile * 128) + (j & 3) * 32, 16, 1024, 2), kIdS, j > 0);
         tc_commit(s_ready + 8 * g);
         if (last) tc_commit(empty + 8 * st);
+        if (end) tc_commit(q_free + 8 * g);   // the piece's last
       }
       __syncwarp();
     };
     auto k_there = [&](uint32_t m) { ok = ok && warp_wait_or_fail(full + 8 * (2 * m % kSt), (2 * m / kSt) & 1, fail); };
-    for (; ok; cur.pos += cur.n) {
-      if (cur.pos < hi) cur.piece(a, hi);
-      if (cur.pos >= hi) break;
+#pragma unroll 1
+    for (; ok && cur.pos < hi; next_piece(a, &cur, &cur, hi)) {
       const int gs = halves(cur.block);
       k_there(n);
 #pragma unroll
@@ -226,8 +251,9 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
         ok = warp_wait_or_fail(q_ready + 8 * g, pieces[g]++ & 1, fail);
         if (!ok) break;
         tc_fence_after();
-        scores(n, g, g + 1 == gs);
+        scores(n, g, g + 1 == gs, cur.n == 1);
       }
+#pragma unroll 1
       for (int i = 0; i < cur.n && ok; ++i, ++n) {
         const uint32_t st = (2 * n + 1) % kSt, vt = smem0 + st * L::kTileBytes;
         const bool more = i + 1 < cur.n;
@@ -254,7 +280,7 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
           if (!ok) break;
           ++mine[g];
           // The next S overwrites this P: products that one thread issues run in order.
-          if (more) scores(n + 1, g, g + 1 == gs);
+          if (more) scores(n + 1, g, g + 1 == gs, i + 2 == cur.n);
         }
         if (ok && elect_one()) tc_commit(empty + 8 * st);
         __syncwarp();
@@ -266,47 +292,14 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
     const int bar = 2 + g;                       // of the half's threads
     const uint32_t t_lane = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t t_s = t_lane + g * 128, t_o = t_lane + 256 + g * 128;
-    uint8_t* qt = smem + L::kOffQ + g * L::kTileBytes;
     uint32_t* flags = s_row + (g * 128 + row) * (D / 16);
     uint32_t mine = 0, pieces = 0;   // tiles and pieces of this half
-    constexpr int kLpr = D / 8, kRpp = 128 / kLpr, kPasses = kLpr;   // lanes a row of q or of the output, rows a pass, passes
-    const int ch = row % kLpr, r_0 = row / kLpr;
-    // q's rows of a piece, D / 8 lanes a row: into registers, and to their place.
-    auto q_load = [&](const PagedCursor& c, uint4 (&w)[kPasses]) {
-      const uint8_t* q = a.q + c.b * a.sqb + static_cast<int64_t>(c.h) * a.G * a.sqh + ch * 16;
-      const int first = c.block * kPgRowBlock + g * 128 + r_0;
-#pragma unroll
-      for (int j = 0; j < kPasses; ++j) {
-        const int Rg = first + j * kRpp, node = paged_node(a, Rg);
-        w[j] = make_uint4(0, 0, 0, 0);
-        if (Rg < rows_total && node < c.rq.n) w[j] = *reinterpret_cast<const uint4*>(q + node * a.sqn + (Rg - node * a.G) * a.sqh);
-      }
-    };
-    auto q_store = [&](const uint4 (&w)[kPasses]) {
-      const uint32_t flip = a.coef < 0.f ? 0x80008000u : 0u;   // scores grow with S
-#pragma unroll
-      for (int j = 0; j < kPasses; ++j)
-        *reinterpret_cast<uint4*>(qt + block_off(128, r_0 + j * kRpp, ch)) = make_uint4(w[j].x ^ flip, w[j].y ^ flip, w[j].z ^ flip, w[j].w ^ flip);
-      fence_async_smem();
-      mbar_arrive(q_ready + 8 * g);
-    };
-    const float coef = fabsf(a.coef);
-    PagedCursor* place = s_cur[warp];
-    if (lane == 0) place[1] = cur;
-    __syncwarp();
-    next_piece(a, place + 1, place, hi);
-    if (place->pos < hi) {
-      if (tid == 0) a.first[blockIdx.x] = place->item(a);
-      if (g < halves(place->block)) {
-        uint4 w[kPasses];
-        q_load(*place, w);
-        q_store(w);
-      }
-    }
+    if (place->pos < hi && tid == 0) a.first[blockIdx.x] = place->item(a);
     uint32_t count = 0;   // pieces
     // A wait that gives up ends no loop here: these warps meet at barriers, so all
     // run on to the end (every later wait then returns at once), without meaning:
     // the rows of every piece that ends after it are NaN.
+#pragma unroll 1
     for (; place[count & 1].pos < hi; ++count) {
       const PagedCursor& cur = place[count & 1];
       const PagedReq& rq = cur.rq;
@@ -321,10 +314,13 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
       for (int j = 0; j < D / 16; ++j) flags[j] = 0;
       if (a.parents && active) {
         const int32_t* par = a.parents + static_cast<int64_t>(cur.b) * a.N;
+#pragma unroll 1
         for (int i = tid; i < rq.n; i += soft) s_par[i] = static_cast<int16_t>(tree_up(par, i));
         named_barrier_sync(1, soft);
+#pragma unroll 1
         for (int i = tid; i < rq.n; i += soft) {
           int d = 0;
+#pragma unroll 1
           for (int m = s_par[i]; m >= 0; m = s_par[m]) ++d;
           s_depth[i] = static_cast<int16_t>(d);
         }
@@ -335,9 +331,11 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
       const int open = max(pos - a.window + 1, 0);   // the window's first position
       const float slope = kVar && a.slopes && node >= 0 ? a.slopes[cur.h * a.G + Rg - at * a.G] * kLog2e : 0.f;
 
-      const int tiles = active ? cur.n : 0, t0 = cur.t0;
-      float m_run = 0.f, l = 0.f;   // m_run means something once the row has seen a slot
-      bool seen = node < 0;           // (what no row needs may be anything)
+      const int tiles = active ? cur.n : 0, t0 = cur.t0, clear = cur.clear, inside = cur.inside;
+      const uint32_t all_pages = (1u << (kPgTile >> a.c.page_shift)) - 1u;
+      const float c = kVar ? 1.f : a.coef;   // of what the second reading finds
+      float m_run = 0.f, l = 0.f;            // m_run means something once the row has seen a slot
+      bool seen = false;
 #pragma unroll 1
       for (int i = 0; i < tiles; ++i, ++mine) {
         const uint32_t tile = n + i;
@@ -345,25 +343,27 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
         wait_or_fail(s_ready + 8 * g, mine & 1, fail);   // and every product before this S is done
         tc_fence_after();
         const uint32_t there = s_there[tile & 15];
-        const bool special = cur.special(a, tok0, there);
+        const bool special = tok0 + kPgTile > clear || tok0 < inside || there != all_pages;
         uint32_t see[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};   // what the row sees of the tile
         if (special) {
-          uint32_t path[4] = {0, 0, 0, 0};   // tokens on the row's way up
           if (a.parents) {
             int far = 0;
-            for (int m = node; m >= 0 && far < a.window; m = s_par[m], ++far) {
-              const int c = rq.base + m - tok0;
-              if (c < 0) break;   // parents come before
+#pragma unroll
+            for (int j = 0; j < 4; ++j) see[j] = 0;
+#pragma unroll 1
+            for (int m = node; m >= 0 && far < a.window; m = s_par[m], ++far) {   // tokens on the row's way up
+              const int t = rq.base + m - tok0;
+              if (t < 0) break;   // parents come before
 #pragma unroll
               for (int j = 0; j < 4; ++j)
-                if (c >> 5 == j) path[j] |= 1u << (c & 31);
+                if (t >> 5 == j) see[j] |= 1u << (t & 31);
             }
           }
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const int c = tok0 + 32 * j;
-            see[j] = a.parents ? (below(rq.base - c) & ~below(open - c)) | path[j] : below(rq.base + node + 1 - c) & ~below(open - c);
-            see[j] &= below(rq.len - c);
+            const int t = tok0 + 32 * j;
+            const uint32_t before = below((a.parents ? rq.base : rq.base + node + 1) - t) & ~below(open - t);
+            see[j] = (a.parents ? see[j] | before : before) & below(rq.len - t);
             if (!(there >> (32 * j >> a.c.page_shift) & 1)) see[j] &= 0xffff0000u;
             if (!(there >> ((32 * j + 16) >> a.c.page_shift) & 1)) see[j] &= 0x0000ffffu;
             if (node < 0) see[j] = 0;
@@ -376,105 +376,100 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
           s_at[g * 128 + row] = static_cast<float>(m >= 0 && m < rq.n ? s_depth[m] : m);
           named_barrier_sync(bar, 128);
         }
-        const float c = kVar ? 1.f : coef;
+        // ---- maximum
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if (kVar || special) {
 #pragma unroll 1
-        for (int u = 0; u < 2; ++u) {
-          const uint32_t see0 = u ? see[2] : see[0], see1 = u ? see[3] : see[1];
-          // N scores from token `at_t` of the tile on, in units of log2 but for the factor c; -inf where the row does not see.
-          auto scores = [&]<int kN>(uint32_t (&x)[kN], int at_t) {
-#pragma unroll
-            for (int j = 0; j < kN; j += 16) tmem_ld16(t_s + at_t + j, x + j);
+          for (int j = 0; j < kPgTile; j += 32) {
+            uint32_t x[32];
+            tmem_ld32(t_s + j, x);
+            const uint32_t on = j == 0 ? see[0] : j == 32 ? see[1] : j == 64 ? see[2] : see[3];
             tmem_ld_wait();
             tmem_use(x);
             if (kVar) {
               if (a.cap != 0.f) {
 #pragma unroll
-                for (int j = 0; j < kN; ++j) {
+                for (int e = 0; e < 32; ++e) {
                   float r;
-                  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(__uint_as_float(x[j]) * coef)));
-                  x[j] = __float_as_uint(fmaf(-2.f * a.cap, r, a.cap));
+                  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(__uint_as_float(x[e]) * a.coef)));
+                  x[e] = __float_as_uint(fmaf(-2.f * a.cap, r, a.cap));
                 }
               } else {
 #pragma unroll
-                for (int j = 0; j < kN; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * coef);
+                for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * a.coef);
               }
               if (a.slopes) {
-                if (a.parents) {
-                  const float off = static_cast<float>(-depth);
+                const float off = static_cast<float>(a.parents ? -depth : tok0 + j - pos);
 #pragma unroll
-                  for (int j = 0; j < kN; ++j)
-                    x[j] = __float_as_uint(fmaf(slope, s_at[g * 128 + at_t + j] + off, __uint_as_float(x[j])));
-                } else {
-                  const float off = static_cast<float>(tok0 + at_t - pos);
-#pragma unroll
-                  for (int j = 0; j < kN; ++j) x[j] = __float_as_uint(fmaf(slope, off + static_cast<float>(j), __uint_as_float(x[j])));
+                for (int e = 0; e < 32; ++e) {
+                  const float far = a.parents ? s_at[g * 128 + j + e] : static_cast<float>(e);
+                  x[e] = __float_as_uint(fmaf(slope, far + off, __uint_as_float(x[e])));
                 }
               }
             }
-            if (special) {
-              const uint64_t on = (static_cast<uint64_t>(see1) << 32 | see0) >> (at_t & 63);
 #pragma unroll
-              for (int j = 0; j < kN; ++j) x[j] = on >> j & 1 ? x[j] : 0xff800000u;
+            for (int e = 0; e < 32; ++e) {
+              x[e] = on >> e & 1 ? x[e] : 0xff800000u;
+              mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(x[e]));
             }
-          };
-          uint32_t h[32];
-          float total;
-          for (;;) {
-            // ---- weights by the running maximum, their sum
-            uint32_t w[64];
-            scores(w, u * 64);
-            const float2 c2 = make_float2(c, c), m2 = make_float2(-m_run, -m_run);
-            float2 sum[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) sum[j] = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const float2 y = __ffma2_rn(make_float2(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1])), c2, m2);
-              const float2 p = make_float2(ex2(y.x), ex2(y.y));
-              sum[j & 3] = __fadd2_rn(sum[j & 3], p);
-              h[j] = T::pack2(p.x, p.y);
-            }
-            sum[0] = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
-            total = sum[0].x + sum[0].y;
-            // The sum bounds each weight: no maximum is needed to see that none is too large.
-            if (!__any_sync(0xffffffffu, !seen || total > kPgMost)) break;
-            // ---- rare: the scores' maximum, and the row by it
-            float most = -INFINITY;
-#pragma unroll 1
-            for (int j = 0; j < 64; j += 16) {
-              uint32_t x[16];
-              scores(x, u * 64 + j);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) most = fmaxf(most, __uint_as_float(x[e]));
-            }
-            const float top = most == -INFINITY ? -INFINITY : fmaf(most, c, -m_run);
-            const bool raise = seen ? total > kPgMost && top > kPgLift<T> : top > -INFINITY;
-            const float f = raise && seen ? ex2(kPgLift<T> - top) : 1.f;
-            if (raise) m_run += top - kPgLift<T>;
-            const bool settled = __all_sync(0xffffffffu, !raise);   // nothing has changed: what is still unseen has no weight, NaN stays
-            seen = seen || raise;
-            l *= f;
-            if (i + u > 0 && __any_sync(0xffffffffu, f != 1.f)) {
-              if (u == 1) {   // the first tokens' products are the last that touch O
-                wait_or_fail(first_done + 8 * g, mine & 1, fail);
-                tc_fence_after();
-              }
-#pragma unroll 1
-              for (int j = 0; j < D / 16; ++j) {
-                uint32_t o[16];
-                tmem_ld16(t_o + j * 16, o);
-                tmem_ld_wait();
-                tmem_use(o);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                tmem_st16(t_o + j * 16, o);
-              }
-            }
-            if (settled) break;
+            tmem_st16(t_s + j, x);
+            tmem_st16(t_s + j + 16, x + 16);
           }
-          l += total;
-          tmem_st16(t_s + u * 64, h);
-          tmem_st16(t_s + u * 64 + 16, h + 16);
+          tmem_st_wait();
+        } else {
+#pragma unroll 1
+          for (int j = 0; j < kPgTile; j += 64) {
+            uint32_t x[64];
+            tmem_ld32(t_s + j, x);
+            tmem_ld32(t_s + j + 32, x + 32);
+            tmem_ld_wait();
+            tmem_use(x);
+#pragma unroll
+            for (int e = 0; e < 64; e += 2) mx[e >> 1 & 3] = fmaxf(fmaxf(mx[e >> 1 & 3], __uint_as_float(x[e])), __uint_as_float(x[e + 1]));
+          }
+        }
+        const float most = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        const float top = most == -INFINITY ? -INFINITY : fmaf(most, c, -m_run);
+        const bool raise = seen ? top > kPgSlack + kPgLift<T> : top > -INFINITY;
+        if (__any_sync(0xffffffffu, raise)) {
+          const float f = raise && seen ? ex2(kPgLift<T> - top) : 1.f;
+          if (raise) m_run += top - kPgLift<T>;
+          seen = seen || raise;
+          l *= f;
+          if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+#pragma unroll 1
+            for (int j = 0; j < D; j += 16) {
+              uint32_t o[16];
+              tmem_ld16(t_o + j, o);
+              tmem_ld_wait();
+              tmem_use(o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st16(t_o + j, o);
+            }
+          }
+        }
+        // ---- weights over the scores, their sum
+        const float2 c2 = make_float2(c, c), m2 = make_float2(-m_run, -m_run);
+        float2 sum[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum[j] = make_float2(0.f, 0.f);
+#pragma unroll 1
+        for (int u = 0; u < 2; ++u) {
+          uint32_t x[64];
+          tmem_ld32(t_s + u * 64, x);
+          tmem_ld32(t_s + u * 64 + 32, x + 32);
+          tmem_ld_wait();
+          tmem_use(x);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float2 y = __ffma2_rn(make_float2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), c2, m2);
+            const float2 p = make_float2(ex2(y.x), ex2(y.y));
+            sum[j & 3] = __fadd2_rn(sum[j & 3], p);
+            x[j] = T::pack2(p.x, p.y);
+          }
+          tmem_st16(t_s + u * 64, x);
+          tmem_st16(t_s + u * 64 + 16, x + 16);
           if (special && u == 1) {   // what was taken out of V, before the tile is given up
             wait_or_fail(v_fit + 8 * (tile % kDepth), (tile / kDepth) & 1, fail);
             if (const_cast<volatile uint32_t*>(s_odd)[tile % kDepth])
@@ -484,29 +479,28 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
           tc_fence_before();
           mbar_arrive(p_ready + 16 * g + 8 * u);
         }
+        sum[0] = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
+        l += sum[0].x + sum[0].y;
       }
       n += cur.n;
-      // ---- the piece's rows, under whose last products the next piece's are loaded
-      const PagedCursor& next = place[~count & 1];
+      // ---- the piece's rows, under whose last products the cursor moves on
       next_piece(a, &cur, place + (~count & 1), hi);
-      const bool more = next.pos < hi;
-      uint4 w[kPasses];
-      if (more && g < halves(next.block)) q_load(next, w);
       if (active) {
         wait_or_fail(o_done + 8 * g, pieces++ & 1, fail);
         tc_fence_after();
         if (*fail) l = __int_as_float(0x7fc00000);
         if (node < 0) l = 0.f;
         const float f = l == 0.f ? 0.f : cur.whole ? 1.f / l : 1.f;
-        float* part = a.part + static_cast<int64_t>(2 * blockIdx.x + (count == 0 ? 0 : 1)) * kPgRowBlock * (D + 2);
+        float* part = a.part + static_cast<int64_t>(2 * blockIdx.x + (count == 0 ? 0 : 1)) * kPgRowBlock * (D + 2) + g * 128 + row;
+        const int64_t to = (static_cast<int64_t>(cur.b) * a.N + at) * a.Hq + cur.h * a.G + (Rg - at * a.G);
+        uint8_t* out = static_cast<uint8_t*>(a.out) + to * D * 2;
 #pragma unroll 1
-        for (int j = 0; j < D / 32; ++j) {
-          const int d0 = j * 32;
+        for (int j = 0; j < D; j += 32) {
           uint32_t o[32];
-          tmem_ld32(t_o + j * 32, o);
+          tmem_ld32(t_o + j, o);
+          const uint32_t up = flags[j / 32], down = flags[D / 32 + j / 32];
           tmem_ld_wait();
           tmem_use(o);
-          const uint32_t up = flags[d0 / 32], down = flags[D / 32 + d0 / 32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(f == 0.f ? 0.f : __uint_as_float(o[e]) * f);
           if (__any_sync(0xffffffffu, (up | down) != 0 && f != 0.f)) {
@@ -514,40 +508,28 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
             for (int e = 0; e < 32; ++e)
               if (f != 0.f) o[e] = __float_as_uint(put_back(__uint_as_float(o[e]), up >> e & 1, down >> e & 1));
           }
-          if (cur.whole) {   // the rows of q are done with: their place takes the output's
+          if (cur.whole) {
+            if (Rg < rows_total) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t y[4];
+              for (int e = 0; e < 4; ++e) {
+                uint32_t y[4];
 #pragma unroll
-              for (int x = 0; x < 4; ++x) y[x] = T::pack2(__uint_as_float(o[8 * e + 2 * x]), __uint_as_float(o[8 * e + 2 * x + 1]));
-              *reinterpret_cast<uint4*>(qt + block_off(128, row, d0 / 8 + e)) = make_uint4(y[0], y[1], y[2], y[3]);
+                for (int x = 0; x < 4; ++x) y[x] = T::pack2(__uint_as_float(o[8 * e + 2 * x]), __uint_as_float(o[8 * e + 2 * x + 1]));
+                *reinterpret_cast<uint4*>(out + (j + 8 * e) * 2) = make_uint4(y[0], y[1], y[2], y[3]);
+              }
             }
           } else {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) part[(d0 + e) * kPgRowBlock + g * 128 + row] = __uint_as_float(o[e]);
+            for (int e = 0; e < 32; ++e) part[(j + e) * kPgRowBlock] = __uint_as_float(o[e]);
           }
+          __syncwarp();
         }
         if (!cur.whole)
-          *reinterpret_cast<float2*>(part + kPgRowBlock * D + (g * 128 + row) * 2) = make_float2(l == 0.f ? -INFINITY : m_run, l);
+          *reinterpret_cast<float2*>(part + kPgRowBlock * D + g * 128 + row) = make_float2(l == 0.f ? -INFINITY : m_run, l);
         else if (a.lse && Rg < rows_total)
-          a.lse[(static_cast<int64_t>(cur.b) * a.N + at) * a.Hq + cur.h * a.G + (Rg - at * a.G)] = l == 0.f ? -INFINITY : (m_run + log2f(l)) * kLn2;
+          a.lse[to] = l == 0.f ? -INFINITY : (m_run + log2f(l)) * kLn2;
         tc_fence_before();
-        named_barrier_sync(bar, 128);   // O has been read, the output is in place
-        if (cur.whole) {
-#pragma unroll
-          for (int j = 0; j < kPasses; ++j) {
-            const int r = r_0 + j * kRpp, RR = row0 + r;
-            if (RR < rows_total) {
-              const int nn = paged_node(a, RR);
-              const int64_t to = (static_cast<int64_t>(cur.b) * a.N + nn) * a.Hq + cur.h * a.G + (RR - nn * a.G);
-              *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + to * D * 2 + ch * 16) = *reinterpret_cast<const uint4*>(qt + block_off(128, r, ch));
-            }
-          }
-          // The thread that puts a piece of q in place is the one that read the output there.
-        }
       }
-      if (more && g < halves(next.block)) q_store(w);
-      __syncwarp();   // every lane is done with this piece's cursor
       if (a.parents) named_barrier_sync(4, kPgRowSoft);   // the tree's place is free for the next piece
     }
   }

@@ -115,11 +115,13 @@ __global__ void __launch_bounds__(kRopeThreads) kv_append_rope_kernel(const Rope
   const int64_t end = static_cast<int64_t>(max(base, 0)) + n;
   bad = bad || end > static_cast<int64_t>(a.c.max_pages) << a.c.page_shift;
   if (!bad && n > 0)
+#pragma unroll 1
     for (int64_t lp = (base >> a.c.page_shift) + tid; lp <= (end - 1) >> a.c.page_shift; lp += kRopeThreads)
       bad = bad || paged_page(a.c, b, static_cast<int>(lp)) < 0;
   bool bad_tree = false;
   if (a.parents) {
     const int upto = row0 == 0 ? n : min(row0 + rows, n);   // the first CTA looks at the whole tree
+#pragma unroll 1
     for (int i = tid; i < upto; i += kRopeThreads) {
       s_par[i] = a.parents[static_cast<int64_t>(b) * a.N + i];
       bad_tree = bad_tree || bad_parent(s_par[i], i);
@@ -144,6 +146,7 @@ __global__ void __launch_bounds__(kRopeThreads) kv_append_rope_kernel(const Rope
       s_off[i][tid] = page < 0 ? -1 : page * a.c.sp[i] + (slot & ((1 << a.c.page_shift) - 1)) * a.c.st[i];
   }
   __syncthreads();
+#pragma unroll 1
   for (int i = tid; i < rows * half; i += kRopeThreads) {
     const int r = i / half, j = i - r * half;
     const float2 cs = rope_angle(max(s_pos[r], 0), a.inv_freq[j]);
@@ -153,6 +156,7 @@ __global__ void __launch_bounds__(kRopeThreads) kv_append_rope_kernel(const Rope
   __syncthreads();
 
   // ---- rotation
+#pragma unroll 1
   for (int it = 0; it * kStep < total; it += kRopeBatch) {
     if (it > 0) load(it);
 #pragma unroll

@@ -70,7 +70,7 @@ bool page_map(const sv_paged_cache& c, const PagedView& v, int kv, CUtensorMap* 
 int paged_block(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : kPgRowBlock; }
 
 // What an item's beginning and end cost, in tiles.
-constexpr int kPagedColExtra = 1, kPagedRowExtra = 2;
+constexpr int kPagedColExtra = 1, kPagedRowExtra = 4;
 
 constexpr int kPagedGridMost = 160;   // CTAs a workspace is sized for: one an SM, whatever the device
 constexpr int64_t kPagedMostRows = int64_t{1} << 26;   // rows of a kv head; their node is exact up to 2^32 / G
@@ -119,7 +119,7 @@ template <typename T, int D>
 cudaError_t launch_attention(const CUtensorMap& k, const CUtensorMap& v, const PagedAttnArgs& a, cudaStream_t st) {
   if (a.R == 16) return launch_cols<T, D, 1>(k, v, a, st);
   if (a.R == 32) return launch_cols<T, D, 2>(k, v, a, st);
-  return a.cap != 0.f || a.slopes ? launch_rows<T, D, true>(k, v, a, st) : launch_rows<T, D, false>(k, v, a, st);
+  return a.cap != 0.f || a.slopes || a.coef < 0.f ? launch_rows<T, D, true>(k, v, a, st) : launch_rows<T, D, false>(k, v, a, st);
 }
 
 }  // namespace
