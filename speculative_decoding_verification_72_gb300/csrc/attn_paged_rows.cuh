@@ -21,8 +21,8 @@
 // Capped or biased scores, and those of a tile that some row does not see whole,
 // are made final in TMEM on the first reading: -inf where the row's 128 bits say
 // so, which the thread works out from its position and path. What must not be read
-// of such a tile's V is taken out by two warps of their own as soon as it is there;
-// they also bring the next piece's q once the last scores of this one are done.
+// of such a tile's V is taken out by two warps of their own as soon as it is there.
+// The rows of the next piece's q come in under the last products of this one.
 //
 // The roles run different code at once, and all of it has to stay in the
 // instruction cache: loops are rolled, and what is rare is out of line. With the
@@ -31,7 +31,7 @@
 // and more time: prompts 425 us against 419 before, capped trees 337 against 218.
 //
 // Warps 0-3 and 4-7: softmax of the halves. 8: TMA. 9: MMA, which takes the
-// halves by turns, so that they fall out of step. 10 and 11: V and q.
+// halves by turns, so that they fall out of step. 10 and 11: V.
 #pragma once
 
 #include "attn_paged_cols.cuh"
@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
   __shared__ AttnLine s_line;
   __shared__ int32_t s_warp[kPgRowThreads / 32];
   __shared__ PagedCursor s_cur[kPgRowThreads / 32][2];
-  __shared__ __align__(8) uint64_t s_bar[2 * kSt + kDepth + 14];
+  __shared__ __align__(8) uint64_t s_bar[2 * kSt + kDepth + 12];
   __shared__ uint32_t s_tmem, s_fail, s_there[16], s_odd[kDepth];   // s_odd: whether values were taken out of a tile's V
   const uint32_t smem0 = (smem_u32(raw) + 1023u) & ~1023u;
   uint8_t* smem = raw + (smem0 - smem_u32(raw));
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t full = smem_u32(s_bar), empty = full + 8 * kSt, v_fit = empty + 8 * kSt, s_ready = v_fit + 8 * kDepth;
-  const uint32_t p_ready = s_ready + 16, first_done = p_ready + 32, o_done = first_done + 16, q_ready = o_done + 16, q_free = q_ready + 16;
+  const uint32_t p_ready = s_ready + 16, first_done = p_ready + 32, o_done = first_done + 16, q_ready = o_done + 16;
   if (tid == 0) {
     s_fail = 0;
 #pragma unroll 1
@@ -125,8 +125,7 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
       mbar_init(p_ready + 16 * i + 8, 128);   // tokens 64 .. 127
       mbar_init(first_done + 8 * i, 1);
       mbar_init(o_done + 8 * i, 1);
-      mbar_init(q_ready + 8 * i, 64);
-      mbar_init(q_free + 8 * i, 1);
+      mbar_init(q_ready + 8 * i, 128);
     }
     fence_barrier_init();
   }
@@ -159,29 +158,8 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
   } else if (warp >= 10) {
     // -------------------------------------------- V's rows that must not be read
     // A wait that gives up ends no loop here either: two warps meet at a barrier.
-    uint32_t pieces[2] = {0, 0};   // by half
 #pragma unroll 1
     for (; cur.pos < hi; next_piece(a, &cur, &cur, hi)) {
-      // ---- q's rows, D / 8 threads a row
-      const int gs = halves(cur.block);
-      constexpr int kLpr = D / 8;
-      const int ch = (tid - 320) % kLpr;
-      const uint8_t* q = a.q + cur.b * a.sqb + static_cast<int64_t>(cur.h) * a.G * a.sqh + ch * 16;
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        if (g == gs) break;
-        if (pieces[g]++ > 0) wait_or_fail(q_free + 8 * g, pieces[g] & 1, fail);   // of the piece before
-#pragma unroll 4
-        for (int r = (tid - 320) / kLpr; r < 128; r += 64 / kLpr) {
-          const int Rg = cur.block * kPgRowBlock + g * 128 + r, node = paged_node(a, Rg);
-          const bool there = Rg < rows_total && node < cur.rq.n;
-          copy16(smem0 + L::kOffQ + g * L::kTileBytes + block_off(128, r, ch), there ? q + node * a.sqn + (Rg - node * a.G) * a.sqh : a.q, there);
-        }
-      }
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      fence_async_smem();
-      mbar_arrive(q_ready);
-      if (gs == 2) mbar_arrive(q_ready + 8);
 #pragma unroll 1
       for (int i = 0; i < cur.n; ++i, ++n) {
         const int tok0 = (cur.t0 + i) * kPgTile;
@@ -226,7 +204,7 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
     constexpr uint32_t kIdS = tc_idesc(T::kMma, false, false, 128, 128), kIdO = tc_idesc(T::kMma, false, true, 128, D);
     bool ok = true;
     uint32_t pieces[2] = {0, 0}, mine[2] = {0, 0};   // by half; mine: tiles
-    auto scores = [&](uint32_t m, int g, bool last, bool end) {
+    auto scores = [&](uint32_t m, int g, bool last) {
       const uint32_t st = 2 * m % kSt;
       const uint32_t qt = smem0 + L::kOffQ + g * L::kTileBytes, kt = smem0 + st * L::kTileBytes;
       if (elect_one()) {
@@ -236,7 +214,6 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
                      tc_desc(kt + (j >> 2) * (kPgTile * 128) + (j & 3) * 32, 16, 1024, 2), kIdS, j > 0);
         tc_commit(s_ready + 8 * g);
         if (last) tc_commit(empty + 8 * st);
-        if (end) tc_commit(q_free + 8 * g);   // the piece's last
       }
       __syncwarp();
     };
@@ -251,7 +228,7 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
         ok = warp_wait_or_fail(q_ready + 8 * g, pieces[g]++ & 1, fail);
         if (!ok) break;
         tc_fence_after();
-        scores(n, g, g + 1 == gs, cur.n == 1);
+        scores(n, g, g + 1 == gs);
       }
 #pragma unroll 1
       for (int i = 0; i < cur.n && ok; ++i, ++n) {
@@ -280,7 +257,7 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
           if (!ok) break;
           ++mine[g];
           // The next S overwrites this P: products that one thread issues run in order.
-          if (more) scores(n + 1, g, g + 1 == gs, i + 2 == cur.n);
+          if (more) scores(n + 1, g, g + 1 == gs);
         }
         if (ok && elect_one()) tc_commit(empty + 8 * st);
         __syncwarp();
@@ -294,7 +271,32 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
     const uint32_t t_s = t_lane + g * 128, t_o = t_lane + 256 + g * 128;
     uint32_t* flags = s_row + (g * 128 + row) * (D / 16);
     uint32_t mine = 0, pieces = 0;   // tiles and pieces of this half
-    if (place->pos < hi && tid == 0) a.first[blockIdx.x] = place->item(a);
+    // q's rows of a piece, D / 8 threads a row: on their way to their place, and there.
+    auto q_start = [&](const PagedCursor& c) {
+      constexpr int kLpr = D / 8;
+      const int ch = row % kLpr;
+      const uint8_t* q = a.q + c.b * a.sqb + static_cast<int64_t>(c.h) * a.G * a.sqh + ch * 16;
+      const uint32_t qt = smem0 + L::kOffQ + g * L::kTileBytes;
+      const int first = c.block * kPgRowBlock + g * 128;
+#pragma unroll 2
+      for (int r = row / kLpr; r < 128; r += 128 / kLpr) {
+        const int Rg = first + r, node = paged_node(a, Rg);
+        const bool there = Rg < rows_total && node < c.rq.n;
+        copy16(qt + block_off(128, r, ch), there ? q + node * a.sqn + (Rg - node * a.G) * a.sqh : a.q, there);
+      }
+    };
+    auto q_end = [&] {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      fence_async_smem();
+      mbar_arrive(q_ready + 8 * g);
+    };
+    if (place->pos < hi) {
+      if (tid == 0) a.first[blockIdx.x] = place->item(a);
+      if (g < halves(place->block)) {
+        q_start(*place);
+        q_end();
+      }
+    }
     uint32_t count = 0;   // pieces
     // A wait that gives up ends no loop here: these warps meet at barriers, so all
     // run on to the end (every later wait then returns at once), without meaning:
@@ -484,7 +486,10 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
       }
       n += cur.n;
       // ---- the piece's rows, under whose last products the cursor moves on
+      const PagedCursor& next = place[~count & 1];
       next_piece(a, &cur, place + (~count & 1), hi);
+      const bool bring = next.pos < hi && g < halves(next.block);
+      if (bring) q_start(next);   // the half's scores of this piece are done
       if (active) {
         wait_or_fail(o_done + 8 * g, pieces++ & 1, fail);
         tc_fence_after();
@@ -530,6 +535,7 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
           a.lse[to] = l == 0.f ? -INFINITY : (m_run + log2f(l)) * kLn2;
         tc_fence_before();
       }
+      if (bring) q_end();
       if (a.parents) named_barrier_sync(4, kPgRowSoft);   // the tree's place is free for the next piece
     }
   }
