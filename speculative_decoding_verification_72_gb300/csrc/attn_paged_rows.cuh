@@ -80,6 +80,24 @@ __device__ __noinline__ void note_seen(const uint32_t* from, uint32_t s0, uint32
       for (int w = 0; w < D / 16; ++w) to[w] |= from[t * (D / 16) + w];
 }
 
+// A warp's rows of O (TMEM) with what was taken out of V put back.
+template <int D>
+__device__ __noinline__ void put_back_rows(uint32_t t_o, const uint32_t* flags) {
+#pragma unroll 1
+  for (int j = 0; j < D; j += 16) {
+    uint32_t o[16];
+    __syncwarp();
+    tmem_ld16(t_o + j, o);
+    const uint32_t up = flags[j / 32] >> (j & 31), down = flags[D / 32 + j / 32] >> (j & 31);
+    tmem_ld_wait();
+    tmem_use(o);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(put_back(__uint_as_float(o[e]), up >> e & 1, down >> e & 1));
+    tmem_st16(t_o + j, o);
+  }
+  tmem_st_wait();
+}
+
 // 16 bytes from global to shared memory, or zeros.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
@@ -96,7 +114,7 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
   __shared__ AttnLine s_line;
   __shared__ int32_t s_warp[kPgRowThreads / 32];
   __shared__ PagedCursor s_cur[kPgRowThreads / 32][2];
-  __shared__ __align__(8) uint64_t s_bar[2 * kSt + kDepth + 12];
+  __shared__ __align__(8) uint64_t s_bar[2 * kSt + kDepth + 10];
   __shared__ uint32_t s_tmem, s_fail, s_there[16], s_odd[kDepth];   // s_odd: whether values were taken out of a tile's V
   const uint32_t smem0 = (smem_u32(raw) + 1023u) & ~1023u;
   uint8_t* smem = raw + (smem0 - smem_u32(raw));
@@ -108,7 +126,7 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t full = smem_u32(s_bar), empty = full + 8 * kSt, v_fit = empty + 8 * kSt, s_ready = v_fit + 8 * kDepth;
-  const uint32_t p_ready = s_ready + 16, first_done = p_ready + 32, o_done = first_done + 16, q_ready = o_done + 16;
+  const uint32_t p_ready = s_ready + 16, o_done = p_ready + 32, q_ready = o_done + 16;
   if (tid == 0) {
     s_fail = 0;
 #pragma unroll 1
@@ -123,7 +141,6 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
       mbar_init(s_ready + 8 * i, 1);
       mbar_init(p_ready + 16 * i, 128);       // tokens 0 .. 63 of a tile, of half i
       mbar_init(p_ready + 16 * i + 8, 128);   // tokens 64 .. 127
-      mbar_init(first_done + 8 * i, 1);
       mbar_init(o_done + 8 * i, 1);
       mbar_init(q_ready + 8 * i, 128);
     }
@@ -202,16 +219,21 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
   } else if (warp == 9) {
     // ------------------------------------------------------------------ MMA
     constexpr uint32_t kIdS = tc_idesc(T::kMma, false, false, 128, 128), kIdO = tc_idesc(T::kMma, false, true, 128, D);
+    // Operands' descriptors: a step of 16 along K is 32 bytes of a row, or 16 rows of V.
+    const uint64_t d_q = tc_desc(smem0 + L::kOffQ, 16, 1024, 2), d_k = tc_desc(smem0, 16, 1024, 2);
+    const uint64_t d_v = tc_desc(smem0, kPgTile * 128, 1024, 2);
+    auto at = [](uint64_t d, uint32_t bytes) { return d + (bytes >> 4); };
     bool ok = true;
     uint32_t pieces[2] = {0, 0}, mine[2] = {0, 0};   // by half; mine: tiles
     auto scores = [&](uint32_t m, int g, bool last) {
       const uint32_t st = 2 * m % kSt;
-      const uint32_t qt = smem0 + L::kOffQ + g * L::kTileBytes, kt = smem0 + st * L::kTileBytes;
       if (elect_one()) {
+        const uint64_t q = at(d_q, g * L::kTileBytes), k = at(d_k, st * L::kTileBytes);
 #pragma unroll
-        for (int j = 0; j < D / 16; ++j)
-          tc_mma_f16(tmem + g * 128, tc_desc(qt + (j >> 2) * (kPgTile * 128) + (j & 3) * 32, 16, 1024, 2),
-                     tc_desc(kt + (j >> 2) * (kPgTile * 128) + (j & 3) * 32, 16, 1024, 2), kIdS, j > 0);
+        for (int j = 0; j < D / 16; ++j) {
+          const uint32_t off = (j >> 2) * (kPgTile * 128) + (j & 3) * 32;
+          tc_mma_f16(tmem + g * 128, at(q, off), at(k, off), kIdS, j > 0);
+        }
         tc_commit(s_ready + 8 * g);
         if (last) tc_commit(empty + 8 * st);
       }
@@ -232,7 +254,8 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
       }
 #pragma unroll 1
       for (int i = 0; i < cur.n && ok; ++i, ++n) {
-        const uint32_t st = (2 * n + 1) % kSt, vt = smem0 + st * L::kTileBytes;
+        const uint32_t st = (2 * n + 1) % kSt;
+        const uint64_t v = at(d_v, st * L::kTileBytes);
         const bool more = i + 1 < cur.n;
         ok = warp_wait_or_fail(v_fit + 8 * (n % kDepth), (n / kDepth) & 1, fail);
         if (more) k_there(n + 1);
@@ -247,9 +270,7 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
             if (elect_one()) {
 #pragma unroll
               for (int j = 4 * u; j < 4 * u + 4; ++j)   // P's halves lie where those of S did
-                tc_mma_f16_ts(tmem + 256 + g * 128, tmem + g * 128 + (j & 3) * 8 + u * 64, tc_desc(vt + 2048 * j, kPgTile * 128, 1024, 2),
-                              kIdO, i > 0 || j > 0);
-              if (u == 0) tc_commit(first_done + 8 * g);
+                tc_mma_f16_ts(tmem + 256 + g * 128, tmem + g * 128 + (j & 3) * 8 + u * 64, at(v, 2048 * j), kIdO, i > 0 || j > 0);
               if (u == 1 && !more) tc_commit(o_done + 8 * g);
             }
             __syncwarp();
@@ -337,7 +358,7 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
       const uint32_t all_pages = (1u << (kPgTile >> a.c.page_shift)) - 1u;
       const float c = kVar ? 1.f : a.coef;   // of what the second reading finds
       float m_run = 0.f, l = 0.f;            // m_run means something once the row has seen a slot
-      bool seen = false;
+      bool seen = false, any_odd = false;
 #pragma unroll 1
       for (int i = 0; i < tiles; ++i, ++mine) {
         const uint32_t tile = n + i;
@@ -474,8 +495,10 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
           tmem_st16(t_s + u * 64 + 16, x + 16);
           if (special && u == 1) {   // what was taken out of V, before the tile is given up
             wait_or_fail(v_fit + 8 * (tile % kDepth), (tile / kDepth) & 1, fail);
-            if (const_cast<volatile uint32_t*>(s_odd)[tile % kDepth])
+            if (const_cast<volatile uint32_t*>(s_odd)[tile % kDepth]) {
+              any_odd = true;
               note_seen<D>(s_tok + (tile % kDepth) * 128 * (D / 16), see[0], see[1], see[2], see[3], flags);
+            }
           }
           tmem_st_wait();
           tc_fence_before();
@@ -493,6 +516,7 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
       if (active) {
         wait_or_fail(o_done + 8 * g, pieces++ & 1, fail);
         tc_fence_after();
+        if (any_odd) put_back_rows<D>(t_o, flags);
         if (*fail) l = __int_as_float(0x7fc00000);
         if (node < 0) l = 0.f;
         const float f = l == 0.f ? 0.f : cur.whole ? 1.f / l : 1.f;
@@ -503,16 +527,10 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
         for (int j = 0; j < D; j += 32) {
           uint32_t o[32];
           tmem_ld32(t_o + j, o);
-          const uint32_t up = flags[j / 32], down = flags[D / 32 + j / 32];
           tmem_ld_wait();
           tmem_use(o);
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(f == 0.f ? 0.f : __uint_as_float(o[e]) * f);
-          if (__any_sync(0xffffffffu, (up | down) != 0 && f != 0.f)) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (f != 0.f) o[e] = __float_as_uint(put_back(__uint_as_float(o[e]), up >> e & 1, down >> e & 1));
-          }
           if (cur.whole) {
             if (Rg < rows_total) {
 #pragma unroll
