@@ -61,6 +61,10 @@ __device__ __forceinline__ void tc_mma_f16(uint32_t d, uint64_t a, uint64_t b, u
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld4(uint32_t addr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+
 // Box of the cache's 4-D map: 64 elements of the tokens of a page, for one head.
 __device__ __forceinline__ void tma_load_page(uint32_t dst, const void* map, int x, int head, int page, uint32_t bar) {
   asm volatile(
@@ -213,6 +217,11 @@ __global__ void __launch_bounds__(PgColLayout<D, MT>::kThreads, 1)
   } else if (warp == 4 * MT + 1) {
     // ------------------------------------------------------------------ MMA
     constexpr uint32_t kIdS = tc_idesc(T::kMma, false, false, 128, R), kIdO = tc_idesc(T::kMma, true, true, 128, L::kNo);
+    // Operands' descriptors: a step of 16 along K is 32 bytes of a row, or 16 rows of V and P. 64-wide heads are half of the
+    // product's 128 rows; a block stride of 0 gives the other half the same rows.
+    const uint64_t d_q = tc_desc(smem0 + L::kOffQ, 16, 1024, 2), d_k = tc_desc(smem0, 16, 1024, 2);
+    const uint64_t d_v = tc_desc(smem0, D == 128 ? kPgTile * 128 : 0, 1024, 2), d_p = tc_desc(smem0 + L::kOffP, 0, 1024, 2);
+    auto at = [](uint64_t d, uint32_t bytes) { return d + (bytes >> 4); };
     bool ok = true;
     uint32_t pieces = 0;
     auto scores = [&](uint32_t m) {
@@ -221,12 +230,11 @@ __global__ void __launch_bounds__(PgColLayout<D, MT>::kThreads, 1)
       if (m >= 2) ok = ok && warp_wait_or_fail(s_free + 8 * sb, ((m >> 1) - 1) & 1, fail);
       if (!ok) return;
       tc_fence_after();
-      const uint32_t kt = smem0 + st * L::kTileBytes;
       if (elect_one()) {
+        const uint64_t kt = at(d_k, st * L::kTileBytes);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-          tc_mma_f16(tmem + sb * R, tc_desc(kt + (k >> 2) * (kPgTile * 128) + (k & 3) * 32, 16, 1024, 2),
-                     tc_desc(smem0 + L::kOffQ + (k >> 2) * (R * 128) + (k & 3) * 32, 16, 1024, 2), kIdS, k > 0);
+          tc_mma_f16(tmem + sb * R, at(kt, (k >> 2) * (kPgTile * 128) + (k & 3) * 32), at(d_q, (k >> 2) * (R * 128) + (k & 3) * 32), kIdS, k > 0);
         tc_commit(empty + 8 * st);
         tc_commit(s_ready + 8 * sb);
       }
@@ -244,13 +252,10 @@ __global__ void __launch_bounds__(PgColLayout<D, MT>::kThreads, 1)
         ok = ok && warp_wait_or_fail(full + 8 * st, (s / kSt) & 1, fail) && warp_wait_or_fail(p_ready, n & 1, fail);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t vt = smem0 + st * L::kTileBytes;
         if (elect_one()) {
-          // 64-wide heads are half of the product's 128 rows; a block stride of 0 gives the other half the same rows.
+          const uint64_t vt = at(d_v, st * L::kTileBytes);
 #pragma unroll
-          for (int k = 0; k < kPgTile / 16; ++k)
-            tc_mma_f16(tmem + 2 * R, tc_desc(vt + 2048 * k, D == 128 ? kPgTile * 128 : 0, 1024, 2),
-                       tc_desc(smem0 + L::kOffP + 2048 * k, 0, 1024, 2), kIdO, i > 0 || k > 0);
+          for (int k = 0; k < kPgTile / 16; ++k) tc_mma_f16(tmem + 2 * R, at(vt, 2048 * k), at(d_p, 2048 * k), kIdO, i > 0 || k > 0);
           tc_commit(empty + 8 * st);
           tc_commit(p_free);
         }
@@ -511,27 +516,31 @@ __global__ void __launch_bounds__(PgColLayout<D, MT>::kThreads, 1)
       named_barrier_sync(bar, 128);
       tc_fence_after();
       if (row < D) {
-        uint32_t w[2][16];
+#pragma unroll 1
+        for (int j = 0; j < 16 && s_out[r00 + j].w; j += 4) {
+          uint32_t w[2][4];
+          tmem_ld4(t_o + j, w[0]);
+          tmem_ld4(t_o + R + j, w[1]);
+          tmem_ld_wait();
+          tmem_use(w[0]);
+          tmem_use(w[1]);
 #pragma unroll
-        for (int t = 0; t < 2; ++t) tmem_ld16(t_o + t * R, w[t]);
-        tmem_ld_wait();
-#pragma unroll
-        for (int t = 0; t < 2; ++t) tmem_use(w[t]);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const int r = r00 + j;
-          const int4 to = s_out[r];
-          if (!to.w) break;
-          const float f = __int_as_float(to.z);
-          float o = f == 0.f ? 0.f : (__uint_as_float(w[0][j]) + __uint_as_float(w[1][j])) * f;
-          if (any_inf && f != 0.f)
-            o = put_back(o, s_inf[r * (D / 16) + (row >> 5)] >> (row & 31) & 1, s_inf[r * (D / 16) + D / 32 + (row >> 5)] >> (row & 31) & 1);
-          if (cur.whole) {
-            const int64_t at = static_cast<uint32_t>(to.x) | static_cast<int64_t>(to.y) << 32;
-            static_cast<uint16_t*>(a.out)[at * D + row] = static_cast<uint16_t>(T::pack2(o, 0.f));
-          } else {
-            part[r * D + row] = o;
+          for (int k = 0; k < 4; ++k) {
+            const int r = r00 + j + k;
+            const int4 to = s_out[r];
+            if (!to.w) break;
+            const float f = __int_as_float(to.z);
+            float o = f == 0.f ? 0.f : (__uint_as_float(w[0][k]) + __uint_as_float(w[1][k])) * f;
+            if (any_inf && f != 0.f)
+              o = put_back(o, s_inf[r * (D / 16) + (row >> 5)] >> (row & 31) & 1, s_inf[r * (D / 16) + D / 32 + (row >> 5)] >> (row & 31) & 1);
+            if (cur.whole) {
+              const int64_t at = static_cast<uint32_t>(to.x) | static_cast<int64_t>(to.y) << 32;
+              static_cast<uint16_t*>(a.out)[at * D + row] = static_cast<uint16_t>(T::pack2(o, 0.f));
+            } else {
+              part[r * D + row] = o;
+            }
           }
+          __syncwarp();
         }
       }
       tc_fence_before();
