@@ -11,6 +11,9 @@
 // follow each other and one half's softmax runs under the other's products; one
 // CTA an SM.
 //
+// Where a kv head has no more than 128 rows, both halves take them, and the tiles
+// by turns; at a piece's end one half's O, maxima and sums go to the other.
+//
 // A thread has one row, so maximum, exponentials and sum are its own. It reads its
 // scores twice, for the maximum and for the exponentials, which it writes over
 // what it has read; P of the first 64 tokens is multiplied while those of the
@@ -167,8 +170,9 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
   uint32_t n = 0;
   volatile uint32_t* fail = &s_fail;
   const int rows_total = a.N * a.G;
-  // Halves of a block that have rows.
-  auto halves = [&](int block) { return rows_total - block * kPgRowBlock > 128 ? 2 : 1; };
+  // Halves of a block that have rows; split: each has all of them, and every second tile.
+  const bool split = a.R == 128;
+  auto halves = [&](int block) { return split || rows_total - block * kPgRowBlock > 128 ? 2 : 1; };
 
   if (warp == 8) {
     paged_load<D, kSt>(a, &k_map, &v_map, &cur, hi, smem0, full, empty, s_there, fail);
@@ -242,26 +246,29 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
     auto k_there = [&](uint32_t m) { ok = ok && warp_wait_or_fail(full + 8 * (2 * m % kSt), (2 * m / kSt) & 1, fail); };
 #pragma unroll 1
     for (; ok && cur.pos < hi; next_piece(a, &cur, &cur, hi)) {
-      const int gs = halves(cur.block);
-      k_there(n);
+      const int gs = halves(cur.block), tiles = cur.n;
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         if (g == gs || !ok) break;
-        ok = warp_wait_or_fail(q_ready + 8 * g, pieces[g]++ & 1, fail);
+        const int first = split ? g : 0;   // the half's first tile
+        if (g == 0 || (split && tiles > 1)) k_there(n + first);
+        ok = ok && warp_wait_or_fail(q_ready + 8 * g, pieces[g]++ & 1, fail);
         if (!ok) break;
         tc_fence_after();
-        scores(n, g, g + 1 == gs);
+        if (first < tiles) scores(n + first, g, split || g + 1 == gs);
       }
+      const int step = split ? 2 : 1;
 #pragma unroll 1
-      for (int i = 0; i < cur.n && ok; ++i, ++n) {
+      for (int i = 0; i < tiles && ok; ++i, ++n) {
         const uint32_t st = (2 * n + 1) % kSt;
         const uint64_t v = at(d_v, st * L::kTileBytes);
-        const bool more = i + 1 < cur.n;
+        const bool more = i + step < tiles;
         ok = warp_wait_or_fail(v_fit + 8 * (n % kDepth), (n / kDepth) & 1, fail);
-        if (more) k_there(n + 1);
+        if (more) k_there(n + step);
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
           if (g == gs || !ok) break;
+          if (split && g != (i & 1)) continue;
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             ok = ok && warp_wait_or_fail(p_ready + 16 * g + 8 * u, mine[g] & 1, fail);
@@ -270,7 +277,7 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
             if (elect_one()) {
 #pragma unroll
               for (int j = 4 * u; j < 4 * u + 4; ++j)   // P's halves lie where those of S did
-                tc_mma_f16_ts(tmem + 256 + g * 128, tmem + g * 128 + (j & 3) * 8 + u * 64, at(v, 2048 * j), kIdO, i > 0 || j > 0);
+                tc_mma_f16_ts(tmem + 256 + g * 128, tmem + g * 128 + (j & 3) * 8 + u * 64, at(v, 2048 * j), kIdO, i >= step || j > 0);
               if (u == 1 && !more) tc_commit(o_done + 8 * g);
             }
             __syncwarp();
@@ -278,7 +285,7 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
           if (!ok) break;
           ++mine[g];
           // The next S overwrites this P: products that one thread issues run in order.
-          if (more) scores(n + 1, g, g + 1 == gs);
+          if (more) scores(n + step, g, split || g + 1 == gs);
         }
         if (ok && elect_one()) tc_commit(empty + 8 * st);
         __syncwarp();
@@ -298,7 +305,7 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
       const int ch = row % kLpr;
       const uint8_t* q = a.q + c.b * a.sqb + static_cast<int64_t>(c.h) * a.G * a.sqh + ch * 16;
       const uint32_t qt = smem0 + L::kOffQ + g * L::kTileBytes;
-      const int first = c.block * kPgRowBlock + g * 128;
+      const int first = split ? 0 : c.block * kPgRowBlock + g * 128;
 #pragma unroll 2
       for (int r = row / kLpr; r < 128; r += 128 / kLpr) {
         const int Rg = first + r, node = paged_node(a, Rg);
@@ -328,7 +335,7 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
       const PagedReq& rq = cur.rq;
       const int gs = halves(cur.block), soft = 128 * gs;
       const bool active = g < gs;
-      const int row0 = cur.block * kPgRowBlock + g * 128;
+      const int row0 = split ? 0 : cur.block * kPgRowBlock + g * 128;
       // ---- the thread's row, the request's tree
       const int Rg = row0 + row, at = paged_node(a, Rg);
       const int node = Rg < rows_total && at < rq.n ? at : -1;
@@ -360,7 +367,7 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
       float m_run = 0.f, l = 0.f;            // m_run means something once the row has seen a slot
       bool seen = false, any_odd = false;
 #pragma unroll 1
-      for (int i = 0; i < tiles; ++i, ++mine) {
+      for (int i = split ? g : 0; i < tiles; i += split ? 2 : 1, ++mine) {
         const uint32_t tile = n + i;
         const int tok0 = (t0 + i) * kPgTile;
         wait_or_fail(s_ready + 8 * g, mine & 1, fail);   // and every product before this S is done
@@ -459,7 +466,7 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
           if (raise) m_run += top - kPgLift<T>;
           seen = seen || raise;
           l *= f;
-          if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+          if (i >= (split ? 2 : 1) && __any_sync(0xffffffffu, f != 1.f)) {   // O holds something
 #pragma unroll 1
             for (int j = 0; j < D; j += 16) {
               uint32_t o[16];
@@ -512,25 +519,58 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
       const PagedCursor& next = place[~count & 1];
       next_piece(a, &cur, place + (~count & 1), hi);
       const bool bring = next.pos < hi && g < halves(next.block);
-      if (bring) q_start(next);   // the half's scores of this piece are done
+      if (bring && !split) q_start(next);   // the half's scores of this piece are done
       if (active) {
-        wait_or_fail(o_done + 8 * g, pieces++ & 1, fail);
+        if (!split || g < tiles) wait_or_fail(o_done + 8 * g, pieces++ & 1, fail);
         tc_fence_after();
         if (any_odd) put_back_rows<D>(t_o, flags);
+        float f0 = 1.f, f1 = 0.f;   // of this half's O, and of the other's
+        float* other = reinterpret_cast<float*>(smem + L::kOffQ) + row;   // [D][128], where q has been
+        if (split) {
+          if (g == 1) {
+            reinterpret_cast<float2*>(s_at)[row] = make_float2(m_run, l);
+#pragma unroll 1
+            for (int j = 0; j < (g < tiles ? D : 0); j += 16) {   // without tiles it has no O, and q is in use
+              uint32_t o[16];
+              tmem_ld16(t_o + j, o);
+              tmem_ld_wait();
+              tmem_use(o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) other[(j + e) * 128] = __uint_as_float(o[e]);
+            }
+            tc_fence_before();
+          }
+          named_barrier_sync(4, kPgRowSoft);
+          if (g == 0) {
+            const float2 ml = reinterpret_cast<const float2*>(s_at)[row];
+            const float m0 = l == 0.f ? -INFINITY : m_run, m1 = ml.y == 0.f ? -INFINITY : ml.x, m = fmaxf(m0, m1);
+            f0 = m0 == -INFINITY ? 0.f : ex2(m0 - m);
+            f1 = m1 == -INFINITY ? 0.f : ex2(m1 - m);
+            if (m != -INFINITY) m_run = m;
+            l = (f0 == 0.f ? 0.f : l * f0) + (f1 == 0.f ? 0.f : ml.y * f1);
+          }
+        }
         if (*fail) l = __int_as_float(0x7fc00000);
         if (node < 0) l = 0.f;
         const float f = l == 0.f ? 0.f : cur.whole ? 1.f / l : 1.f;
-        float* part = a.part + static_cast<int64_t>(2 * blockIdx.x + (count == 0 ? 0 : 1)) * kPgRowBlock * (D + 2) + g * 128 + row;
+        f0 = f == 0.f ? 0.f : f0 * f;
+        f1 = f == 0.f ? 0.f : f1 * f;
+        const int lane_of = split ? row : g * 128 + row;
+        float* part = a.part + static_cast<int64_t>(2 * blockIdx.x + (count == 0 ? 0 : 1)) * a.R * (D + 2) + lane_of;
         const int64_t to = (static_cast<int64_t>(cur.b) * a.N + at) * a.Hq + cur.h * a.G + (Rg - at * a.G);
         uint8_t* out = static_cast<uint8_t*>(a.out) + to * D * 2;
+        const bool writes = !split || g == 0;
 #pragma unroll 1
-        for (int j = 0; j < D; j += 32) {
+        for (int j = 0; j < (writes ? D : 0); j += 32) {
           uint32_t o[32];
           tmem_ld32(t_o + j, o);
           tmem_ld_wait();
           tmem_use(o);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(f == 0.f ? 0.f : __uint_as_float(o[e]) * f);
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(f0 == 0.f ? 0.f : __uint_as_float(o[e]) * f0);
+          if (f1 != 0.f)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(fmaf(other[(j + e) * 128], f1, __uint_as_float(o[e])));
           if (cur.whole) {
             if (Rg < rows_total) {
 #pragma unroll
@@ -543,18 +583,19 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
             }
           } else {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) part[(j + e) * kPgRowBlock] = __uint_as_float(o[e]);
+            for (int e = 0; e < 32; ++e) part[(j + e) * a.R] = __uint_as_float(o[e]);
           }
           __syncwarp();
         }
-        if (!cur.whole)
-          *reinterpret_cast<float2*>(part + kPgRowBlock * D + g * 128 + row) = make_float2(l == 0.f ? -INFINITY : m_run, l);
-        else if (a.lse && Rg < rows_total)
+        if (writes && !cur.whole)
+          *reinterpret_cast<float2*>(part + a.R * D + lane_of) = make_float2(l == 0.f ? -INFINITY : m_run, l);
+        else if (writes && a.lse && Rg < rows_total)
           a.lse[to] = l == 0.f ? -INFINITY : (m_run + log2f(l)) * kLn2;
         tc_fence_before();
       }
+      if (a.parents || split) named_barrier_sync(4, kPgRowSoft);   // the tree's place and the other half's are free for the next piece
+      if (bring && split) q_start(next);
       if (bring) q_end();
-      if (a.parents) named_barrier_sync(4, kPgRowSoft);   // the tree's place is free for the next piece
     }
   }
   __syncthreads();

@@ -66,8 +66,9 @@ bool page_map(const sv_paged_cache& c, const PagedView& v, int kv, CUtensorMap* 
 // --------------------------------------------------------------- attention
 
 // Rows of a block: all of a kv head's as columns where they are at most 32 (in
-// one or two groups of 16), else blocks of 256 lanes.
-int paged_block(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : kPgRowBlock; }
+// one or two groups of 16), as 128 lanes that share the tiles between their two
+// copies where they are at most 128, else blocks of 256 lanes.
+int paged_block(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 ? 128 : kPgRowBlock; }
 
 // What an item's beginning and end cost, in tiles.
 constexpr int kPagedColExtra = 1, kPagedRowExtra = 4;
@@ -230,9 +231,9 @@ sv_status spec_attention(const sv_rows* q, int32_t dtype, const sv_paged_cache* 
   a.plan = reinterpret_cast<int32_t*>(ws + p.off_plan);
   const int64_t items = B * p.RB * cache->Hkv;
   const int64_t tiles = (static_cast<int64_t>(cache->max_pages) * cache->page_size + kPgTile - 1) / kPgTile;
-  a.extra = p.block == kPgRowBlock ? kPagedRowExtra : kPagedColExtra;
+  a.extra = p.block >= 128 ? kPagedRowExtra : kPagedColExtra;
   if (items > INT32_MAX / (tiles + a.extra) || static_cast<int64_t>(cache->max_pages) * cache->page_size + N > INT32_MAX - 255) return SV_ERR_INVALID_ARG;
-  a.grid = static_cast<int32_t>(std::min<int64_t>({sm_count(), kPagedGridMost, items * tiles}));
+  a.grid = static_cast<int32_t>(std::min<int64_t>({sm_count(), kPagedGridMost, items * (tiles + a.extra)}));
   CUtensorMap k, v;
   if (!page_map(*cache, a.c, 0, &k) || !page_map(*cache, a.c, 1, &v)) return SV_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
