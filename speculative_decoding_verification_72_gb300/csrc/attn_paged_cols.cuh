@@ -219,6 +219,7 @@ __global__ void __launch_bounds__(PgColLayout<D, MT>::kThreads, 1)
     constexpr uint32_t kIdS = tc_idesc(T::kMma, false, false, 128, R), kIdO = tc_idesc(T::kMma, true, true, 128, L::kNo);
     // Operands' descriptors: a step of 16 along K is 32 bytes of a row, or 16 rows of V and P. 64-wide heads are half of the
     // product's 128 rows; a block stride of 0 gives the other half the same rows.
+    const uint32_t tmem = uniform(s_tmem), smem0 = uniform(smem_u32(smem));
     const uint64_t d_q = tc_desc(smem0 + L::kOffQ, 16, 1024, 2), d_k = tc_desc(smem0, 16, 1024, 2);
     const uint64_t d_v = tc_desc(smem0, D == 128 ? kPgTile * 128 : 0, 1024, 2), d_p = tc_desc(smem0 + L::kOffP, 0, 1024, 2);
     auto at = [](uint64_t d, uint32_t bytes) { return d + (bytes >> 4); };
@@ -244,10 +245,11 @@ __global__ void __launch_bounds__(PgColLayout<D, MT>::kThreads, 1)
     for (; ok && cur.pos < hi; next_piece(a, place, place, hi)) {
       ok = warp_wait_or_fail(q_ready, pieces++ & 1, fail);
       if (!ok) break;
+      const int tiles = uniform(cur.n);
       scores(n);
 #pragma unroll 1
-      for (int i = 0; i < cur.n && ok; ++i, ++n) {
-        if (i + 1 < cur.n) scores(n + 1);
+      for (int i = 0; i < tiles && ok; ++i, ++n) {
+        if (i + 1 < tiles) scores(n + 1);
         const uint32_t s = 2 * n + 1, st = s % kSt;
         ok = ok && warp_wait_or_fail(full + 8 * st, (s / kSt) & 1, fail) && warp_wait_or_fail(p_ready, n & 1, fail);
         if (!ok) break;

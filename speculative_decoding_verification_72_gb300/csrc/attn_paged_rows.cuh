@@ -229,19 +229,17 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
     auto at = [](uint64_t d, uint32_t bytes) { return d + (bytes >> 4); };
     bool ok = true;
     uint32_t pieces[2] = {0, 0}, mine[2] = {0, 0};   // by half; mine: tiles
+    // In the elected thread: S of tile m.
     auto scores = [&](uint32_t m, int g, bool last) {
       const uint32_t st = 2 * m % kSt;
-      if (elect_one()) {
-        const uint64_t q = at(d_q, g * L::kTileBytes), k = at(d_k, st * L::kTileBytes);
+      const uint64_t q = at(d_q, g * L::kTileBytes), k = at(d_k, st * L::kTileBytes);
 #pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-          const uint32_t off = (j >> 2) * (kPgTile * 128) + (j & 3) * 32;
-          tc_mma_f16(tmem + g * 128, at(q, off), at(k, off), kIdS, j > 0);
-        }
-        tc_commit(s_ready + 8 * g);
-        if (last) tc_commit(empty + 8 * st);
+      for (int j = 0; j < D / 16; ++j) {
+        const uint32_t off = (j >> 2) * (kPgTile * 128) + (j & 3) * 32;
+        tc_mma_f16(tmem + g * 128, at(q, off), at(k, off), kIdS, j > 0);
       }
-      __syncwarp();
+      tc_commit(s_ready + 8 * g);
+      if (last) tc_commit(empty + 8 * st);
     };
     auto k_there = [&](uint32_t m) { ok = ok && warp_wait_or_fail(full + 8 * (2 * m % kSt), (2 * m / kSt) & 1, fail); };
 #pragma unroll 1
@@ -255,7 +253,8 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
         ok = ok && warp_wait_or_fail(q_ready + 8 * g, pieces[g]++ & 1, fail);
         if (!ok) break;
         tc_fence_after();
-        if (first < tiles) scores(n + first, g, split || g + 1 == gs);
+        if (first < tiles && elect_one()) scores(n + first, g, split || g + 1 == gs);
+        __syncwarp();
       }
       const int step = split ? 2 : 1;
 #pragma unroll 1
@@ -264,31 +263,38 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
         const uint64_t v = at(d_v, st * L::kTileBytes);
         const bool more = i + step < tiles;
         ok = warp_wait_or_fail(v_fit + 8 * (n % kDepth), (n / kDepth) & 1, fail);
-        if (more) k_there(n + step);
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
           if (g == gs || !ok) break;
           if (split && g != (i & 1)) continue;
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            ok = ok && warp_wait_or_fail(p_ready + 16 * g + 8 * u, mine[g] & 1, fail);
-            if (!ok) break;
-            tc_fence_after();
-            if (elect_one()) {
-#pragma unroll
-              for (int j = 4 * u; j < 4 * u + 4; ++j)   // P's halves lie where those of S did
-                tc_mma_f16_ts(tmem + 256 + g * 128, tmem + g * 128 + (j & 3) * 8 + u * 64, at(v, 2048 * j), kIdO, i >= step || j > 0);
-              if (u == 1 && !more) tc_commit(o_done + 8 * g);
-            }
-            __syncwarp();
-          }
+          const bool last = split || g + 1 == gs;
+          ok = warp_wait_or_fail(p_ready + 16 * g, mine[g] & 1, fail);
           if (!ok) break;
+          tc_fence_after();
+          // P's halves lie where those of S did.
+          if (elect_one())
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              tc_mma_f16_ts(tmem + 256 + g * 128, tmem + g * 128 + j * 8, at(v, 2048 * j), kIdO, i >= step || j > 0);
+          __syncwarp();
+          if (more && (g == 0 || split)) k_there(n + step);   // under these products
+          ok = ok && warp_wait_or_fail(p_ready + 16 * g + 8, mine[g] & 1, fail);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+#pragma unroll
+            for (int j = 4; j < 8; ++j)
+              tc_mma_f16_ts(tmem + 256 + g * 128, tmem + g * 128 + 64 + (j - 4) * 8, at(v, 2048 * j), kIdO, true);
+            if (last) tc_commit(empty + 8 * st);
+            // The next S overwrites this P: products that one thread issues run in order.
+            if (more)
+              scores(n + step, g, last);
+            else
+              tc_commit(o_done + 8 * g);
+          }
+          __syncwarp();
           ++mine[g];
-          // The next S overwrites this P: products that one thread issues run in order.
-          if (more) scores(n + step, g, split || g + 1 == gs);
         }
-        if (ok && elect_one()) tc_commit(empty + 8 * st);
-        __syncwarp();
       }
     }
   } else if (warp < 8) {

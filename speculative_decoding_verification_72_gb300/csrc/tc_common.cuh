@@ -56,6 +56,10 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// A value that all lanes of a converged warp have, as one that is known to be
+// uniform: what is reckoned from it stays in uniform registers.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_or_sync(0xffffffffu, x); }
+
 // ------------------------------------------------------------------- TMEM
 
 // Warp-collective; cols a power of two >= 32. The address lands at smem word `slot`.
@@ -157,9 +161,27 @@ __device__ __forceinline__ bool wait_or_fail(uint32_t bar, uint32_t parity, vola
   return mbar_try_wait_for(bar, parity, kWaitSleepNs) || wait_or_fail_slow(bar, parity, fail);
 }
 
+// Whether a phase is over, without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred P;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 P, [%1], %2;\n\t"
+      "selp.b32 %0, 1, 0, P;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// wait_or_fail for phases that are mostly over: try_wait answers later than test_wait.
+__device__ __forceinline__ bool ready_or_fail(uint32_t bar, uint32_t parity, volatile uint32_t* fail) {
+  return mbar_test(bar, parity) || wait_or_fail(bar, parity, fail);
+}
+
 // The same for a whole warp, which goes on converged and of one mind.
 __device__ __forceinline__ bool warp_wait_or_fail(uint32_t bar, uint32_t parity, volatile uint32_t* fail) {
-  return __all_sync(0xffffffffu, wait_or_fail(bar, parity, fail));
+  return __all_sync(0xffffffffu, ready_or_fail(bar, parity, fail));
 }
 
 }  // namespace sv
