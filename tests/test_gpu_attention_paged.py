@@ -307,3 +307,64 @@ def test_no_requests():
     c = sv.paged_cache(2, 2, 16, 64)
     e = torch.empty((0, 3, 4, 64), dtype=BF, device=DEV)
     assert sv.spec_attention(e, c, i32(np.zeros((0, 2))), i32([]))["out"].shape == (0, 3, 4, 64)
+
+
+# ------------------------------------------------------- many pieces, refusals from Python
+
+@pytest.mark.parametrize("B,N,H,G,D,L,dtype", [
+    (40, 75, 3, 4, 128, 300, BF), (30, 150, 2, 2, 64, 500, F16), (70, 12, 4, 4, 64, 700, BF), (90, 9, 3, 5, 128, 260, F16),
+    (200, 1, 8, 4, 128, 200, BF), (150, 5, 8, 5, 64, 300, F16), (3, 1301, 2, 7, 64, 100, BF)])
+def test_many_pieces(B, N, H, G, D, L, dtype):
+    """Every CTA has many items, of blocks with one half and with two, some of them shared with its neighbours."""
+    q, cache, tab = big(B, N, H, G, D, 16, L, dtype, N + L)
+    base = [(L * (7 * b % B)) // B for b in range(B)]
+    r = sv.spec_attention(q, cache, tab, i32(base))
+    assert int(r["status"].max()) == 0
+    check_attention(r, in_64(q, cache, tab, base), dtype, N * G)
+
+
+@pytest.mark.parametrize("N,G", [(2, 4), (12, 4), (70, 4)])
+def test_nan_keys_under_a_cap(N, G):
+    rng = np.random.default_rng(21)
+    c = host_cache(rng, 30, 16, 1, 64, BF)
+    tab = table(rng, [200 + N], 16, 30)
+    c["k"][tab[0, 3], 5, 0, 9] = np.nan      # a slot that every row sees
+    r, want = run(rng, [200], N, 1, G, 64, 16, BF, cap=20.0, tab=tab, pages=30, cache=c)
+    assert torch.isnan(r["out"]).all() and torch.isnan(r["lse"]).all()
+
+
+@pytest.mark.parametrize("N,G", [(2, 4), (12, 4), (70, 4)])
+@pytest.mark.parametrize("cap", [1.0, 30.0])
+def test_scores_far_past_the_cap(N, G, cap):
+    run(np.random.default_rng(22), [150, 3], N, 1, G, 64, 16, BF, cap=cap, q_std=300.0)
+
+
+def test_python_refusals():
+    E = sv.SpecVerifyError
+    c = sv.paged_cache(4, 2, 16, 64)
+    q = torch.zeros((2, 3, 4, 64), dtype=BF, device=DEV)
+    tab, base = i32([[0, 1], [2, 3]]), i32([0, 5])
+    ok = sv.spec_attention(q, c, tab, base)
+    for bad in (dict(q=q[..., :32]), dict(q=q[:, :, :3]), dict(q=q.half()), dict(q=q.float()), dict(q=q[0]), dict(q=q.cpu()),
+                dict(page_table=tab[:1]), dict(seq_base=base[:1]), dict(parents=i32([[0]])), dict(n_nodes=i32([1])), dict(window=-1),
+                dict(softcap=-1.0), dict(softcap=float("nan")), dict(slopes=torch.zeros(3, device=DEV)), dict(slopes=torch.zeros(4)),
+                dict(workspace=torch.zeros(8, device=DEV)), dict(out=[]), dict(out={}), dict(cache=(c.k,)), dict(cache=(c.k, c.v[:2])),
+                dict(cache=(c.k, c.v.half())), dict(cache=(c.k.float(), c.v.float())), dict(cache=(c.k[:, :8], c.v[:, :8])),
+                dict(cache=(c.k[..., ::2], c.v[..., ::2])), dict(cache=tuple(t.transpose(1, 3) for t in c)),
+                dict(cache=tuple(t.expand(4, 16, 2, 64)[:, :, :1].expand(4, 16, 2, 64) for t in c))):
+        a = dict(q=q, cache=c, page_table=tab, seq_base=base)
+        a.update(bad)
+        with pytest.raises(E):
+            sv.spec_attention(**a)
+    k = torch.zeros((2, 3, 2, 64), dtype=BF, device=DEV)
+    f = torch.ones(32, device=DEV)
+    for bad in (dict(k_new=k[:, :, :1]), dict(v_new=k[:1]), dict(k_new=k.half()), dict(inv_freq=f.double()), dict(inv_freq=f[:31]),
+                dict(inv_freq=f.repeat(2)), dict(inv_freq=f.cpu()), dict(q=q[:, :2]), dict(q=q.half()), dict(parents=i32([[0]])),
+                dict(n_nodes=i32([1])), dict(page_table=tab[0]), dict(out=dict(out_len=base, status=torch.empty_like(base)))):
+        a = dict(cache=c, k_new=k, v_new=k, page_table=tab, seq_base=base, inv_freq=f)
+        a.update(bad)
+        with pytest.raises(E):
+            sv.spec_kv_append_rope(**a)
+    with pytest.raises(E):
+        sv.spec_attention(torch.zeros((1, 1025, 2, 64), dtype=BF, device=DEV), c, tab[:1], base[:1], parents=torch.zeros((1, 1025), dtype=torch.int32, device=DEV))
+    assert torch.equal(sv.spec_attention(q, c, tab, base)["out"], ok["out"])
