@@ -309,7 +309,8 @@ __global__ void __launch_bounds__(kPgJoinThreads) attn_paged_join_kernel(const P
   float m = -INFINITY, l = 0.f, v[kPer];
 #pragma unroll
   for (int k = 0; k < kPer; ++k) v[k] = 0.f;
-  constexpr int kBatch = D == 128 ? kPgJoinBatch / 2 : kPgJoinBatch;
+  // Blocks of many rows are mostly in two pieces, of few rows in many.
+  constexpr int kBatch = kLanes ? 2 : D == 128 ? kPgJoinBatch / 2 : kPgJoinBatch;
 #pragma unroll 1
   for (int i0 = c0; i0 <= c1; i0 += kBatch) {
     float2 ml[kBatch];
