@@ -145,6 +145,7 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
   __shared__ AttnLine s_line;
   __shared__ int32_t s_warp[kPgRowThreads / 32];
   __shared__ PagedCursor s_cur[kPgRowThreads / 32][2];
+  __shared__ float2 s_ml[128];   // split: maxima and sums of half 1 (its other places are in use until half 0 is done)
   __shared__ __align__(8) uint64_t s_bar[2 * kSt + kDepth + 10];
   __shared__ uint32_t s_tmem, s_fail, s_there[16], s_odd[kDepth];   // s_odd: whether values were taken out of a tile's V
   const uint32_t smem0 = (smem_u32(raw) + 1023u) & ~1023u;
@@ -558,7 +559,7 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
         float* other = reinterpret_cast<float*>(smem + L::kOffQ) + row;   // [D][128], where q has been
         if (split) {
           if (g == 1) {
-            reinterpret_cast<float2*>(s_at)[row] = make_float2(m_run, l);
+            s_ml[row] = make_float2(m_run, l);
 #pragma unroll 1
             for (int j = 0; j < (g < tiles ? D : 0); j += 16) {   // without tiles it has no O, and q is in use
               uint32_t o[16];
@@ -572,7 +573,7 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
           }
           named_barrier_sync(4, kPgRowSoft);
           if (g == 0) {
-            const float2 ml = reinterpret_cast<const float2*>(s_at)[row];
+            const float2 ml = s_ml[row];
             const float m0 = l == 0.f ? -INFINITY : m_run, m1 = ml.y == 0.f ? -INFINITY : ml.x, m = fmaxf(m0, m1);
             f0 = m0 == -INFINITY ? 0.f : ex2(m0 - m);
             f1 = m1 == -INFINITY ? 0.f : ex2(m1 - m);

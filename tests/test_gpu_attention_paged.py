@@ -86,6 +86,15 @@ def test_tree_variants(N, G, cap, window, bias):
         slopes=slopes_of(G) if bias else None, q_std=8.0 if cap else 2.0)
 
 
+@pytest.mark.parametrize("N,G", [(33, 1), (20, 4), (16, 8)])
+@pytest.mark.parametrize("window", [0, 100])
+@pytest.mark.parametrize("D", [64, 128])
+def test_biased_trees_whose_rows_share_tiles(N, G, window, D):
+    """One tile, an even and an odd number of them: the half that is done first leaves the other's positions alone."""
+    rng = np.random.default_rng(N + window)
+    run(rng, [0, 3, 130, 260, 700], N, 2, G, D, 16, BF, parents=tree(rng, 5, N), window=window, slopes=slopes_of(2 * G))
+
+
 @pytest.mark.parametrize("N,G", [(2, 4), (20, 4)])
 @pytest.mark.parametrize("sm,cap", [(-0.3, 0.0), (-0.3, 4.0), (0.0, 0.0), (3.0, 0.0), (3.0, 20.0)])
 def test_scales(N, G, sm, cap):
