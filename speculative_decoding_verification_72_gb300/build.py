@@ -58,7 +58,7 @@ def _binding_object(out):
 def build(verbose=False):
     os.makedirs(OUT_DIR, exist_ok=True)
     obj = os.path.join(OUT_DIR, "binding.o")
-    lib = [nvcc_path(), ARCH, "-O3", "-lineinfo", "-std=c++20", "--shared", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
+    lib = [nvcc_path(), ARCH, "-O3", "-lineinfo", "-std=c++17", "--shared", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
            "-I", os.path.join(ROOT, "include"), "--threads", "0", "-o", OUT, *SRCS]
     with ThreadPoolExecutor(2) as pool:
         jobs = [pool.submit(_run, lib), pool.submit(_binding_object, obj)]

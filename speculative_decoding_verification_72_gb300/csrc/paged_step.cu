@@ -67,11 +67,16 @@ bool page_map(const sv_paged_cache& c, const PagedView& v, int kv, CUtensorMap* 
 
 // Rows of a block: all of a kv head's as columns where they are at most 32 (in
 // one or two groups of 16), as 128 lanes that share the tiles between their two
-// copies where they are at most 128, else blocks of 256 lanes.
+// copies where they are at most 128, else blocks of 256 lanes. Each is there for
+// its time: 16 requests of 48 rows over a window of 4096 took 49 us as 128 lanes
+// that share tiles and 58 us as lanes of one half; with 32 rows as lanes
+// half of what the tensor cores do would be rows that are not there.
 int paged_block(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 128 ? 128 : kPgRowBlock; }
 
-// What an item's beginning and end cost, in tiles.
-constexpr int kPagedColExtra = 1, kPagedRowExtra = 4;
+// What an item's beginning and end (q, first products, the last rows out) cost, in
+// tiles. Of few rows: 32 chains of 24 rows 144 us at 0, 140 at 1, 138 at 2. Of many:
+// prompts of 4099 329 us at 2, 279 at 3, 257 at 4, 262 at 6; capped trees 127 at 3, 130 at 4.
+constexpr int kPagedColExtra = 2, kPagedRowExtra = 4;
 
 constexpr int kPagedGridMost = 160;   // CTAs a workspace is sized for: one an SM, whatever the device
 constexpr int64_t kPagedMostRows = int64_t{1} << 26;   // rows of a kv head; their node is exact up to 2^32 / G
@@ -163,6 +168,8 @@ sv_status spec_kv_append_rope(const sv_paged_cache* cache, int32_t dtype, const 
   a.rot = rotary_dims;
   a.interleaved = interleaved != 0;
   a.inv_heads = static_cast<uint32_t>(((1ll << 32) + heads - 1) / heads);
+  // Rows a CTA: enough units for each thread to have kRopeBatch in flight (12297 rows of prompts take 52 us so, 57 with
+  // twice and 67 with half as many), fewer where that would leave SMs without a CTA.
   const int64_t units = heads * (cache->D / 16);
   int64_t R = std::max<int64_t>(1, kRopeBatch * kRopeThreads / units);
   R = std::min<int64_t>({R, kRopeRows, N, std::max<int64_t>(1, static_cast<int64_t>(B) * N / (2 * sm_count()))});
