@@ -51,6 +51,9 @@ struct PgRowLayout {
   static constexpr int kTileBytes = kPgTile * D * 2;
   static constexpr int kStages = 128 * 1024 / kTileBytes;
   static constexpr int kDepth = kStages / 2;                             // V tiles in the ring
+  static constexpr bool kAhead = D == 64;                                // TMEM has room for a third S
+  static constexpr int kBufs = kAhead ? 3 : 2;
+  static constexpr int kVThreads = kAhead ? 32 : 64;
   static constexpr int kOffQ = kStages * kTileBytes;                     // [2 halves][128 rows]
   static constexpr int kOffMisc = kOffQ + 2 * kTileBytes;
   // V's non-finite columns by token and by row; parents and depths of the nodes; positions of a tile's tokens by half
@@ -140,13 +143,14 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
     attn_paged_rows_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                            const __grid_constant__ PagedAttnArgs a) {
   using L = PgRowLayout<D>;
-  constexpr int kSt = L::kStages, kDepth = L::kDepth;
+  constexpr int kSt = L::kStages, kDepth = L::kDepth, kBufs = L::kBufs, kVT = L::kVThreads;
+  constexpr bool kAhead = L::kAhead;
   extern __shared__ uint8_t raw[];
   __shared__ AttnLine s_line;
   __shared__ int32_t s_warp[kPgRowThreads / 32];
   __shared__ PagedCursor s_cur[kPgRowThreads / 32][2];
   __shared__ float2 s_ml[128];   // split: maxima and sums of half 1 (its other places are in use until half 0 is done)
-  __shared__ __align__(8) uint64_t s_bar[2 * kSt + kDepth + 10];
+  __shared__ __align__(8) uint64_t s_bar[2 * kSt + kDepth + 12];
   __shared__ uint32_t s_tmem, s_fail, s_there[16], s_odd[kDepth];   // s_odd: whether values were taken out of a tile's V
   const uint32_t smem0 = (smem_u32(raw) + 1023u) & ~1023u;
   uint8_t* smem = raw + (smem0 - smem_u32(raw));
@@ -158,7 +162,7 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t full = smem_u32(s_bar), empty = full + 8 * kSt, v_fit = empty + 8 * kSt, s_ready = v_fit + 8 * kDepth;
-  const uint32_t p_ready = s_ready + 16, o_done = p_ready + 32, q_ready = o_done + 16;
+  const uint32_t p_ready = s_ready + 8 * kBufs, o_done = p_ready + 32, q_ready = o_done + 8 * kBufs;
   if (tid == 0) {
     s_fail = 0;
 #pragma unroll 1
@@ -167,15 +171,16 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
       mbar_init(empty + 8 * i, 1);
     }
 #pragma unroll 1
-    for (int i = 0; i < kDepth; ++i) mbar_init(v_fit + 8 * i, 64);
+    for (int i = 0; i < kDepth; ++i) mbar_init(v_fit + 8 * i, kVT);
 #pragma unroll 1
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kBufs; ++i) {   // by S's place, which is the half where there are two
       mbar_init(s_ready + 8 * i, 1);
-      mbar_init(p_ready + 16 * i, 128);       // tokens 0 .. 63 of a tile, of half i
-      mbar_init(p_ready + 16 * i + 8, 128);   // tokens 64 .. 127
       mbar_init(o_done + 8 * i, 1);
-      mbar_init(q_ready + 8 * i, 128);
     }
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) mbar_init(p_ready + 8 * i, 128);   // by half: tokens 0 .. 63 of a tile, 64 .. 127; or by place
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) mbar_init(q_ready + 8 * i, 128);
     fence_barrier_init();
   }
   if (warp == 9) tmem_alloc(smem_u32(&s_tmem), 512);
@@ -205,7 +210,7 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
 
   if (warp == 8) {
     paged_load<D, kSt>(a, &k_map, &v_map, &cur, hi, smem0, full, empty, s_there, fail);
-  } else if (warp >= 10) {
+  } else if (warp >= 12 - kVT / 32) {
     // -------------------------------------------- V's rows that must not be read
     // A wait that gives up ends no loop here either: two warps meet at a barrier.
 #pragma unroll 1
@@ -220,7 +225,7 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
         uint8_t* vt = smem + st * L::kTileBytes;
         uint32_t odd = 0;
 #pragma unroll 1
-        for (int row = tid - 320; special && row < kPgTile; row += 64) {
+        for (int row = tid - (kPgRowThreads - kVT); special && row < kPgTile; row += kVT) {
           const bool valid = there >> (row >> a.c.page_shift) & 1 && tok0 + row < cur.rq.len;
 #pragma unroll
           for (int ch = 0; ch < D / 8; ++ch) {
@@ -231,10 +236,10 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
               *p = make_uint4(0, 0, 0, 0);
           }
         }
-        odd = named_barrier_or(5, 64, odd != 0);
+        odd = named_barrier_or(5, kVT, odd != 0);
         uint32_t* flags = s_tok + (n % kDepth) * 128 * (D / 16);
 #pragma unroll 1
-        for (int row = tid - 320; odd && row < kPgTile; row += 64) {
+        for (int row = tid - (kPgRowThreads - kVT); odd && row < kPgTile; row += kVT) {
           const bool valid = there >> (row >> a.c.page_shift) & 1 && tok0 + row < cur.rq.len;
 #pragma unroll 1
           for (int ch = 0; ch < D / 8; ++ch) {
@@ -244,12 +249,12 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
             to[D / 8] = static_cast<uint8_t>(f >> 8);
           }
         }
-        if (tid == 320) s_odd[n % kDepth] = odd;
+        if (tid == kPgRowThreads - kVT) s_odd[n % kDepth] = odd;
         fence_async_smem();
         mbar_arrive(v_fit + 8 * (n % kDepth));
       }
     }
-  } else if (warp == 9) {
+  } else if (warp >= 9) {
     // ------------------------------------------------------------------ MMA
     constexpr uint32_t kIdS = tc_idesc(T::kMma, false, false, 128, 128), kIdO = tc_idesc(T::kMma, false, true, 128, D);
     // Operands' descriptors: a step of 16 along K is 32 bytes of a row, or 16 rows of V.
@@ -257,72 +262,135 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
     const uint64_t d_v = tc_desc(smem0, kPgTile * 128, 1024, 2);
     auto at = [](uint64_t d, uint32_t bytes) { return d + (bytes >> 4); };
     bool ok = true;
-    uint32_t pieces[2] = {0, 0}, mine[2] = {0, 0};   // by half; mine: tiles
-    // In the elected thread: S of tile m.
-    auto scores = [&](uint32_t m, int g, bool last) {
-      const uint32_t st = 2 * m % kSt;
-      const uint64_t q = at(d_q, g * L::kTileBytes), k = at(d_k, st * L::kTileBytes);
-#pragma unroll
-      for (int j = 0; j < D / 16; ++j) {
-        const uint32_t off = (j >> 2) * (kPgTile * 128) + (j & 3) * 32;
-        tc_mma_f16(tmem + g * 128, at(q, off), at(k, off), kIdS, j > 0);
-      }
-      tc_commit(s_ready + 8 * g);
-      if (last) tc_commit(empty + 8 * st);
-    };
-    auto k_there = [&](uint32_t m) { ok = ok && warp_wait_or_fail(full + 8 * (2 * m % kSt), (2 * m / kSt) & 1, fail); };
+    if constexpr (kAhead) {
+      // Products of both halves by turns, in order: k counts them.
+      const uint32_t tmem = uniform(s_tmem);
+      uint32_t k = 0;
+      if (warp == 9) {   // P V
 #pragma unroll 1
-    for (; ok && cur.pos < hi; next_piece(a, &cur, &cur, hi)) {
-      const int gs = halves(cur.block), tiles = cur.n;
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        if (g == gs || !ok) break;
-        const int first = split ? g : 0;   // the half's first tile
-        if (g == 0 || (split && tiles > 1)) k_there(n + first);
-        ok = ok && warp_wait_or_fail(q_ready + 8 * g, pieces[g]++ & 1, fail);
-        if (!ok) break;
-        tc_fence_after();
-        if (first < tiles && elect_one()) scores(n + first, g, split || g + 1 == gs);
-        __syncwarp();
-      }
-      const int step = split ? 2 : 1;
+        for (; ok && cur.pos < hi; next_piece(a, &cur, &cur, hi)) {
+          const int gs = uniform(halves(cur.block)), tiles = uniform(cur.n);
+          const bool both = !split && gs == 2;   // a tile is for both halves
+          const int total = both ? 2 * tiles : tiles;
 #pragma unroll 1
-      for (int i = 0; i < tiles && ok; ++i, ++n) {
-        const uint32_t st = (2 * n + 1) % kSt;
-        const uint64_t v = at(d_v, st * L::kTileBytes);
-        const bool more = i + step < tiles;
-        ok = warp_wait_or_fail(v_fit + 8 * (n % kDepth), (n / kDepth) & 1, fail);
+          for (int j = 0; j < total && ok; ++j, ++k) {
+            const uint32_t m = n + (both ? j >> 1 : j), st = (2 * m + 1) % kSt, buf = k % kBufs;
+            const int g = gs == 2 ? j & 1 : 0;
+            if (!both || !g) ok = warp_wait_or_fail(v_fit + 8 * (m % kDepth), (m / kDepth) & 1, fail);
+            ok = ok && warp_wait_or_fail(p_ready + 8 * buf, k / kBufs & 1, fail);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+              const uint64_t v = at(d_v, st * L::kTileBytes);
+              const uint32_t t_p = tmem + buf * 128, t_o = tmem + kBufs * 128 + g * D;
+#pragma unroll
+              for (int x = 0; x < 8; ++x)   // P's halves lie where those of S did
+                tc_mma_f16_ts(t_o, t_p + (x & 3) * 8 + (x >> 2) * 64, at(v, 2048 * x), kIdO, j >= gs || x > 0);
+              tc_commit(o_done + 8 * buf);
+              if (!both || g) tc_commit(empty + 8 * st);
+            }
+            __syncwarp();
+          }
+          n += tiles;
+        }
+      } else {   // q K^T
+        uint32_t pieces0 = 0, pieces1 = 0;
+#pragma unroll 1
+        for (; ok && cur.pos < hi; next_piece(a, &cur, &cur, hi)) {
+          const int gs = uniform(halves(cur.block)), tiles = uniform(cur.n);
+          const bool both = !split && gs == 2;
+          const int total = both ? 2 * tiles : tiles;
+#pragma unroll 1
+          for (int j = 0; j < max(total, gs) && ok; ++j) {
+            if (j < gs) ok = warp_wait_or_fail(q_ready + 8 * j, (j ? pieces1++ : pieces0++) & 1, fail);
+            if (j >= total) break;
+            const uint32_t m = n + (both ? j >> 1 : j), st = 2 * m % kSt, buf = k % kBufs;
+            const int g = gs == 2 ? j & 1 : 0;
+            if (!both || !g) ok = ok && warp_wait_or_fail(full + 8 * st, (2 * m / kSt) & 1, fail);
+            if (k >= kBufs) ok = ok && warp_wait_or_fail(o_done + 8 * buf, (k / kBufs - 1) & 1, fail);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+              const uint64_t q = at(d_q, g * L::kTileBytes), kt = at(d_k, st * L::kTileBytes);
+#pragma unroll
+              for (int x = 0; x < D / 16; ++x) tc_mma_f16(tmem + buf * 128, at(q, x * 32), at(kt, x * 32), kIdS, x > 0);
+              tc_commit(s_ready + 8 * buf);
+              if (!both || g) tc_commit(empty + 8 * st);
+            }
+            __syncwarp();
+            ++k;
+          }
+          n += tiles;
+        }
+      }
+    } else {
+      uint32_t pieces[2] = {0, 0}, mine[2] = {0, 0};   // by half; mine: tiles
+      // In the elected thread: S of tile m.
+      auto scores = [&](uint32_t m, int g, bool last) {
+        const uint32_t st = 2 * m % kSt;
+        const uint64_t q = at(d_q, g * L::kTileBytes), k = at(d_k, st * L::kTileBytes);
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+          const uint32_t off = (j >> 2) * (kPgTile * 128) + (j & 3) * 32;
+          tc_mma_f16(tmem + g * 128, at(q, off), at(k, off), kIdS, j > 0);
+        }
+        tc_commit(s_ready + 8 * g);
+        if (last) tc_commit(empty + 8 * st);
+      };
+      auto k_there = [&](uint32_t m) { ok = ok && warp_wait_or_fail(full + 8 * (2 * m % kSt), (2 * m / kSt) & 1, fail); };
+#pragma unroll 1
+      for (; ok && cur.pos < hi; next_piece(a, &cur, &cur, hi)) {
+        const int gs = halves(cur.block), tiles = cur.n;
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
           if (g == gs || !ok) break;
-          if (split && g != (i & 1)) continue;
-          const bool last = split || g + 1 == gs;
-          ok = warp_wait_or_fail(p_ready + 16 * g, mine[g] & 1, fail);
+          const int first = split ? g : 0;   // the half's first tile
+          if (g == 0 || (split && tiles > 1)) k_there(n + first);
+          ok = ok && warp_wait_or_fail(q_ready + 8 * g, pieces[g]++ & 1, fail);
           if (!ok) break;
           tc_fence_after();
-          // P's halves lie where those of S did.
-          if (elect_one())
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              tc_mma_f16_ts(tmem + 256 + g * 128, tmem + g * 128 + j * 8, at(v, 2048 * j), kIdO, i >= step || j > 0);
+          if (first < tiles && elect_one()) scores(n + first, g, split || g + 1 == gs);
           __syncwarp();
-          if (more && (g == 0 || split)) k_there(n + step);   // under these products
-          ok = ok && warp_wait_or_fail(p_ready + 16 * g + 8, mine[g] & 1, fail);
-          if (!ok) break;
-          tc_fence_after();
-          if (elect_one()) {
+        }
+        const int step = split ? 2 : 1;
+#pragma unroll 1
+        for (int i = 0; i < tiles && ok; ++i, ++n) {
+          const uint32_t st = (2 * n + 1) % kSt;
+          const uint64_t v = at(d_v, st * L::kTileBytes);
+          const bool more = i + step < tiles;
+          ok = warp_wait_or_fail(v_fit + 8 * (n % kDepth), (n / kDepth) & 1, fail);
 #pragma unroll
-            for (int j = 4; j < 8; ++j)
-              tc_mma_f16_ts(tmem + 256 + g * 128, tmem + g * 128 + 64 + (j - 4) * 8, at(v, 2048 * j), kIdO, true);
-            if (last) tc_commit(empty + 8 * st);
-            // The next S overwrites this P: products that one thread issues run in order.
-            if (more)
-              scores(n + step, g, last);
-            else
-              tc_commit(o_done + 8 * g);
+          for (int g = 0; g < 2; ++g) {
+            if (g == gs || !ok) break;
+            if (split && g != (i & 1)) continue;
+            const bool last = split || g + 1 == gs;
+            ok = warp_wait_or_fail(p_ready + 16 * g, mine[g] & 1, fail);
+            if (!ok) break;
+            tc_fence_after();
+            // P's halves lie where those of S did.
+            if (elect_one())
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                tc_mma_f16_ts(tmem + 256 + g * 128, tmem + g * 128 + j * 8, at(v, 2048 * j), kIdO, i >= step || j > 0);
+            __syncwarp();
+            if (more && (g == 0 || split)) k_there(n + step);   // under these products
+            ok = ok && warp_wait_or_fail(p_ready + 16 * g + 8, mine[g] & 1, fail);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int j = 4; j < 8; ++j)
+                tc_mma_f16_ts(tmem + 256 + g * 128, tmem + g * 128 + 64 + (j - 4) * 8, at(v, 2048 * j), kIdO, true);
+              if (last) tc_commit(empty + 8 * st);
+              // The next S overwrites this P: products that one thread issues run in order.
+              if (more)
+                scores(n + step, g, last);
+              else
+                tc_commit(o_done + 8 * g);
+            }
+            __syncwarp();
+            ++mine[g];
           }
-          __syncwarp();
-          ++mine[g];
         }
       }
     }
@@ -331,9 +399,9 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
     const int g = warp >> 2, row = tid & 127;   // the thread's half, its row of it
     const int bar = 2 + g;                       // of the half's threads
     const uint32_t t_lane = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t t_s = t_lane + g * 128, t_o = t_lane + 256 + g * 128;
+    const uint32_t t_o = t_lane + kBufs * 128 + g * D;
     uint32_t* flags = s_row + (g * 128 + row) * (D / 16);
-    uint32_t mine = 0, pieces = 0;   // tiles and pieces of this half
+    uint32_t mine = 0, pieces = 0;   // tiles and pieces of this half; kAhead: products of both halves before this piece
     // q's rows of a piece, D / 8 threads a row: on their way to their place, and there.
     auto q_start = [&](const PagedCursor& c) {
       constexpr int kLpr = D / 8;
@@ -402,10 +470,11 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
       float m_run = 0.f, l = 0.f;            // m_run means something once the row has seen a slot
       bool seen = false, any_odd = false;
 #pragma unroll 1
-      for (int i = split ? g : 0; i < tiles; i += split ? 2 : 1, ++mine) {
-        const uint32_t tile = n + i;
+      for (int i = split ? g : 0; i < tiles; i += split ? 2 : 1) {
+        const uint32_t tile = n + i, k = kAhead ? mine + (split ? i : gs * i + g) : mine++;
+        const uint32_t buf = kAhead ? k % kBufs : g, phase = (kAhead ? k / kBufs : k) & 1, t_s = t_lane + buf * 128;
         const int tok0 = (t0 + i) * kPgTile;
-        wait_or_fail(s_ready + 8 * g, mine & 1, fail);   // and every product before this S is done
+        wait_or_fail(s_ready + 8 * buf, phase, fail);   // every product before this S is done, but for kAhead the half's last
         tc_fence_after();
         const uint32_t there = s_there[tile & 15];
         const bool special = tok0 + kPgTile > clear || tok0 < inside || there != all_pages;
@@ -498,6 +567,10 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
           seen = seen || raise;
           l *= f;
           if (i >= (split ? 2 : 1) && __any_sync(0xffffffffu, f != 1.f)) {   // O holds something
+            if (kAhead) {
+              wait_or_fail(o_done + 8 * ((k - gs) % kBufs), (k - gs) / kBufs & 1, fail);
+              tc_fence_after();
+            }
 #pragma unroll 1
             for (int j = 0; j < D; j += 16) {
               uint32_t o[16];
@@ -540,7 +613,7 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
           }
           tmem_st_wait();
           tc_fence_before();
-          mbar_arrive(p_ready + 16 * g + 8 * u);
+          if (!kAhead || u == 1) mbar_arrive(p_ready + (kAhead ? 8 * buf : 16 * g + 8 * u));
         }
         sum[0] = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
         l += sum[0].x + sum[0].y;
@@ -552,7 +625,12 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
       const bool bring = next.pos < hi && g < halves(next.block);
       if (bring && !split) q_start(next);   // the half's scores of this piece are done
       if (active) {
-        if (!split || g < tiles) wait_or_fail(o_done + 8 * g, pieces++ & 1, fail);
+        if (!kAhead && (!split || g < tiles)) wait_or_fail(o_done + 8 * g, pieces++ & 1, fail);
+        if (kAhead && (!split || g < tiles)) {   // the half's last, and before `other` is written the last S of both
+          const uint32_t all = mine + (split ? tiles : gs * tiles) - 1, k = split ? all - ((tiles - 1 - g) & 1) : all - (gs - 1 - g);
+          if (split) wait_or_fail(s_ready + 8 * (all % kBufs), all / kBufs & 1, fail);
+          wait_or_fail(o_done + 8 * (k % kBufs), k / kBufs & 1, fail);
+        }
         tc_fence_after();
         if (any_odd) put_back_rows<D>(t_o, flags);
         float f0 = 1.f, f1 = 0.f;   // of this half's O, and of the other's
@@ -624,7 +702,10 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
           a.lse[to] = l == 0.f ? -INFINITY : (m_run + log2f(l)) * kLn2;
         tc_fence_before();
       }
-      if (a.parents || split) named_barrier_sync(4, kPgRowSoft);   // the tree's place and the other half's are free for the next piece
+      if (kAhead) mine += split || gs == 1 ? cur.n : 2 * cur.n;
+      // The tree's place and the other half's are free for the next piece; a half without rows keeps step (a wait must not
+      // be for a phase after the one that is next on its barrier).
+      if (a.parents || split || (kAhead && gs == 1)) named_barrier_sync(4, kPgRowSoft);
       if (bring && split) q_start(next);
       if (bring) q_end();
     }
