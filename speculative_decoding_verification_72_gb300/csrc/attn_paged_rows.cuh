@@ -6,25 +6,27 @@
 //   S_g [128 rows, 128 tokens] = q_g K^T,   O_g [128 rows, D] += P_g V,
 // K and V as TMA brings them (V transposed by the descriptor), P_g in the type
 // of V over the columns of S_g in TMEM. Per tile the products of a half take
-// 8 D clocks and its 128 x 128 exponentials 512 (32 a clock). S and O of both
-// halves fill all 512 columns of TMEM, so within a half S, softmax and P V
-// follow each other and one half's softmax runs under the other's products; one
-// CTA an SM.
+// 8 D clocks and its 128 x 128 exponentials 512 (32 a clock). With 128-wide heads S
+// and O of both halves fill all 512 columns of TMEM, so within a half S, softmax
+// and P V follow each other and one half's softmax runs under the other's
+// products; one CTA an SM. With 64-wide heads there is room for a third S: products
+// are taken by turns, S three ahead of P V by a warp of its own, and the softmax
+// of neither half waits for them (a piece of 1001 rows 570 us, so 645 without).
 //
 // Where a kv head has no more than 128 rows, both halves take them, and the tiles
 // by turns; at a piece's end one half's O, maxima and sums go to the other.
 //
 // A thread has one row, so maximum, exponentials and sum are its own. It reads its
 // scores twice, for the maximum and for the exponentials, which it writes over
-// what it has read; P of the first 64 tokens is multiplied while those of the
-// others are worked out. The running maximum is raised only when a score exceeds
+// what it has read; with 128-wide heads P of the first 64 tokens is multiplied
+// while those of the others are worked out. The running maximum is raised only when a score exceeds
 // it by 2^8; the warp then rescales its rows of O. P is rounded to 16 bits (half a
 // step of the type: 2^-8 of a bf16 weight, 2^-11 of f16's), its sum is not.
 //
 // Capped or biased scores, and those of a tile that some row does not see whole,
 // are made final in TMEM on the first reading: -inf where the row's 128 bits say
 // so, which the thread works out from its position and path. What must not be read
-// of such a tile's V is taken out by two warps of their own as soon as it is there.
+// of such a tile's V is taken out by warps of their own as soon as it is there.
 // The rows of the next piece's q come in under the last products of this one.
 //
 // The roles run different code at once, and all of it has to stay in the
@@ -33,8 +35,16 @@
 // weights' sum showed that none was too large) a tile took fewer instructions
 // and more time: prompts 425 us against 419 before, capped trees 337 against 218.
 //
+// Measured: two prompts of 4099 rows (32 heads on 8 of 128) 257 us, 1.08 PFLOP/s,
+// a tile of two halves 3400 clocks against 2048 of its products: the MMA warp's
+// waits for what is there already (150 clocks each, five a half) and its issue.
+// 64-wide heads: 1200 clocks a half, all of it softmax, which alone takes 900.
+// Trees of 64 nodes on 16 requests of up to 8192 tokens 99 us, 3.6 TB/s. Sixteen
+// softmax warps instead of eight took as long (piece 580 us, prompts 267).
+//
 // Warps 0-3 and 4-7: softmax of the halves. 8: TMA. 9: MMA, which takes the
-// halves by turns, so that they fall out of step. 10 and 11: V.
+// halves by turns, so that they fall out of step. 10 and 11: V; with 64-wide
+// heads 9 has P V, 10 has S and 11 V.
 #pragma once
 
 #include "attn_paged_cols.cuh"
@@ -137,7 +147,7 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 
-// kVar: scores are capped or biased, or their factor is negative.
+// kVar: scores are capped or biased, or their factor is negative (the maximum of products is then not that of scores).
 template <typename T, int D, bool kVar>
 __global__ void __launch_bounds__(kPgRowThreads, 1)
     attn_paged_rows_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
