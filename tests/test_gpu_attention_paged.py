@@ -332,6 +332,35 @@ def test_many_pieces(B, N, H, G, D, L, dtype):
     check_attention(r, in_64(q, cache, tab, base), dtype, N * G)
 
 
+@pytest.mark.parametrize("N,D", [(9, 128), (9, 64), (2, 128)])
+def test_more_requests_than_threads(N, D):
+    q, cache, _ = big(900, N, 1, 4, D, 16, 0, BF, 4)
+    tab = torch.arange(8, dtype=torch.int32, device=DEV).repeat(900, 1)
+    base = [(i * 37) % 110 for i in range(900)]
+    r = sv.spec_attention(q, cache, tab, i32(base))
+    assert int(r["status"].max()) == 0
+    check_attention(r, in_64(q, cache, tab, base), BF, N * 4)
+
+
+@pytest.mark.parametrize("D,G", [(64, 2), (128, 1)])
+def test_more_blocks_than_threads(D, G):
+    """A prompt of 150,000 rows in a window of 100; every 997th row and the last ones against 64 bits."""
+    N, w = 150_000, 100
+    q, cache, tab = big(1, N, 1, G, D, 64, 0, BF, 5)
+    r = sv.spec_attention(q, cache, tab, i32([0]), window=w)
+    assert int(r["status"].max()) == 0
+    rows = torch.tensor([*range(0, N, 997), *range(N - 40, N)], device=DEV)
+    at = rows[:, None] - torch.arange(w, device=DEV)
+    see = (at >= 0)[:, None]
+    k, v = (t[tab[0].long()].flatten(0, 1)[at.clamp(min=0)][:, :, 0].double() for t in cache)   # [rows, w, D]
+    qq = q[0, rows].double()
+    z = torch.einsum("rgd,rwd->rgw", qq, k).mul(D ** -0.5).masked_fill(~see, -torch.inf)
+    p = torch.softmax(z, -1)
+    want = (p @ v, torch.logsumexp(z, -1), p @ v.abs(), torch.einsum("rgd,rwd->rgw", qq.abs(), k.abs()).amax(-1) * D ** -0.5,
+            z.masked_fill(~see, 0).abs().amax(-1), see.sum(-1).double().expand(-1, G))
+    check_attention(dict(out=r["out"][:, rows], lse=r["lse"][:, rows]), [t.cpu().numpy()[None] for t in want], BF, N * G)
+
+
 @pytest.mark.parametrize("N,G", [(2, 4), (12, 4), (70, 4)])
 def test_nan_keys_under_a_cap(N, G):
     rng = np.random.default_rng(21)
