@@ -27,10 +27,11 @@ __device__ __forceinline__ int paged_page(const PagedView& c, int b, int lp) {
 }
 
 // A node's parent in a tree whose nodes follow their parents: -1 ends a path,
-// and so does what is no earlier node.
+// and so does what is no earlier node, however far out of range (what is kept
+// of the parents in 16 bits is this, never what was given).
 __device__ __forceinline__ int tree_up(const int32_t* parents, int n) {
   const int p = parents[n];
-  return p < n ? p : -1;
+  return p >= 0 && p < n ? p : -1;
 }
 __device__ __forceinline__ int tree_depth(const int32_t* parents, int n) {
   int d = 0;

@@ -150,6 +150,17 @@ def test_bad_parents(N, G):
     assert r["status"].cpu().tolist() == [2, 2, 2, 2]
 
 
+@pytest.mark.parametrize("value", [-2, -32768, -32769, -40000, -65536, -(1 << 31), 1 << 16, (1 << 31) - 1])
+@pytest.mark.parametrize("N,G,D", [(6, 4, 64), (40, 1, 64), (40, 4, 128), (150, 2, 64)])
+def test_parents_far_out_of_range(value, N, G, D):
+    """They end the path, at the root and inside a tree, whatever their low bits are."""
+    rng = np.random.default_rng(23)
+    par = tree(rng, 4, N)
+    par[0, 0] = par[1, 3] = par[2, 0] = par[2, 4] = value
+    r, _ = run(rng, [20, 130, 0, 64], N, 1, G, D, 16, BF, parents=par)
+    assert r["status"].cpu().tolist() == [2, 2, 2, 0]
+
+
 # ------------------------------------------------------- what must not be read
 
 @pytest.mark.parametrize("dtype", [BF, F16])

@@ -94,6 +94,15 @@ def test_bad_pages_counts_parents():
     assert (r["q"][4] == 0).all()
 
 
+@pytest.mark.parametrize("value", [-2, -32768, -40000, -65536, -(1 << 31), 1 << 16, (1 << 31) - 1])
+def test_parents_far_out_of_range(value):
+    rng = np.random.default_rng(8)
+    par = tree(rng, 3, 40)
+    par[0, 0] = par[1, 3] = value
+    r = run(rng, [20, 130, 0], 40, 2, 4, 64, 16, torch.bfloat16, parents=par)
+    assert r["status"].cpu().tolist() == [2, 2, 0]
+
+
 def test_far_positions():
     """Angles of thousands of turns: positions near 2^20 and 2^24 in a table whose other pages are missing."""
     for base in (1 << 20, (1 << 24) - 40):
