@@ -372,6 +372,33 @@ def test_more_blocks_than_threads(D, G):
     check_attention(dict(out=r["out"][:, rows], lse=r["lse"][:, rows]), [t.cpu().numpy()[None] for t in want], BF, N * G)
 
 
+@pytest.mark.parametrize("D,dtype", [(128, BF), (64, F16)])
+def test_a_half_without_rows_waits_through_long_pieces(D, dtype):
+    """65 rows of 4 heads after 190 million tokens: a block of 256 rows and one of 4, of which one CTA has some 30,000 tiles
+    (longer than any wait's limit) before a block of 256 of the next request. The prefix goes round 64 pages, so it is one
+    round with every weight counted `turns` times."""
+    N, G, turns = 65, 4, (23400, 22900)
+    g = torch.Generator(device=DEV).manual_seed(24)
+    mk = lambda *s: torch.randn(s, generator=g, device=DEV).to(dtype)  # noqa: E731
+    q, cache = mk(2, N, G, D), sv.PagedCache(mk(66, 128, 1, D), mk(66, 128, 1, D))
+    tab = (torch.arange(64 * turns[0] + 1, device=DEV, dtype=torch.int32) % 64).repeat(2, 1)
+    for b, n in enumerate(turns):
+        tab[b, 64 * n] = 64 + b
+    r = sv.spec_attention(q, cache, tab, i32([8192 * n for n in turns]))
+    assert r["status"].cpu().tolist() == [0, 0]
+    for b, n in enumerate(turns):
+        k, v = (torch.cat([t[:64].flatten(0, 1), t[64 + b, :N]])[:, 0].double() for t in cache)
+        z = torch.einsum("ngd,sd->ngs", q[b].double(), k) * D ** -0.5
+        z[..., :8192] += np.log(n)
+        z.masked_fill_((torch.arange(8192 + N, device=DEV) > 8192 + torch.arange(N, device=DEV)[:, None])[:, None], -torch.inf)
+        p = torch.softmax(z, -1)
+        # A CTA sums up to 40,000 tiles, eight products of 16 slots a tile, each sum off by a step of fp32 (2^-23); besides
+        # that the weights' and the output's rounding, and scores off by 2^-16 of a sum of at most 64 or so.
+        off = 8 * 40000 * 2.0 ** -23 + 2.0 ** -10
+        assert ((r["lse"][b] - torch.logsumexp(z, -1)).abs() < off).all()
+        assert ((r["out"][b].double() - p @ v).abs() < (2 * off + 2.0 ** -7) * (p @ v.abs())).all()
+
+
 @pytest.mark.parametrize("N,G", [(2, 4), (12, 4), (70, 4)])
 def test_nan_keys_under_a_cap(N, G):
     rng = np.random.default_rng(21)
