@@ -715,8 +715,10 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
       if (kAhead) mine += split || gs == 1 ? cur.n : 2 * cur.n;
       // The tree's place and the other half's are free for the next piece; a half without rows keeps step (a wait must not
       // be for a phase after the one that is next on its barrier, nor last as long as the other half's piece: of a few
-      // million tokens that is longer than the limit).
-      if (a.parents || split || gs == 1) named_barrier_sync(4, kPgRowSoft);
+      // million tokens that is longer than the limit). Where both halves' products share places, the other half does not go
+      // on alone before this one has seen its last product done.
+      const bool alone = kAhead && next.pos < hi && halves(next.block) == 1;
+      if (a.parents || split || gs == 1 || alone) named_barrier_sync(4, kPgRowSoft);
       if (bring && split) q_start(next);
       if (bring) q_end();
     }

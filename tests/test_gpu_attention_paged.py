@@ -372,6 +372,19 @@ def test_more_blocks_than_threads(D, G):
     check_attention(dict(out=r["out"][:, rows], lse=r["lse"][:, rows]), [t.cpu().numpy()[None] for t in want], BF, N * G)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_blocks_of_two_halves_and_of_one_by_turns(D):
+    """Pieces of two halves go over to pieces of one and back in every CTA, again and again the same bits."""
+    q, cache, tab = big(40, 70, 2, 4, D, 16, 1500, F16, 25)
+    base = i32([(1500 * (7 * b % 40)) // 40 for b in range(40)])
+    first = sv.spec_attention(q, cache, tab, base)
+    assert int(first["status"].max()) == 0
+    check_attention(first, in_64(q, cache, tab, base.tolist()), F16, 280)
+    for _ in range(20):
+        r = sv.spec_attention(q, cache, tab, base)
+        assert all(torch.equal(r[n], first[n]) for n in r)
+
+
 @pytest.mark.parametrize("D,dtype", [(128, BF), (64, F16)])
 def test_a_half_without_rows_waits_through_long_pieces(D, dtype):
     """65 rows of 4 heads after 190 million tokens: a block of 256 rows and one of 4, of which one CTA has some 30,000 tiles
