@@ -666,14 +666,14 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
             f0 = m0 == -INFINITY ? 0.f : ex2(m0 - m);
             f1 = m1 == -INFINITY ? 0.f : ex2(m1 - m);
             if (m != -INFINITY) m_run = m;
-            l = (f0 == 0.f ? 0.f : l * f0) + (f1 == 0.f ? 0.f : ml.y * f1);
+            l = fmaf(l, f0, ml.y * f1);   // a factor of 0 is no reason to leave a sum or an O out: 0 times NaN shows
           }
         }
         if (*fail) l = __int_as_float(0x7fc00000);
         if (node < 0) l = 0.f;
         const float f = l == 0.f ? 0.f : cur.whole ? 1.f / l : 1.f;
-        f0 = f == 0.f ? 0.f : f0 * f;
-        f1 = f == 0.f ? 0.f : f1 * f;
+        f0 *= f;
+        f1 *= f;
         const int lane_of = split ? row : g * 128 + row;
         float* part = a.part + static_cast<int64_t>(2 * blockIdx.x + (count == 0 ? 0 : 1)) * a.R * (D + 2) + lane_of;
         const int64_t to = (static_cast<int64_t>(cur.b) * a.N + at) * a.Hq + cur.h * a.G + (Rg - at * a.G);
@@ -686,8 +686,8 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
           tmem_ld_wait();
           tmem_use(o);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(f0 == 0.f ? 0.f : __uint_as_float(o[e]) * f0);
-          if (f1 != 0.f)
+          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(f == 0.f ? 0.f : __uint_as_float(o[e]) * f0);
+          if (split && tiles > 1 && f != 0.f)   // the other half has an O
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(fmaf(other[(j + e) * 128], f1, __uint_as_float(o[e])));
           if (cur.whole) {

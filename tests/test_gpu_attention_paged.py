@@ -422,6 +422,43 @@ def test_nan_keys_under_a_cap(N, G):
     assert torch.isnan(r["out"]).all() and torch.isnan(r["lse"]).all()
 
 
+@pytest.mark.parametrize("N,G,tree_rows", [(6, 4, False), (36, 1, False), (10, 4, True), (130, 2, False)])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("low", [0, 1, 2])
+@pytest.mark.parametrize("what", ["k nan", "k all nan", "v nan", "v inf", "v last inf"])
+def test_what_is_not_finite_far_below_the_maximum(N, G, tree_rows, D, low, what):
+    """Scores of one tile are 200 or more below the others', so its weights are zero to fp32; what is not finite there still
+    shows. 300 requests with the same rows, so that CTAs have all tiles of an item and parts of one."""
+    rng = np.random.default_rng(26)
+    base = 256 + 40
+    tab = table(rng, [base + N], 16, 30)
+    c = host_cache(rng, 30, 16, 1, D, BF)
+    hq, gq = normal(rng, (1, N, G, D), BF)
+    hq[..., 0], gq[..., 0] = 8.0, 8.0
+    spots = [(tab[0, p // 16], p % 16) for p in range(base)]
+    for p, at in enumerate(spots):
+        c["k"][at][0, 0] = 0.0 if p // 128 == low else 300.0
+    at = [spots[p] for p in range(base) if p // 128 == low]
+    if what == "k nan":
+        c["k"][at[3]][0, 9] = np.nan
+    elif what == "k all nan":
+        for x in at:
+            c["k"][x][0, 9] = np.nan
+    elif what == "v nan":
+        c["v"][at[3]][0, 9] = np.nan
+    else:
+        c["v"][at[-1 if "last" in what else 3]][0, 9] = np.inf
+    parents = tree(rng, 1, N) if tree_rows else None
+    c = {n: torch.from_numpy(x).to(BF).double().numpy() for n, x in c.items()}
+    want = K.attention(hq, c, tab, [base], parents, None, D ** -0.5)
+    many = lambda x: i32(x).expand(300, -1).contiguous()  # noqa: E731
+    r = sv.spec_attention(gq.expand(300, -1, -1, -1), to_gpu(c, BF), many(tab), i32([base] * 300),
+                          parents=many(parents) if tree_rows else None)
+    check_attention(r, [np.repeat(x, 300, 0) for x in want], BF, N * G)
+    lost = np.isnan(want[1]) if "k" in what else ~np.isfinite(want[0][..., 9])
+    assert lost.all()
+
+
 @pytest.mark.parametrize("N,G", [(2, 4), (12, 4), (70, 4)])
 @pytest.mark.parametrize("cap", [1.0, 30.0])
 def test_scores_far_past_the_cap(N, G, cap):
