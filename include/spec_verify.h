@@ -581,8 +581,8 @@ typedef struct sv_paged_cache {
  * the angle p * inv_freq[i] (inv_freq fp32, on the device); other dims, and
  * values, are moved as they are. rotary_dims is a multiple of 16, at most D.
  * q [B, N, Hq, D] goes to out_q (contiguous; q itself if that is); q NULL
- * takes Hq = 0. Angles are right to 2^-24 of a turn for positions below 2^24
- * (2^-17 up to 2^31), rotations are fp32 and rounded once. out_len[b] = seq_base[b] +
+ * takes Hq = 0. Angles are right to 2^-23 of a turn for positions below 2^24
+ * (2^-17 up to 2^31) and inv_freq up to 1, rotations are fp32 and rounded once. out_len[b] = seq_base[b] +
  * row count; it is neither seq_base nor n_nodes (SV_ERR_INVALID_ARG: the call
  * reads them to its end). A request with a bad page, slot or row count has
  * nothing written (out_len = seq_base), its queries are rotated all the same.

@@ -7,12 +7,9 @@
 //   (x cos a_i - y sin a_i, y cos a_i + x sin a_i);
 // dims from R on, and values, are moved as they are.
 //
-// Angles. p inv_freq has more bits than fp32 holds, and only its fraction of a
-// turn counts. inv_freq / 2 pi is taken as a sum of two floats, p as p1 + p0
-// with p0 < 2^12, so each product's rounding error is had exactly by fma; whole
-// turns are taken off each product, and what is left is within 2^-24 of a turn
-// for positions below 2^24 (2^-17 up to 2^31). Rotations are fp32, rounded once
-// to the row's type.
+// Angles are right to 2^-23 of a turn for positions below 2^24 (2^-17 up to
+// 2^31) and inv_freq up to 1, without 64 bits: rope_angle.cuh. Rotations are
+// fp32, rounded once to the row's type.
 //
 // A CTA takes a few rows of a request: first the loads of the rows themselves
 // (they need neither page nor angle), then pages, depths and angles (one angle
@@ -28,6 +25,7 @@
 #pragma once
 
 #include "paged_common.cuh"
+#include "rope_angle.cuh"
 
 namespace sv {
 
@@ -53,15 +51,8 @@ struct RopeArgs {
 
 // cos and sin of p f.
 __device__ __forceinline__ float2 rope_angle(int p, float f) {
-  constexpr float kTurn = 0.15915493667125701904f, kTurnLo = 6.4206383e-9f;   // 1 / 2 pi as a sum of floats
-  const float r = f * kTurn, r_lo = fmaf(f, kTurnLo, fmaf(f, kTurn, -r));
-  const float p1 = static_cast<float>(p & ~0xfff), p0 = static_cast<float>(p & 0xfff);
-  float x1 = p1 * r, x0 = p0 * r;
-  const float e = fmaf(p1, r, -x1) + fmaf(p0, r, -x0) + fmaf(p1, r_lo, p0 * r_lo);
-  x1 -= rintf(x1);
-  x0 -= rintf(x0);
   float s, c;
-  sincospif(2.f * (x1 + x0 + e), &s, &c);
+  sincospif(2.f * rope_turn(p, f), &s, &c);
   return make_float2(c, s);
 }
 

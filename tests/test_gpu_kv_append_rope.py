@@ -113,6 +113,22 @@ def test_far_positions():
         run(rng, [base], 16, 1, 2, 128, 128, torch.float16, tab=tab, pages=3)
 
 
+def test_positions_near_the_end_of_32_bits():
+    """The last slots of the longest table; angles of 2^28 turns, right to 2^-17 of one."""
+    W, rng = (2 ** 31 - 256) // 128, np.random.default_rng(9)
+    base, f = W * 128 - 40, inv_freq(128)
+    tab = torch.full((1, W), -1, dtype=torch.int32, device=DEV)
+    tab[0, -1] = 2
+    c = sv.paged_cache(3, 1, 128, 128, torch.float16)
+    (hk, k), (hq, q) = (normal(rng, (1, 16, h, 128), torch.float16) for h in (1, 2))
+    r = sv.spec_kv_append_rope(c, k, k, tab, i32([base]), torch.from_numpy(f).to(DEV), q=q)
+    assert r["status"].item() == 0 and r["out_len"].item() == base + 16
+    for got, x in ((c.k[2, 88:104], hk), (r["q"][0], hq)):
+        want = K.turn(x[0], base + np.arange(16), f)
+        bound = U[torch.float16] * np.abs(want) * 1.001 + np.abs(x).max() * 1.5 * (2 * np.pi * 2.0 ** -17 + 6 * 2.0 ** -24) + 2.0 ** -25
+        assert (np.abs(got.double().cpu().numpy() - want) <= bound).all()
+
+
 def test_offsets_past_32_bits():
     """A cache of more than 2^32 bytes; the rows land on its last page."""
     pages = (1 << 32) // (128 * 2 * 128 * 2) + 3
