@@ -147,7 +147,8 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 
-// kVar: scores are capped or biased, or their factor is negative (the maximum of products is then not that of scores).
+// kVar: scores are capped or biased, or their factor is negative (the maximum of products is then not that of scores) or
+// zero (which a masked product, -inf, must not meet).
 template <typename T, int D, bool kVar>
 __global__ void __launch_bounds__(kPgRowThreads, 1)
     attn_paged_rows_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,

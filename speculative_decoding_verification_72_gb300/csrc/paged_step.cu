@@ -125,7 +125,7 @@ template <typename T, int D>
 cudaError_t launch_attention(const CUtensorMap& k, const CUtensorMap& v, const PagedAttnArgs& a, cudaStream_t st) {
   if (a.R == 16) return launch_cols<T, D, 1>(k, v, a, st);
   if (a.R == 32) return launch_cols<T, D, 2>(k, v, a, st);
-  return a.cap != 0.f || a.slopes || a.coef < 0.f ? launch_rows<T, D, true>(k, v, a, st) : launch_rows<T, D, false>(k, v, a, st);
+  return a.cap != 0.f || a.slopes || !(a.coef > 0.f) ? launch_rows<T, D, true>(k, v, a, st) : launch_rows<T, D, false>(k, v, a, st);
 }
 
 }  // namespace
@@ -211,7 +211,6 @@ sv_status spec_attention(const sv_rows* q, int32_t dtype, const sv_paged_cache* 
   a.coef = static_cast<float>(softcap > 0.f ? 2.0 * scale / softcap : scale);
   a.cap = static_cast<float>(softcap * 1.4426950408889634);
   if (!std::isfinite(a.coef) || !std::isfinite(a.cap)) return SV_ERR_INVALID_ARG;
-  if (std::fabs(a.coef) < 1e-30f) a.coef = 1e-30f;   // 0 times a masked -inf would be NaN
   a.q = static_cast<const uint8_t*>(q->data);
   a.sqb = q->stride_b * 2;
   a.sqn = q->stride_n * 2;

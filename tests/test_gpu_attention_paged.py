@@ -101,6 +101,17 @@ def test_scales(N, G, sm, cap):
     run(np.random.default_rng(9), [3, 200], N, 1, G, 64, 16, BF, sm=sm, cap=cap)
 
 
+@pytest.mark.parametrize("N,G", [(2, 4), (20, 4)])
+@pytest.mark.parametrize("size,sm", [(2.0 ** 54, 2.0 ** -110), (2.0 ** 54, -2.0 ** -110), (2.0 ** 60, 2.0 ** -122), (2.0 ** 60, 0.0)])
+def test_scales_as_small_as_their_products_are_large(N, G, size, sm):
+    """Products of 2^120 at most 2^7 times in all: within fp32."""
+    rng = np.random.default_rng(27)
+    c = host_cache(rng, 20, 16, 1, 64, BF)
+    c["k"] = c["k"] * size
+    hq, gq = normal(rng, (2, N, G, 64), BF)
+    run(rng, [3, 200], N, 1, G, 64, 16, BF, sm=sm, cache=c, pages=20, q=(hq * size, gq * size))
+
+
 def test_negative_slopes_and_rising_maxima():
     """Scores that rise along the line, so that the running maximum does at every tile."""
     for N, G in ((2, 4), (40, 4)):
