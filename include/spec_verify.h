@@ -599,7 +599,8 @@ sv_status spec_kv_append_rope(const sv_paged_cache* cache, int32_t dtype, const 
  * ancestors or, with parents NULL, every earlier row; with window > 0, those
  * of them whose position is less than `window` below its own (pages that no
  * row's window reaches are not read). Scores z = sm_scale q.k; with softcap >
- * 0 they are softcap tanh(z / softcap), to softcap 2^-20; with slopes [Hq] fp32 they become z -
+ * 0 they are softcap tanh(z / softcap), to softcap 2^-20 (softcaps above 128: to
+ * 2^-18 of the score); with slopes [Hq] fp32 they become z -
  * slopes[h] * (distance of positions). out [B, N, Hq, D] in the queries' type,
  * out_lse [B, N, Hq] the natural log of the sum of exponentials (may be NULL).
  * Rows past n_nodes[b], and rows that see nothing, get output 0 and lse -inf;

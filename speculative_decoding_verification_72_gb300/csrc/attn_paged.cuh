@@ -50,6 +50,7 @@ struct PagedAttnArgs {
   uint64_t inv_g;              // ceil(2^32 / G): r / G = r inv_g >> 32 for r G < 2^32
   float coef;                  // of q.k: sm log2(e), or 2 sm log2(e) / cap
   float cap;                   // cap log2(e), or 0
+  float lin;                   // sm log2(e)
   int32_t window;              // 2^31 - 1 for none
   float* part;                 // [2 grid][R (D + 2)]
   int32_t* plan;               // [B RB + 1] places before the blocks, and in all, for one kv head
@@ -204,7 +205,34 @@ struct PagedLook {
   }
 };
 
-// Scores in units of log2, before mask and maximum.
+// From this cap on (in units of log2) its 2^-20, by which capped scores are off,
+// would show in a weight: at 128 a score is off by 2^-13, a weight by half of what
+// f16 rounds off of it.
+constexpr float kPgFarCap = 128.f * kLog2e;
+
+// Scores to cap tanh(z / cap) under a large cap: below a quarter of the cap by
+// tanh u = u - u^3 / 3 + 2 u^5 / 15 - 17 u^7 / 315, to 2^-21 of itself. Rarely taken,
+// so out of line, on a copy, and short.
+template <int kN>
+__device__ __noinline__ void far_caps(float* s, float coef, float cap, float lin) {
+#pragma unroll 1
+  for (int e = 0; e < kN; ++e) {
+    const float t = s[e] * coef, u = t * (0.5f * kLn2), u2 = u * u;
+    s[e] = fabsf(u) < 0.25f ? s[e] * lin * fmaf(u2, fmaf(u2, fmaf(u2, -17.f / 315.f, 2.f / 15.f), -1.f / 3.f), 1.f)
+                            : cap * fmaf(-2.f, 1.f / (1.f + ex2(t)), 1.f);
+  }
+}
+template <int kN>
+__device__ __forceinline__ void cap_far(uint32_t (&x)[kN], const PagedAttnArgs& a) {
+  float y[kN];
+#pragma unroll
+  for (int e = 0; e < kN; ++e) y[e] = __uint_as_float(x[e]);
+  far_caps<kN>(y, a.coef, a.cap, a.lin);
+#pragma unroll
+  for (int e = 0; e < kN; ++e) x[e] = __float_as_uint(y[e]);
+}
+
+// A score in units of log2, before mask and maximum, under no cap or one up to kPgFarCap.
 __device__ __forceinline__ float paged_score(const PagedAttnArgs& a, float s) {
   s *= a.coef;
   if (a.cap == 0.f) return s;

@@ -357,8 +357,14 @@ __global__ void __launch_bounds__(PgColLayout<D, MT>::kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 8; ++j) x[j] = __fmul2_rn(make_float2(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1])), coef2);
         } else {
+          if (a.cap > kPgFarCap) {
+            cap_far(w, a);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] = make_float2(paged_score(a, __uint_as_float(w[2 * j])), paged_score(a, __uint_as_float(w[2 * j + 1])));
+            for (int j = 0; j < 8; ++j) x[j] = make_float2(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = make_float2(paged_score(a, __uint_as_float(w[2 * j])), paged_score(a, __uint_as_float(w[2 * j + 1])));
+          }
           if (a.slopes) {
             const int at = m < 0 || m >= rq.n ? tok : rq.base + s_depth[m];
 #pragma unroll

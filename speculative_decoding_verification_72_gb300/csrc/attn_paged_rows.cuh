@@ -532,7 +532,9 @@ __global__ void __launch_bounds__(kPgRowThreads, 1)
             tmem_ld_wait();
             tmem_use(x);
             if (kVar) {
-              if (a.cap != 0.f) {
+              if (a.cap > kPgFarCap) {
+                cap_far(x, a);
+              } else if (a.cap != 0.f) {
                 cap_scores(x, a.coef, a.cap);
               } else {
 #pragma unroll

@@ -210,7 +210,8 @@ sv_status spec_attention(const sv_rows* q, int32_t dtype, const sv_paged_cache* 
   const double scale = static_cast<double>(sm_scale) * 1.4426950408889634;
   a.coef = static_cast<float>(softcap > 0.f ? 2.0 * scale / softcap : scale);
   a.cap = static_cast<float>(softcap * 1.4426950408889634);
-  if (!std::isfinite(a.coef) || !std::isfinite(a.cap)) return SV_ERR_INVALID_ARG;
+  a.lin = static_cast<float>(scale);
+  if (!std::isfinite(a.coef) || !std::isfinite(a.cap) || !std::isfinite(a.lin)) return SV_ERR_INVALID_ARG;
   a.q = static_cast<const uint8_t*>(q->data);
   a.sqb = q->stride_b * 2;
   a.sqn = q->stride_n * 2;

@@ -476,6 +476,20 @@ def test_scores_far_past_the_cap(N, G, cap):
     run(np.random.default_rng(22), [150, 3], N, 1, G, 64, 16, BF, cap=cap, q_std=300.0)
 
 
+@pytest.mark.parametrize("N,G,tree_rows", [(2, 4, False), (20, 1, True), (12, 4, True), (70, 4, False)])
+@pytest.mark.parametrize("cap,q_std", [(129.0, 2.0), (1e4, 2.0), (1e6, 8.0), (1e30, 2.0), (2e38, 2.0), (200.0, 300.0), (1000.0, 300.0)])
+def test_caps_that_are_large(N, G, tree_rows, cap, q_std):
+    """Below a quarter of the cap a score is off by 2^-21 of itself, above by 2^-20 of the cap, so 2^-18 of itself: a part of
+    the 2^-16 of its |q||k| that its product may be off by."""
+    rng, base, D = np.random.default_rng(28), [150, 3], 64
+    tab = table(rng, [b + N for b in base], 16, 20)
+    c = host_cache(rng, 20, 16, 1, D, F16)
+    hq, gq = normal(rng, (2, N, G, D), F16, q_std)
+    par = tree(rng, 2, N) if tree_rows else None
+    r = sv.spec_attention(gq, to_gpu(c, F16), i32(tab), i32(base), parents=i32(par) if tree_rows else None, softcap=cap)
+    check_attention(r, K.attention(hq, c, tab, base, par, sm=D ** -0.5, cap=cap), F16, N * G)
+
+
 def test_python_refusals():
     E = sv.SpecVerifyError
     c = sv.paged_cache(4, 2, 16, 64)
