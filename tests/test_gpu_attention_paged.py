@@ -490,6 +490,87 @@ def test_caps_that_are_large(N, G, tree_rows, cap, q_std):
     check_attention(r, K.attention(hq, c, tab, base, par, sm=D ** -0.5, cap=cap), F16, N * G)
 
 
+# ------------------------------------------------------- 128-wide heads, deep trees, prompts with all of it
+
+@pytest.mark.parametrize("dtype", [BF, F16])
+@pytest.mark.parametrize("N,G,window", [(6, 4, 0), (36, 1, 50), (70, 4, 0), (70, 4, 50), (5, 5, 7)])
+def test_poison_beside_wide_heads(dtype, N, G, window):
+    rng = np.random.default_rng(29)
+    base, P, D = [0, 37, 100, 250], 64, 128
+    par, lens = tree(rng, 4, N), [b + N for b in base]
+    pages = sum(-(-n // P) for n in lens) + 2
+    tab = table(rng, lens, P, pages)
+    c = host_cache(rng, pages, P, 2, D, dtype)
+    for b, n in enumerate(lens):
+        if n % P:
+            c["k"][tab[b, n // P], n % P:], c["v"][tab[b, n // P], n % P:] = np.nan, np.inf
+    loose = [p for p in range(pages) if p not in tab]
+    c["k"][loose], c["v"][loose] = np.nan, np.nan
+    r, want = run(rng, base, N, 2, G, D, P, dtype, parents=par, window=window, tab=tab, pages=pages, cache=c)
+    assert np.isfinite(want[0]).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F16])
+@pytest.mark.parametrize("N,G", [(6, 4), (36, 1), (70, 4)])
+def test_values_of_wide_heads_that_are_not_finite(dtype, N, G):
+    """In the prefix, in whole tiles and ragged ones, and in nodes that some rows see and others do not."""
+    rng = np.random.default_rng(30)
+    base, P, D = [200, 37], 64, 128
+    par = tree(rng, 2, N)
+    tab = table(rng, [b + N for b in base], P, 12)
+    c = host_cache(rng, 12, P, 1, D, dtype)
+    at = lambda b, p: (tab[b, p // P], p % P, 0)  # noqa: E731
+    for slot, d, x in ((3, 5, np.inf), (130, 64, np.nan), (199, 127, -np.inf), (202, 31, np.inf), (205, 96, np.nan)):
+        c["v"][at(0, slot)][d] = x
+    for slot, d, x in ((39, 0, np.inf), (39, 127, -np.inf), (41, 0, -np.inf), (42, 95, np.nan)):
+        c["v"][at(1, slot)][d] = x
+    r, want = run(rng, base, N, 1, G, D, P, dtype, parents=par, tab=tab, pages=12, cache=c)
+    got, odd = r["out"].double().cpu().numpy(), ~np.isfinite(want[0])
+    # in a tile that every row sees whole an infinity may also be NaN (the second of a weight's two terms has either sign)
+    whole = np.zeros_like(odd)
+    whole[0, ..., 5] = True
+    assert odd.any() and np.array_equal(got[odd & ~whole], want[0][odd & ~whole], equal_nan=True)
+
+
+@pytest.mark.parametrize("N,G,D,depth", [(300, 1, 64, 200), (1024, 1, 128, 1024), (90, 2, 64, 60), (31, 1, 64, 31)])
+def test_deep_trees(N, G, D, depth):
+    rng = np.random.default_rng(31)
+    par = np.array([[-1] + [n - 1 if n < depth else int(rng.integers(n)) for n in range(1, N)]])
+    run(rng, [70], N, 1, G, D, 16, F16, parents=par, window=0 if N < 100 else 150, slopes=slopes_of(G) if N == 300 else None)
+
+
+def in_64_scored(q, cache, tab, base, window=0, cap=0.0, slopes=None):
+    """in_64 for capped and biased scores."""
+    B, N, Hq, D = q.shape
+    H, o = cache.k.shape[2], []
+    for b in range(B):
+        n = base[b] + N
+        k, v = (t[tab[b].long()].flatten(0, 1)[:n].double().repeat_interleave(Hq // H, 1) for t in cache)
+        far = ((base[b] + torch.arange(N, device=DEV))[:, None] - torch.arange(n, device=DEV))[None]
+        see = (far >= 0) & ((far < window) if window else (far >= 0))
+        z = torch.einsum("nhd,shd->hns", q[b].double(), k) * D ** -0.5
+        z = cap * torch.tanh(z / cap) if cap else z
+        z = z if slopes is None else z - torch.tensor(slopes, device=DEV)[:, None, None] * far
+        hid = z.masked_fill(~see, -torch.inf)
+        p = torch.softmax(hid, -1)
+        o.append([torch.einsum("hns,shd->nhd", p, v), torch.logsumexp(hid, -1).T, torch.einsum("hns,shd->nhd", p, v.abs()),
+                  (torch.einsum("nhd,shd->hns", q[b].double().abs(), k.abs()) * see).amax(-1).T * D ** -0.5,
+                  z.masked_fill(~see, 0).abs().amax(-1).T, see.sum(-1).double().expand(Hq, -1).T])
+    return [torch.stack(x).cpu().numpy() for x in zip(*o)]
+
+
+@pytest.mark.parametrize("D,G,dtype", [(128, 4, BF), (64, 8, F16), (128, 1, F16), (64, 2, BF)])
+@pytest.mark.parametrize("cap,window,bias", [(50.0, 0, False), (30.0, 300, False), (0.0, 129, True), (50.0, 512, True), (1000.0, 0, False)])
+def test_prompts_with_caps_windows_and_biases(D, G, dtype, cap, window, bias):
+    N = 1001 if G < 8 else 600
+    q, cache, tab = big(2, N, 2, G, D, 32, 700, dtype, 32)
+    q, base, slopes = (q * 4).to(dtype), [700, 33], slopes_of(2 * G) if bias else None
+    r = sv.spec_attention(q, cache, tab, i32(base), softcap=cap, window=window,
+                          slopes=None if slopes is None else torch.tensor(slopes, dtype=torch.float32, device=DEV))
+    assert int(r["status"].max()) == 0
+    check_attention(r, in_64_scored(q, cache, tab, base, window, cap, slopes), dtype, N * G, cap if cap <= 128 else 0.0)
+
+
 def test_python_refusals():
     E = sv.SpecVerifyError
     c = sv.paged_cache(4, 2, 16, 64)

@@ -103,6 +103,19 @@ def test_parents_far_out_of_range(value):
     assert r["status"].cpu().tolist() == [2, 2, 0]
 
 
+def test_a_chain_given_as_a_tree():
+    """The deepest tree that is taken: bit for bit a chain's rows."""
+    rng = np.random.default_rng(10)
+    N, H, D, P = 1024, 2, 64, 64
+    (_, k), (_, v), (_, q) = (normal(rng, (2, N, h, D), torch.bfloat16) for h in (H, H, 4))
+    base, tab, f = i32([40, 7]), i32(table(rng, [40 + N, 7 + N], P, 40)), torch.from_numpy(inv_freq(D)).to(DEV)
+    one, two = sv.paged_cache(40, H, P, D), sv.paged_cache(40, H, P, D)
+    par = i32(np.tile(np.arange(-1, N - 1), (2, 1)))
+    a = sv.spec_kv_append_rope(one, k, v, tab, base, f, q=q, parents=par)
+    b = sv.spec_kv_append_rope(two, k, v, tab, base, f, q=q)
+    assert all(torch.equal(a[n], b[n]) for n in b) and torch.equal(one.k, two.k) and torch.equal(one.v, two.v)
+
+
 def test_far_positions():
     """Angles of thousands of turns: positions near 2^20 and 2^24 in a table whose other pages are missing."""
     for base in (1 << 20, (1 << 24) - 40):
