@@ -84,8 +84,13 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
 
 // cap tanh(z / cap) = cap (1 - 2 / (1 + e^(2 z / cap))), where coef brings x to the
 // exponent. A reciprocal takes the unit that the exponentials need twice as long
-// as one of those, so three of four are Newton's: from the exponent negated (12 % off at
-// most) three steps lead to 5e-8. (All on that unit: capped trees took 145 us, so 134.)
+// as one of those, so three of four are Newton's, from the bits subtracted from a
+// constant: as a number of steps of 2^-23 the bits of d = 2^e (1 + x) are e + 127 + x,
+// so those of 253 + c - (e + 127 + x) are of 2^(-1 - e) (1 + c - x), and for x > c of
+// 2^(-2 - e) (2 + c - x). Times d that is (1 + x) (1 + c - x) / 2, at most (1 + c / 2)^2 / 2
+// and at least (1 + c) / 2; c = sqrt(24) - 4 makes them as far from 1 on both sides,
+// 5.1 %, of which three steps leave 1.2e-7, fp32's rounding. (All on the unit:
+// capped trees took 145 us, so 134.)
 __device__ __forceinline__ void cap_scores(uint32_t (&x)[32], float coef, float cap) {
   const float2 coef2 = make_float2(coef, coef), one = make_float2(1.f, 1.f), two = make_float2(2.f, 2.f);
   const float2 cap2 = make_float2(cap, cap), down = make_float2(-2.f * cap, -2.f * cap);
@@ -96,7 +101,7 @@ __device__ __forceinline__ void cap_scores(uint32_t (&x)[32], float coef, float 
       asm("min.NaN.f32 %0, %0, 0f42800000;" : "+f"(t.x));   // at 64: 1 / (1 + 2^64) is 0 to the sum
       asm("min.NaN.f32 %0, %0, 0f42800000;" : "+f"(t.y));
       const float2 d = __fadd2_rn(make_float2(ex2(t.x), ex2(t.y)), one), n = make_float2(-d.x, -d.y);
-      r = make_float2(__uint_as_float(0x7ef311c7u - __float_as_uint(d.x)), __uint_as_float(0x7ef311c7u - __float_as_uint(d.y)));
+      r = make_float2(__uint_as_float(0x7ef311c3u - __float_as_uint(d.x)), __uint_as_float(0x7ef311c3u - __float_as_uint(d.y)));
 #pragma unroll
       for (int k = 0; k < 3; ++k) r = __fmul2_rn(r, __ffma2_rn(n, r, two));
     } else {
