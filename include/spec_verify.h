@@ -586,6 +586,7 @@ typedef struct sv_paged_cache {
  * row count; it is neither seq_base nor n_nodes (SV_ERR_INVALID_ARG: the call
  * reads them to its end). A request with a bad page, slot or row count has
  * nothing written (out_len = seq_base), its queries are rotated all the same.
+ * No other output is any of the inputs but out_q.
  * Rows of out_q past the row count, or of a negative seq_base, are 0. Requests
  * must not share the pages written. 2 Hkv + Hq is at most 16384. */
 sv_status spec_kv_append_rope(const sv_paged_cache* cache, int32_t dtype, const sv_rows* k_new, const sv_rows* v_new,
@@ -597,14 +598,15 @@ sv_status spec_kv_append_rope(const sv_paged_cache* cache, int32_t dtype, const 
  * multiple of Hkv; head h reads kv head h / (Hq / Hkv)) whose keys and values
  * are in the cache. Row n sees every slot below seq_base[b], itself, and its
  * ancestors or, with parents NULL, every earlier row; with window > 0, those
- * of them whose position is less than `window` below its own (pages that no
- * row's window reaches are not read). Scores z = sm_scale q.k; with softcap >
+ * of them whose position is less than `window` below its own (slots below all
+ * rows' windows are read, if at all, as the rest of a 128-slot tile, and pages
+ * there may be missing or another request's). Scores z = sm_scale q.k; with softcap >
  * 0 they are softcap tanh(z / softcap), to softcap 2^-20 (softcaps above 128: to
  * 2^-18 of the score); with slopes [Hq] fp32 they become z -
  * slopes[h] * (distance of positions). out [B, N, Hq, D] in the queries' type,
  * out_lse [B, N, Hq] the natural log of the sum of exponentials (may be NULL).
- * Rows past n_nodes[b], and rows that see nothing, get output 0 and lse -inf;
- * slots on a bad page are not seen. Values in slots that a row does not see
+ * Rows past n_nodes[b], and rows that see nothing or nothing but scores of
+ * -inf, get output 0 and lse -inf; slots on a bad page are not seen. Values in slots that a row does not see
  * never reach it, NaN and infinities among them; values that are not finite
  * make the outputs of the rows that see them infinite or NaN. Scores, maxima and sums are
  * fp32; the softmax's terms are rounded to the cache's type where they

@@ -24,10 +24,11 @@
 // way. One warp issues TMA, one MMA, four (for 32 rows, eight) are the softmax.
 //
 // Measured: one token each of 64 requests of up to 8192 tokens (32 heads on 8 of
-// 128) 234 us, 5.7 TB/s; its floor at 6.8 TB/s is 198, the rest is 10 us at each
-// end, the join among them. 32 chains of six rows with capped scores 138 us for
-// 675 MB (a cap is an exponential and a reciprocal more a score). One token of one
-// request 12 us, which are launches and latencies in a row.
+// 128) 235 us, 5.7 TB/s; its floor at 6.8 TB/s is 198. Further requests come at
+// 6.1 TB/s, and 13 us are the ends of a call, the join among them. 32 chains of six
+// rows with capped scores 138 us for 675 MB (a cap is an exponential and a reciprocal
+// more a score). One token of one request 14 us, which are launches and latencies
+// in a row.
 #pragma once
 
 #include "attn_paged.cuh"

@@ -8,7 +8,8 @@ into place (a key is rotated by its depth, which is where it lands). As in
 ``kv_q8``: torch CUDA tensors in, outputs and workspaces allocated by the call
 unless given, work enqueued on the current stream of the cache's device,
 SpecVerifyError on anything the call cannot take; calls can be captured in a
-CUDA graph. The arguments are checked and marshalled by csrc/binding.cpp;
+CUDA graph. They are for serving: tensors that require a gradient are taken, and
+what comes back has none. The arguments are checked and marshalled by csrc/binding.cpp;
 ``_SIGS`` declares the C entry points for direct use.
 """
 
@@ -69,8 +70,8 @@ def spec_kv_append_rope(cache, k_new, v_new, page_table, seq_base, inv_freq, q=N
     parents [B, N] (at most 1024 rows; None: a chain, position = slot). inv_freq [rotary dims / 2] float32: the pair of dims
     (i, i + rotary dims / 2), or (2 i, 2 i + 1) if interleaved, turns by position * inv_freq[i]. n_nodes [B] shortens
     requests. Requests must not share the pages written. Returns dict(out_len [B], status [B]) and, with q given, q
-    (contiguous, 0 in rows past n_nodes; out["q"] may be q where that is contiguous). out["out_len"] is another tensor than
-    seq_base and n_nodes."""
+    (contiguous, 0 in rows past n_nodes; out["q"] may be q where that is contiguous). No other output may be one of the
+    inputs (for seq_base and n_nodes as out["out_len"] that is checked)."""
     return binding().kv_append_rope(cache, k_new, v_new, page_table, seq_base, inv_freq, q, parents, n_nodes, interleaved,
                                     out)
 
