@@ -19,10 +19,10 @@
 // touch, since a request with a bad one is left untouched.
 //
 // Bound by memory: 302 MB of three 4099-row prompts (32 heads on 8 of 128) take
-// 52 us, 5.8 TB/s of reads and writes mixed (the look at all pages grows with the
-// square of a prompt: 131072 rows take 531 us on pages of 128, 959 on pages of 16). Sines by thread for a whole row,
-// not by unit, since 48 heads share them. A step's 192 or 1024 rows take 7 us,
-// the launch and three dependent loads.
+// 52 us, 5.8 TB/s of reads and writes mixed. The look at all pages grows with the
+// square of a prompt: 131072 rows take 531 us on pages of 128, 959 on pages of 16.
+// Sines by thread for a whole row, not by unit, since 48 heads share them. A step's
+// 192 or 1024 rows take 8 and 9 us, the launch and three dependent loads.
 #pragma once
 
 #include "paged_common.cuh"
